@@ -381,12 +381,12 @@ def _run_own(st):
     if op == "dense_fwd":
         q = _quantizer(te, st, st["scaling"]) if st["fmt"] == "nvfp4" else None
         te.te_dense_fp4_fwd(st["x"], st["w"], st["w_scales"], st["out"], st["fmt"], bias=st["b"], q=q,
-                            w_scale_inv=st["w_scale_inv"])
+                            kernel_scale_inv=st["w_scale_inv"])
         return {"out": st["out"]}
     if op == "dense_bwd":
         q = _quantizer(te, st, st["scaling"]) if st["fmt"] == "nvfp4" else None
         te.te_dense_fp4_bwd(st["dy"], st["w"], st["w_scales"], st["xt"], st["xt_scales"], st["dx"], st["dw"],
-                            st["fmt"], dbias=st["dbias"], q=q, w_scale_inv=st["w_scale_inv"],
+                            st["fmt"], dbias=st["dbias"], q=q, kernel_scale_inv=st["w_scale_inv"],
                             x_scale_inv=st["x_scale_inv"])
         return {"dx": st["dx"], "dw": st["dw"], "dbias": st["dbias"]}
     q = _quantizer(te, st, "delayed") if st["dx"] == "e4m3" else None
