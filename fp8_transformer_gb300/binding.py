@@ -23,7 +23,9 @@ TE_IDENTITY, TE_RELU, TE_GELU, TE_SILU, TE_SWIGLU, TE_GEGLU, TE_REGLU = range(7)
 TE_SCALING_DELAYED, TE_SCALING_CURRENT = 0, 1
 (TE_OP_NORM_FWD, TE_OP_ACT_LU, TE_OP_DACT_DBIAS, TE_OP_LAYERNORM_DENSE_FWD,
  TE_OP_LAYERNORM_MLP_FWD, TE_OP_NORM_BWD, TE_OP_LAYERNORM_MLP_BWD,
- TE_OP_LAYERNORM_DENSE_BWD, TE_OP_LAYERNORM_MLP_FWD_HOST, TE_OP_GEMM) = range(10)
+ TE_OP_LAYERNORM_DENSE_BWD, TE_OP_LAYERNORM_MLP_FWD_HOST, TE_OP_GEMM, TE_OP_DENSE_FP4_FWD,
+ TE_OP_DENSE_FP4_BWD) = range(12)
+TE_MXFP8, TE_MXFP4, TE_NVFP4 = range(3)
 
 NORM_TYPES = {"layernorm": TE_LAYERNORM, "rmsnorm": TE_RMSNORM}
 ACT_TYPES = {"identity": TE_IDENTITY, "relu": TE_RELU, "gelu": TE_GELU, "silu": TE_SILU,
@@ -32,6 +34,7 @@ ACT_TYPES = {"identity": TE_IDENTITY, "relu": TE_RELU, "gelu": TE_GELU, "silu": 
 ACT_TUPLES = {("relu",): "relu", ("gelu",): "gelu", ("silu",): "silu",
               ("silu", "linear"): "swiglu", ("gelu", "linear"): "geglu",
               ("relu", "linear"): "reglu"}
+BLOCK_FORMATS = {"mxfp8": TE_MXFP8, "mxfp4": TE_MXFP4, "nvfp4": TE_NVFP4}
 
 _DTYPE = {torch.float32: TE_F32, torch.bfloat16: TE_BF16, torch.uint8: TE_E4M3,
           torch.float8_e4m3fn: TE_E4M3}
@@ -43,7 +46,9 @@ EXPORTED = ["te_status_string", "te_version", "te_get_device_status", "te_worksp
             "te_layernorm_dense_bwd",
             "te_dact_dbias_quantize_noalloc",
             "te_dact_dbias_noalloc_capacity", "te_selftest_wait_timeout",
-            "te_layernorm_mlp_fwd_host", "te_update_scales", "te_stream_probe"]
+            "te_layernorm_mlp_fwd_host", "te_update_scales", "te_stream_probe",
+            "te_block_scale_bytes", "te_block_quantize", "te_block_dequantize", "te_block_gemm",
+            "te_dense_fp4_fwd", "te_dense_fp4_bwd", "te_dact_dbias_ckpt"]
 KERNEL_KINDS = ["norm_fwd", "quantize", "act_lu", "dact_dbias", "gemm", "gemm_act", "norm_bwd",
                 "transpose"]
 
@@ -118,6 +123,19 @@ _SIGS = {
     "te_profile_end": (ctypes.c_int, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int32)]),
     "te_update_scales": (ctypes.c_int, [_QP, ctypes.c_int, _vp]),
     "te_stream_probe": (ctypes.c_int, [_vp, _vp, _sz, ctypes.c_int, _sz, _vp]),
+    "te_block_scale_bytes": (_sz, [ctypes.c_int, _i64, _i64]),
+    "te_block_quantize": (ctypes.c_int, [_vp, ctypes.c_int, _i64, _i64, ctypes.c_int, _QP, _vp, _vp,
+                                         _vp, _vp, _vp]),
+    "te_block_dequantize": (ctypes.c_int, [_vp, _vp, ctypes.c_int, _vp, _i64, _i64, _vp,
+                                           ctypes.c_int, _vp]),
+    "te_block_gemm": (ctypes.c_int, [_vp, _vp, _vp, _vp, ctypes.c_int, _i64, _i64, _i64, _vp, _vp,
+                                     _vp, ctypes.c_int, _vp, ctypes.c_int, _vp]),
+    "te_dense_fp4_fwd": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, ctypes.c_int, _QP, _vp, _vp,
+                                        _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "te_dense_fp4_bwd": (ctypes.c_int, [_vp, ctypes.c_int, _vp, _vp, _vp, _vp, ctypes.c_int, _QP,
+                                        _vp, _vp, _i64, _i64, _i64, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "te_dact_dbias_ckpt": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int, _i64, _i64, ctypes.c_int,
+                                          _QP, _vp, ctypes.c_int, _vp, _vp, _vp, _sz, _vp]),
 }
 
 
@@ -190,15 +208,16 @@ class Quantizer:
 
     @classmethod
     def from_tensors(cls, scale, scale_inv, amax, mode="delayed"):
-        """A quantizer over caller-owned one-element fp32 tensors (e.g. views into a bank)."""
+        """A quantizer over caller-owned one-element fp32 tensors (e.g. views into a bank).
+        amax=None with delayed scaling: the call's amax is not kept."""
         q = cls.__new__(cls)
         q.scale, q.scale_inv, q.amax = scale, scale_inv, amax
         q.mode = TE_SCALING_CURRENT if mode == "current" else TE_SCALING_DELAYED
         return q
 
     def c(self) -> _Quantizer:
-        return _Quantizer(self.scale.data_ptr(), self.scale_inv.data_ptr(), self.amax.data_ptr(),
-                          self.mode)
+        return _Quantizer(self.scale.data_ptr(), self.scale_inv.data_ptr(),
+                          None if self.amax is None else self.amax.data_ptr(), self.mode)
 
 
 class QuantizerSet:
@@ -489,3 +508,201 @@ def te_dact_dbias_quantize_noalloc(dy, x_preact, act, dx, dbias=None, q=None, st
 def dact_dbias_noalloc_capacity() -> int:
     """Floats of fixed device scratch behind te_dact_dbias_quantize_noalloc."""
     return int(lib().te_dact_dbias_noalloc_capacity())
+
+
+# ------------------------------------------------------------------- block-scaled tensors ---
+
+
+def _format(fmt) -> int:
+    return BLOCK_FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
+
+
+def _on_device(*tensors):
+    """The tensors (None left out) lie on the current device, where the kernels are launched."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must live on the current device (cuda:{dev})")
+
+
+def _expect(name, t, shape, *dtypes):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+
+
+_ACT_DTYPES = (torch.float32, torch.bfloat16)
+_BYTES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def block_scale_bytes(fmt, rows, cols) -> int:
+    """Bytes of the scales of a [rows, cols] tensor packed along its columns."""
+    return int(lib().te_block_scale_bytes(_format(fmt), int(rows), int(cols)))
+
+
+def block_empty(fmt, rows, cols, device="cuda"):
+    """(codes, scales): uninitialized buffers for a [rows, cols] tensor packed along its columns."""
+    f = _format(fmt)
+    codes = torch.empty(rows, cols if f == TE_MXFP8 else cols // 2, dtype=torch.uint8, device=device)
+    return codes, torch.empty(block_scale_bytes(f, rows, cols), dtype=torch.uint8, device=device)
+
+
+def _expect_packed(name, f, codes, scales, rows, cols):
+    _expect(name, codes, (rows, cols if f == TE_MXFP8 else cols // 2),
+            *(_BYTES if f == TE_MXFP8 else _BYTES[:1]))
+    if scales is None or scales.dtype not in _BYTES or \
+            scales.numel() < lib().te_block_scale_bytes(f, rows, cols):
+        raise ValueError(f"{name}: its scales must be uint8 of at least block_scale_bytes(fmt, {rows}, {cols})")
+
+
+def _expect_scalar(name, t):
+    if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+        raise ValueError(f"{name}: a one-element float32 tensor")
+
+
+def _expect_quantizer(f, q):
+    if (f == TE_NVFP4) != (q is not None):
+        raise ValueError("q: the quantizer of nvfp4's tensor scale (None for the other formats)")
+    if q is not None:
+        for name in ("scale", "scale_inv", "amax"):
+            _expect_scalar(f"q.{name}", getattr(q, name))
+        _on_device(q.scale, q.scale_inv, q.amax)
+
+
+def _workspace_for(op, M, H, N, device, workspace, stream):
+    if workspace is None:
+        workspace = _ws(workspace_size(op, M, H, N), device)
+        if stream is not None:  # freed on return: kept from reuse until that stream has passed it
+            workspace.record_stream(stream)
+    return workspace
+
+
+def te_block_quantize(x, fmt, codes=None, scales=None, codes_t=None, scales_t=None, q=None, stream=None):
+    """Pack x [M, N] along N into codes / scales, and (or) x^T [N, M rounded up to 32] along M into
+    codes_t / scales_t, in one pass.  fmt: "mxfp8", "mxfp4" or "nvfp4" (with q, its tensor scale)."""
+    f = _format(fmt)
+    M, N = x.shape
+    _expect("x", x, (M, N), *_ACT_DTYPES)
+    if codes is not None:
+        _expect_packed("codes", f, codes, scales, M, N)
+    if codes_t is not None:
+        _expect_packed("codes_t", f, codes_t, scales_t, N, (M + 31) // 32 * 32)
+    _expect_quantizer(f, q)
+    _on_device(x, codes, scales, codes_t, scales_t)
+    st = lib().te_block_quantize(_ptr(x), _dt(x), M, N, f, _qp(q), _ptr(codes), _ptr(scales),
+                                 _ptr(codes_t), _ptr(scales_t), _stream(stream))
+    _check("te_block_quantize", st)
+
+
+def te_block_dequantize(codes, scales, fmt, out, scale_inv=None, stream=None):
+    """out [M, N] (float32 / bfloat16): the values that packed codes stand for."""
+    f = _format(fmt)
+    M, N = out.shape
+    _expect("out", out, (M, N), *_ACT_DTYPES)
+    _expect_packed("codes", f, codes, scales, M, N)
+    _expect_scalar("scale_inv", scale_inv)
+    _on_device(codes, scales, out, scale_inv)
+    st = lib().te_block_dequantize(_ptr(codes), _ptr(scales), f, _ptr(scale_inv), M, N, _ptr(out),
+                                   _dt(out), _stream(stream))
+    _check("te_block_dequantize", st)
+    return out
+
+
+def te_block_gemm(a, a_scales, b, b_scales, out, fmt, a_scale_inv=None, b_scale_inv=None, bias=None,
+                  stream=None):
+    """out [M, N] = alpha * A B^T + bias of packed 4-bit operands a [M, K / 2] and b [N, K / 2]."""
+    f = _format(fmt)
+    M, N = out.shape
+    K = 2 * a.shape[1]
+    _expect("out", out, (M, N), *_ACT_DTYPES)
+    _expect_packed("a", f, a, a_scales, M, K if f != TE_MXFP8 else K // 2)
+    _expect_packed("b", f, b, b_scales, N, K if f != TE_MXFP8 else K // 2)
+    if bias is not None:
+        _expect("bias", bias, (N,), *_ACT_DTYPES)
+    _expect_scalar("a_scale_inv", a_scale_inv)
+    _expect_scalar("b_scale_inv", b_scale_inv)
+    _on_device(a, a_scales, b, b_scales, out, a_scale_inv, b_scale_inv, bias)
+    st = lib().te_block_gemm(_ptr(a), _ptr(a_scales), _ptr(b), _ptr(b_scales), f, M, N, K,
+                             _ptr(a_scale_inv), _ptr(b_scale_inv), _ptr(bias),
+                             _dt(bias) if bias is not None else TE_F32, _ptr(out), _dt(out),
+                             _stream(stream))
+    _check("te_block_gemm", st)
+    return out
+
+
+def te_dense_fp4_fwd(x, kernel, kernel_scales, out, fmt, bias=None, q=None, kernel_scale_inv=None,
+                     saved_xt=None, saved_xt_scales=None, workspace=None, stream=None):
+    """out [M, N] = x [M, K] @ kernel + bias with x packed on the way; kernel: [N, K / 2], the
+    transposed codes (codes_t) of a kernel stored [K, N]."""
+    f = _format(fmt)
+    M, K = x.shape
+    N = out.shape[1]
+    _expect("x", x, (M, K), *_ACT_DTYPES)
+    _expect("out", out, (M, N), x.dtype)
+    _expect_packed("kernel", f, kernel, kernel_scales, N, K)
+    if bias is not None:
+        _expect("bias", bias, (N,), x.dtype)
+    if saved_xt is not None:
+        _expect_packed("saved_xt", f, saved_xt, saved_xt_scales, K, (M + 31) // 32 * 32)
+    _expect_quantizer(f, q)
+    _expect_scalar("kernel_scale_inv", kernel_scale_inv)
+    _on_device(x, kernel, kernel_scales, out, bias, kernel_scale_inv, saved_xt, saved_xt_scales, workspace)
+    workspace = _workspace_for(TE_OP_DENSE_FP4_FWD, M, K, N, x.device, workspace, stream)
+    st = lib().te_dense_fp4_fwd(_ptr(x), _dt(x), _ptr(kernel), _ptr(kernel_scales), f, _qp(q),
+                                _ptr(kernel_scale_inv), _ptr(bias), M, K, N, _ptr(out),
+                                _ptr(saved_xt), _ptr(saved_xt_scales), _ptr(workspace),
+                                workspace.numel(), _stream(stream))
+    _check("te_dense_fp4_fwd", st)
+    return out
+
+
+def te_dense_fp4_bwd(dy, kernel, kernel_scales, saved_xt, saved_xt_scales, dx, dkernel, fmt, dbias=None,
+                     q=None, kernel_scale_inv=None, x_scale_inv=None, workspace=None, stream=None):
+    """dx = dy @ kernel^T, dkernel [K, N] = x^T @ dy and dbias from 4-bit operands; kernel: [K, N / 2],
+    the codes of a kernel stored [K, N]; saved_xt from te_dense_fp4_fwd."""
+    f = _format(fmt)
+    M, N = dy.shape
+    K = dx.shape[1]
+    _expect("dy", dy, (M, N), *_ACT_DTYPES)
+    _expect("dx", dx, (M, K), dy.dtype)
+    _expect("dkernel", dkernel, (K, N), dy.dtype)
+    _expect_packed("kernel", f, kernel, kernel_scales, K, N)
+    _expect_packed("saved_xt", f, saved_xt, saved_xt_scales, K, (M + 31) // 32 * 32)
+    if dbias is not None:
+        _expect("dbias", dbias, (N,), torch.float32)
+    _expect_quantizer(f, q)
+    _expect_scalar("kernel_scale_inv", kernel_scale_inv)
+    _expect_scalar("x_scale_inv", x_scale_inv)
+    _on_device(dy, kernel, kernel_scales, saved_xt, saved_xt_scales, dx, dkernel, dbias, kernel_scale_inv,
+               x_scale_inv, workspace)
+    workspace = _workspace_for(TE_OP_DENSE_FP4_BWD, M, K, N, dy.device, workspace, stream)
+    st = lib().te_dense_fp4_bwd(_ptr(dy), _dt(dy), _ptr(kernel), _ptr(kernel_scales), _ptr(saved_xt),
+                                _ptr(saved_xt_scales), f, _qp(q), _ptr(kernel_scale_inv),
+                                _ptr(x_scale_inv), M, K, N, _ptr(dx), _ptr(dkernel), _ptr(dbias),
+                                _ptr(workspace), workspace.numel(), _stream(stream))
+    _check("te_dense_fp4_bwd", st)
+    return dx
+
+
+def te_dact_dbias_ckpt(dy, codes, scales, act, dx, dbias=None, act_out=None, q=None, workspace=None,
+                       stream=None):
+    """te_dact_dbias_quantize from an 8-bit checkpoint (codes, scales: mxfp8) of the activation's
+    input; act_out, when given, receives the recomputed activation output."""
+    a = _act_id(act)
+    M, N_in = dx.shape
+    n_out = N_in // 2 if a in (TE_SWIGLU, TE_GEGLU, TE_REGLU) else N_in
+    _expect("dy", dy, (M, n_out), *_ACT_DTYPES)
+    _expect("dx", dx, (M, N_in), *_ACT_DTYPES, *_BYTES)
+    _expect_packed("codes", TE_MXFP8, codes, scales, M, N_in)
+    if act_out is not None:
+        _expect("act_out", act_out, (M, n_out), dy.dtype)
+    if dbias is not None:
+        _expect("dbias", dbias, (N_in,), torch.float32)
+        workspace = _workspace_for(TE_OP_DACT_DBIAS, M, 0, N_in, dy.device, workspace, stream)
+    _on_device(dy, codes, scales, dx, dbias, act_out, workspace)
+    st = lib().te_dact_dbias_ckpt(_ptr(dy), _ptr(codes), _ptr(scales), _dt(dy), M, N_in, a, _qp(q),
+                                  _ptr(dx), _dt(dx), _ptr(act_out), _ptr(dbias), _ptr(workspace),
+                                  0 if workspace is None else workspace.numel(), _stream(stream))
+    _check("te_dact_dbias_ckpt", st)
+    return dx

@@ -7,110 +7,12 @@
 #include <initializer_list>
 #include <utility>
 
+#include "api_util.h"
 #include "kernels.h"
 #include "te_gb300.h"
 
 namespace te {
 namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool opt_aligned16(const void* p) { return p == nullptr || aligned16(p); }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-size_t esize(int dt) { return dt == TE_F32 ? 4 : dt == TE_BF16 ? 2 : 1; }
-bool is_act_dtype(int dt) { return dt == TE_F32 || dt == TE_BF16; }
-bool valid_act(int a) { return a >= TE_IDENTITY && a <= TE_REGLU; }
-bool enabled(const te_quantizer* q) { return q != nullptr && q->scale != nullptr; }
-
-bool quantizer_ok(const te_quantizer* q) {
-  if (!enabled(q)) return true;
-  if (!aligned4(q->scale) || !aligned4(q->scale_inv) || !aligned4(q->amax)) return false;
-  if (q->mode != TE_SCALING_DELAYED && q->mode != TE_SCALING_CURRENT) return false;
-  // Current scaling keeps this call's amax between its two passes.
-  if (q->mode == TE_SCALING_CURRENT && q->amax == nullptr) return false;
-  return true;
-}
-
-constexpr size_t kAlign = 256;
-size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-// Sequential carving of the caller's workspace into 256-byte aligned regions.
-struct Carver {
-  uint8_t* base;
-  size_t used = 0;
-  explicit Carver(void* b) : base(static_cast<uint8_t*>(b)) {}
-  void* take(size_t bytes) {
-    void* p = base ? base + used : nullptr;
-    used += round_up(bytes);
-    return p;
-  }
-};
-
-// The scratch for splitting GEMM tails along K (launch_gemm) is carved last: a workspace that
-// stops short of it still serves the call, with no tile split.  The GEMMs of one call run one
-// after another on its stream, so they share the region, sized for the largest.
-struct SplitScratch {
-  size_t offset = 0;  // where the region starts in the workspace
-  size_t required = 0;  // workspace bytes the call needs (everything before the region)
-};
-
-SplitScratch carve_split(Carver& c, std::initializer_list<size_t> needs) {
-  SplitScratch r;
-  r.required = c.used;
-  r.offset = c.used;
-  size_t most = 0;
-  for (size_t n : needs) most = n > most ? n : most;
-  if (most) c.take(most);
-  return r;
-}
-
-void give_split(GemmArgs& g, const SplitScratch& sc, void* ws, size_t ws_bytes) {
-  if (ws && ws_bytes > sc.offset) {
-    g.split_ws = static_cast<uint8_t*>(ws) + sc.offset;
-    g.split_ws_bytes = ws_bytes - sc.offset;
-  }
-}
-
-cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
-
-te_status zero_scalar(float* p, cudaStream_t s) {
-  if (!p) return TE_OK;
-  return cudaMemsetAsync(p, 0, sizeof(float), s) == cudaSuccess ? TE_OK : TE_ERR_CUDA;
-}
-
-// Runs a bandwidth-bound producer once (no quantizer, or delayed scaling) or twice (current
-// scaling: an amax pass that stores nothing, then the cast pass with scale = 448 / amax).
-template <class Launch>
-te_status run_cast(const te_quantizer* q, int out_dtype, int fake_quant, cudaStream_t s,
-                   Launch&& launch) {
-  CastSpec c;
-  c.out_dtype = out_dtype;
-  c.fake_quant = fake_quant;
-  if (q) {
-    te_status st = zero_scalar(q->amax, s);
-    if (st != TE_OK) return st;
-  }
-  if (!enabled(q)) {
-    c.amax_out = q ? q->amax : nullptr;
-    return launch(c);
-  }
-  if (q->mode == TE_SCALING_DELAYED) {
-    c.scale = q->scale;
-    c.amax_out = q->amax;
-    c.scale_inv_out = q->scale_inv;
-    return launch(c);
-  }
-  CastSpec pass1 = c;
-  pass1.store = 0;
-  pass1.amax_out = q->amax;
-  te_status st = launch(pass1);
-  if (st != TE_OK) return st;
-  CastSpec pass2 = c;
-  pass2.amax_in = q->amax;
-  pass2.scale_out = q->scale;
-  pass2.scale_inv_out = q->scale_inv;
-  return launch(pass2);
-}
 
 // Workspace layout of the composed forward passes (shared by te_workspace_size and the calls).
 struct FwdLayout {
@@ -303,6 +205,8 @@ size_t te_workspace_size(te_op op, int64_t M, int64_t H, int64_t F_or_N, te_dtyp
       return host_fwd_workspace(M, H, F_or_N, dtype, act);
     case TE_OP_GEMM:  // dims = {M, K, N}
       return gemm_split_workspace(M, F_or_N, H, dtype, EPI_BIAS);
+    case TE_OP_DENSE_FP4_FWD: return dense_fp4_fwd_workspace(M, H);
+    case TE_OP_DENSE_FP4_BWD: return dense_fp4_bwd_workspace(M, F_or_N);
     case TE_OP_LAYERNORM_DENSE_BWD:
       return dense_bwd_layout(nullptr, M, H, F_or_N, dtype, quantized != 0, kernel_dtype).bytes;
     default: return 0;

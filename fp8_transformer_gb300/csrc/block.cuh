@@ -1,0 +1,101 @@
+// Block-scaled formats: the scale of a block, the 4-bit conversions and the scale layout.
+//
+// A block is 32 (MXFP4, MXFP8) or 16 (NVFP4) neighbours along the packed axis.
+//   MX:  scale = 2^(c - 127), the smallest power of two with amax / scale <= the largest code
+//        value (6 or 448), so no value saturates; x / scale is exact in fp32, and the one
+//        rounding is the code's.
+//   NV:  sb = E4M3(fp32(fp32(amax * s) / 6)) with s the tensor's fp32 scale; the codes are those of
+//        fp32(x * fp32(s / sb)).  A block whose sb rounds to zero holds zeros.
+// A block that holds an infinity or a NaN gets a NaN scale (and zero codes), so that whatever
+// reads it is NaN too instead of a plausible number.
+#pragma once
+
+#include "common.cuh"
+#include "kernels.h"
+
+namespace te {
+
+// Bits of |v| order like the values, infinities above every finite number and NaN above those.
+constexpr uint32_t kInfBits = 0x7f800000u;
+
+// The byte of one scale within its row of tiles: tiles of 128 rows x 4 blocks, 512 bytes, in
+// which the rows r, r + 32, r + 64, r + 96 are neighbours.  This is the order in which
+// tcgen05.cp.32x128b hands a tile to tensor memory.
+__device__ __forceinline__ uint32_t scale_offset(uint32_t row_in_tile, uint32_t block) {
+  return (block >> 2) * 512 + (row_in_tile & 31) * 16 + (row_in_tile >> 5) * 4 + (block & 3);
+}
+
+// Two fp32 -> two E2M1 codes in a byte (lo in the low half): nearest even, saturating to +-6.
+// Eight fp32 -> eight codes, element 0 lowest.
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float (&v)[8]) {
+  uint32_t r;
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+      "mov.b32 %0, {a, b, c, d};\n\t}"
+      : "=r"(r)
+      : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+  return r;
+}
+
+// Eight E2M1 codes -> exact fp32 pairs (through the exact conversion to f16).
+__device__ __forceinline__ void unpack_e2m1x8(uint32_t w, f32x2 (&v)[4]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = __half22float2(*reinterpret_cast<__half2*>(&h[i]));
+}
+
+// 2^(c - 127) of an E8M0 byte; NaN for 255.
+__device__ __forceinline__ float e8m0_value(uint32_t c) {
+  const uint32_t bits = c == 0 ? 0x00400000u : c == 255 ? 0x7fc00000u : c << 23;
+  return __uint_as_float(bits);
+}
+
+// A block's scale byte and the factor its values are multiplied by before the code's rounding.
+struct BlockScale {
+  uint32_t byte;
+  float mul;
+  bool bad;  // the block holds an infinity or a NaN
+};
+
+template <int FMT>
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float s) {
+  BlockScale r;
+  r.bad = amax_bits >= kInfBits;
+  if constexpr (FMT == TE_NVFP4) {
+    const float t = __fdiv_rn(__fmul_rn(__uint_as_float(amax_bits), s), 6.0f);
+    const uint32_t sb = pack_e4m3x2(t, 0.0f) & 0xffu;
+    const float sf = unpack_e4m3x2(uint16_t(sb)).x;
+    r.byte = r.bad ? 0x7fu : sb;
+    r.mul = sb ? __fdiv_rn(s, sf) : 0.0f;
+  } else {
+    // 6 = 1.5 * 2^2 and 448 = 1.75 * 2^8: one more when the mantissa is above the top's
+    constexpr int kTopExp = FMT == TE_MXFP4 ? 2 : 8;
+    constexpr uint32_t kTopMant = FMT == TE_MXFP4 ? 0x400000u : 0x600000u;
+    int c = int(amax_bits >> 23) - kTopExp + ((amax_bits & 0x7fffffu) > kTopMant ? 1 : 0);
+    c = c < 0 ? 0 : c;
+    r.byte = r.bad ? 255u : uint32_t(c);
+    r.mul = __uint_as_float(uint32_t(254 - c) << 23);  // 2^(127 - c); c <= 253
+  }
+  return r;
+}
+
+// fp32 tensor scale of NVFP4 from the tensor's amax: the block scales of the largest block reach
+// E4M3's largest value (1 when amax is 0 or not finite, FLT_MAX if the quotient overflows).
+__device__ __forceinline__ float nv_scale_from_amax(float amax) {
+  if (!(amax > 0.0f) || !isfinite(amax)) return 1.0f;
+  const float s = __fdiv_rn(6.0f * kE4M3Max, amax);
+  return isfinite(s) ? s : 3.4028234663852886e38f;
+}
+
+}  // namespace te

@@ -1,0 +1,397 @@
+// Packing into and reading back of the block-scaled formats (block.cuh has the arithmetic).
+//
+// Packing is one pass over x.  A CTA takes a tile of 128 rows, so that the scales it makes are
+// whole 512-byte scale tiles that it writes in one run:
+//   along the rows: each lane holds 8 neighbours of a row; the 2 or 4 lanes of a block share its
+//     amax by shuffles, so values go from registers to codes with no second read.
+//   along the columns (the transposed output): the tile is kept in shared memory; a thread then
+//     walks 32 rows of its column(s), lanes on neighbouring columns (no bank conflicts), and the
+//     codes go out through a second small stage, 64 bytes of a transposed row at a time.
+// Both outputs cost one read of x.  What bounds it is memory: a bf16 element is 2 bytes in and
+// 0.53 (4 bits) or 1.03 (8 bits) out for each orientation.
+#include "block.cuh"
+#include "cast.cuh"
+
+namespace te {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTileRows = 128;
+
+// 8 neighbours of T as fp32.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* p) { u = __ldg(static_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void to_smem(void* p) const { *static_cast<uint4*>(p) = u; }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+    v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
+  }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    constexpr uint32_t k = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(u.x & k, u.y & k), __vmaxu2(u.z & k, u.w & k));
+    return max(m & 0xffffu, m >> 16) << 16;
+  }
+};
+template <>
+struct Eight<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const void* p) {
+    a = __ldg(static_cast<const uint4*>(p));
+    b = __ldg(static_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void to_smem(void* p) const {
+    static_cast<uint4*>(p)[0] = a;
+    static_cast<uint4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z);
+    v[3] = __uint_as_float(a.w); v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
+    v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+  }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    constexpr uint32_t k = 0x7fffffffu;
+    return max(max(max(a.x & k, a.y & k), max(a.z & k, a.w & k)),
+               max(max(b.x & k, b.y & k), max(b.z & k, b.w & k)));
+  }
+};
+
+// Codes of 8 neighbours: 4 bytes (x) of E2M1 or 8 bytes of E4M3.
+template <int FMT>
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], const BlockScale& b) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 p = mul2(f2(x[2 * i], x[2 * i + 1]), f2s(b.mul));
+    v[2 * i] = f2lo(p);
+    v[2 * i + 1] = f2hi(p);
+  }
+  uint2 r = make_uint2(0u, 0u);
+  if (b.bad) return r;
+  if constexpr (FMT == TE_MXFP8) {
+    r.x = pack_e4m3x4(v[0], v[1], v[2], v[3]);
+    r.y = pack_e4m3x4(v[4], v[5], v[6], v[7]);
+  } else {
+    r.x = pack_e2m1x8(v);
+  }
+  return r;
+}
+
+// One element of a tile held in shared memory, columns c (and c + 1 for bf16) of row r.
+template <typename T>
+struct Column;  // kCols columns a thread walks at once
+template <>
+struct Column<__nv_bfloat16> {
+  static constexpr int kCols = 2;
+  __device__ __forceinline__ static void get(const uint8_t* p, float (&v)[2]) {
+    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
+    v[0] = bf16_lo(w);
+    v[1] = bf16_hi(w);
+  }
+};
+template <>
+struct Column<float> {
+  static constexpr int kCols = 1;
+  __device__ __forceinline__ static void get(const uint8_t* p, float (&v)[1]) {
+    v[0] = *reinterpret_cast<const float*>(p);
+  }
+};
+
+constexpr int kColTile = 128;           // columns of a tile that is also packed along its columns
+constexpr int kStagePitch = 64 + 16;    // bytes of a transposed row's codes in shared memory
+
+template <typename T>
+__host__ __device__ constexpr int tile_pitch() { return kColTile * int(sizeof(T)) + 16; }
+template <typename T>
+__host__ __device__ constexpr size_t col_smem() { return size_t(kTileRows) * tile_pitch<T>() + kColTile * kStagePitch; }
+
+// TC: columns of a tile (256 when only the rows are packed, for whole 128-byte runs of codes).
+template <typename T, int FMT, int TC, bool COL>
+__global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs a) {
+  constexpr int kBlk = block_len(FMT);
+  constexpr int kLanes = TC / 8;                 // lanes on one row
+  constexpr int kRowsPass = kThreads / kLanes;   // rows a CTA takes at a time
+  constexpr int kPasses = kTileRows / kRowsPass;
+  constexpr int kBatch = 4;                      // passes whose loads are in flight together
+  constexpr int kScaleBytes = kTileRows * (TC / kBlk);
+  __shared__ __align__(16) uint8_t rs[kScaleBytes];
+  __shared__ __align__(16) uint8_t cs[COL ? kScaleBytes : 16];
+  __shared__ float sums[COL ? 4 : 1][COL ? kColTile : 1];
+  extern __shared__ __align__(16) uint8_t dyn[];
+  // the kernel after this one may launch its setup now (it waits for this grid's completion)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  float s = 1.0f;
+  if constexpr (FMT == TE_NVFP4) {
+    s = a.amax_in ? nv_scale_from_amax(*a.amax_in) : *a.scale;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+      if (a.scale_out) *a.scale_out = s;
+      if (a.scale_inv_out) *a.scale_inv_out = __fdiv_rn(1.0f, s);
+    }
+  }
+  const int64_t tiles_c = (a.N + TC - 1) / TC;
+  const int64_t rt = blockIdx.x / tiles_c, ct = blockIdx.x % tiles_c;
+  const int64_t r0 = rt * kTileRows, c0 = ct * TC;
+  const int cl = int(threadIdx.x) % kLanes * 8;  // this lane's column within the tile
+  const bool col_ok = c0 + cl < a.N;             // N is a multiple of 32: whole blocks
+  const int rl = int(threadIdx.x) / kLanes;
+  const T* x = static_cast<const T*>(a.x) + r0 * a.N + c0 + cl;
+  uint8_t* tile = dyn;
+  const int64_t pitch = a.N / codes_per_byte(FMT);
+  uint8_t* codes = static_cast<uint8_t*>(a.codes) + r0 * pitch + (c0 + cl) / codes_per_byte(FMT);
+  uint32_t amax = 0;
+#pragma unroll 1
+  for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
+    Eight<T> e[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int r = (p0 + j) * kRowsPass + rl;
+      if (col_ok && r0 + r < a.M) e[j].load(x + int64_t(r) * a.N);
+      else e[j].zero();
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int r = (p0 + j) * kRowsPass + rl;
+      if constexpr (COL) e[j].to_smem(tile + r * tile_pitch<T>() + cl * int(sizeof(T)));
+      uint32_t m = e[j].amax_bits();
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      if constexpr (kBlk == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      amax = max(amax, m <= kInfBits ? m : 0u);  // blocks with a NaN left out
+      if (!COL || a.codes) {
+        const bool in = col_ok && r0 + r < a.M;
+        BlockScale b = block_scale<FMT>(m, s);
+        if (in) {
+          float v[8];
+          e[j].get(v);
+          const uint2 c = codes8<FMT>(v, b);
+          if constexpr (FMT == TE_MXFP8) *reinterpret_cast<uint2*>(codes + r * pitch) = c;
+          else *reinterpret_cast<uint32_t*>(codes + r * pitch) = c.x;
+        }
+        if (cl % kBlk == 0) rs[scale_offset(r, cl / kBlk)] = in ? uint8_t(b.byte) : uint8_t(0);
+      }
+    }
+  }
+  __syncthreads();
+  // the tile's scale tiles, those of them that the row of tiles has
+  if (!COL || a.codes) {
+    const int64_t groups = scale_groups(FMT, a.N);
+    const int64_t g0 = c0 / kBlk / 4;
+    const int n = int(min(int64_t(kScaleBytes), (groups - g0) * 512));
+    uint8_t* dst = static_cast<uint8_t*>(a.scales) + (rt * groups + g0) * 512;
+    for (int i = int(threadIdx.x) * 16; i < n; i += kThreads * 16)
+      *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(rs + i);
+  }
+  if constexpr (COL) {
+    constexpr int kC = Column<T>::kCols;
+    uint8_t* stage = dyn + kTileRows * tile_pitch<T>();
+    // (column(s), 32 rows) for every thread; fp32 takes two turns
+    for (int u = int(threadIdx.x); u < kColTile / kC * 4; u += kThreads) {
+      const int c = u % (kColTile / kC) * kC, rb = u / (kColTile / kC);
+      const uint8_t* src = tile + rb * 32 * tile_pitch<T>() + c * int(sizeof(T));
+      float v[kC][32];
+#pragma unroll
+      for (int r = 0; r < 32; ++r) {
+        float w[kC];
+        Column<T>::get(src + r * tile_pitch<T>(), w);
+#pragma unroll
+        for (int k = 0; k < kC; ++k) v[k][r] = w[k];
+      }
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        if (a.partials) {
+          float t = 0.0f;
+#pragma unroll
+          for (int r = 0; r < 32; ++r) t += v[k][r];
+          sums[rb][c + k] = t;
+        }
+        const bool in = c0 + c + k < a.N && r0 + rb * 32 < a.M;
+#pragma unroll
+        for (int h = 0; h < 32 / kBlk; ++h) {
+          uint32_t m = 0;
+#pragma unroll
+          for (int r = 0; r < kBlk; ++r) m = max(m, __float_as_uint(v[k][h * kBlk + r]) & 0x7fffffffu);
+          const BlockScale b = block_scale<FMT>(m, s);
+          cs[scale_offset(c + k, rb * (32 / kBlk) + h)] = in ? uint8_t(b.byte) : uint8_t(0);
+          uint32_t q[kBlk / 8];
+#pragma unroll
+          for (int g = 0; g < kBlk / 8; ++g) {
+            float w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = v[k][h * kBlk + g * 8 + i];
+            q[g] = codes8<FMT>(w, b).x;
+          }
+          uint8_t* d = stage + (c + k) * kStagePitch + rb * 16 + h * 8;
+          if constexpr (kBlk == 32) *reinterpret_cast<uint4*>(d) = make_uint4(q[0], q[1], q[2], q[3]);
+          else *reinterpret_cast<uint2*>(d) = make_uint2(q[0], q[1]);
+        }
+      }
+    }
+    __syncthreads();
+    const int64_t mp = (a.M + 31) / 32 * 32;
+    const int64_t groups = scale_groups(FMT, mp);
+    const int64_t g0 = r0 / kBlk / 4;
+    const int n = int(min(int64_t(kScaleBytes), (groups - g0) * 512));
+    uint8_t* dst = static_cast<uint8_t*>(a.scales_t) + (ct * groups + g0) * 512;
+    for (int i = int(threadIdx.x) * 16; i < n; i += kThreads * 16)
+      *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(cs + i);
+    // 16 bytes of codes (32 rows) for each of 4 lanes on a transposed row
+    for (int u = int(threadIdx.x); u < kColTile * 4; u += kThreads) {
+      const int c = u / 4, rb = u % 4;
+      if (c0 + c < a.N && r0 + rb * 32 < mp)
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.codes_t) + ((c0 + c) * mp + r0) / 2 + rb * 16) =
+            *reinterpret_cast<const uint4*>(stage + c * kStagePitch + rb * 16);
+    }
+    if (a.partials)
+      for (int c = int(threadIdx.x); c < kColTile; c += kThreads)
+        if (c0 + c < a.N)
+          a.partials[rt * a.N + c0 + c] = ((sums[0][c] + sums[1][c]) + sums[2][c]) + sums[3][c];
+  }
+  if (a.amax_out) block_amax_commit(__uint_as_float(amax), a.amax_out);
+}
+
+template <typename T, int FMT>
+te_status launch_quant_t(const BlockQuantArgs& a, cudaStream_t s) {
+  const bool col = a.codes_t != nullptr;
+  const int64_t tc = col ? kColTile : 256;
+  const int64_t tiles = ceil_div(a.M, kTileRows) * ceil_div(a.N, tc);
+  if (tiles > 0x7fffffff) return TE_ERR_UNSUPPORTED;
+  if (!col) {
+    block_quantize_kernel<T, FMT, 256, false><<<unsigned(tiles), kThreads, 0, s>>>(a);
+  } else if constexpr (FMT == TE_MXFP8) {
+    return TE_ERR_UNSUPPORTED;  // checkpoints are read along their rows only
+  } else {
+    static PerDevice<bool> attr_set;
+    bool ok = false;
+    if (!attr_set.get(&ok, [](bool* v) {
+          *v = cudaFuncSetAttribute(block_quantize_kernel<T, FMT, kColTile, true>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    int(col_smem<T>())) == cudaSuccess;
+          return *v;
+        }))
+      return TE_ERR_CUDA;
+    block_quantize_kernel<T, FMT, kColTile, true><<<unsigned(tiles), kThreads, col_smem<T>(), s>>>(a);
+  }
+  return cudaGetLastError() == cudaSuccess ? TE_OK : TE_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ reading back ----------
+
+// A tile of 128 rows x 256 columns a CTA: its scales first, in one run, then 8 codes a lane.
+template <int FMT, typename OutT>
+__global__ void __launch_bounds__(kThreads) block_dequantize_kernel(BlockDequantArgs a) {
+  constexpr int TC = 256;
+  constexpr int kBlk = block_len(FMT);
+  constexpr int kScaleBytes = kTileRows * (TC / kBlk);
+  constexpr int kPasses = kTileRows / (kThreads / 32);
+  constexpr int kBatch = 4;
+  __shared__ __align__(16) uint8_t rs[kScaleBytes];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t tiles_c = (a.N + TC - 1) / TC;
+  const int64_t rt = blockIdx.x / tiles_c, ct = blockIdx.x % tiles_c;
+  const int64_t r0 = rt * kTileRows, c0 = ct * TC;
+  const int64_t groups = scale_groups(FMT, a.N);
+  const int64_t g0 = c0 / kBlk / 4;
+  const int n = int(min(int64_t(kScaleBytes), (groups - g0) * 512));
+  const uint8_t* src = static_cast<const uint8_t*>(a.scales) + (rt * groups + g0) * 512;
+  for (int i = int(threadIdx.x) * 16; i < n; i += kThreads * 16)
+    *reinterpret_cast<uint4*>(rs + i) = __ldg(reinterpret_cast<const uint4*>(src + i));
+  const float inv = a.scale_inv ? *a.scale_inv : 1.0f;
+  const int cl = int(threadIdx.x) % 32 * 8;
+  const int rl = int(threadIdx.x) / 32;
+  const int64_t pitch = a.N / codes_per_byte(FMT);
+  const uint8_t* codes = static_cast<const uint8_t*>(a.codes) + r0 * pitch + (c0 + cl) / codes_per_byte(FMT);
+  OutT* out = static_cast<OutT*>(a.out) + r0 * a.N + c0 + cl;
+  __syncthreads();
+  if (c0 + cl >= a.N) return;
+  CastState none;
+#pragma unroll 1
+  for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
+    uint2 w[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int r = (p0 + j) * (kThreads / 32) + rl;
+      w[j] = make_uint2(0u, 0u);
+      if (r0 + r < a.M) {
+        if constexpr (FMT == TE_MXFP8) w[j] = __ldg(reinterpret_cast<const uint2*>(codes + r * pitch));
+        else w[j].x = __ldg(reinterpret_cast<const uint32_t*>(codes + r * pitch));
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int r = (p0 + j) * (kThreads / 32) + rl;
+      if (r0 + r >= a.M) break;
+      const uint32_t sb = rs[scale_offset(r, cl / kBlk)];
+      const f32x2 f = f2s(FMT == TE_NVFP4 ? unpack_e4m3x2(uint16_t(sb)).x : e8m0_value(sb));
+      f32x2 v[4];
+      if constexpr (FMT == TE_MXFP8) {
+        v[0] = unpack_e4m3x2(uint16_t(w[j].x));
+        v[1] = unpack_e4m3x2(uint16_t(w[j].x >> 16));
+        v[2] = unpack_e4m3x2(uint16_t(w[j].y));
+        v[3] = unpack_e4m3x2(uint16_t(w[j].y >> 16));
+      } else {
+        unpack_e2m1x8(w[j].x, v);
+      }
+      float y[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f32x2 t = mul2(v[i], f);  // exact
+        if constexpr (FMT == TE_NVFP4) t = mul2(t, f2s(inv));
+        y[2 * i] = f2lo(t);
+        y[2 * i + 1] = f2hi(t);
+      }
+      store_out<sizeof(OutT) == 4 ? OUT_F32 : OUT_BF16, 8>(out, int64_t(r) * a.N, y, none);
+    }
+  }
+}
+
+template <int FMT>
+te_status launch_dequant_t(const BlockDequantArgs& a, unsigned tiles, cudaStream_t s) {
+  if (a.out_dtype == TE_F32) block_dequantize_kernel<FMT, float><<<tiles, kThreads, 0, s>>>(a);
+  else block_dequantize_kernel<FMT, __nv_bfloat16><<<tiles, kThreads, 0, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? TE_OK : TE_ERR_CUDA;
+}
+
+}  // namespace
+
+te_status launch_block_quantize(const BlockQuantArgs& a, cudaStream_t s) {
+  if (a.M == 0) return TE_OK;
+  ProfileScope prof(TE_KERNEL_QUANTIZE, s);
+  const bool f32 = a.x_dtype == TE_F32;
+  switch (a.fmt) {
+    case TE_MXFP4:
+      return f32 ? launch_quant_t<float, TE_MXFP4>(a, s) : launch_quant_t<__nv_bfloat16, TE_MXFP4>(a, s);
+    case TE_NVFP4:
+      return f32 ? launch_quant_t<float, TE_NVFP4>(a, s) : launch_quant_t<__nv_bfloat16, TE_NVFP4>(a, s);
+    default:
+      return f32 ? launch_quant_t<float, TE_MXFP8>(a, s) : launch_quant_t<__nv_bfloat16, TE_MXFP8>(a, s);
+  }
+}
+
+te_status launch_amax(const void* x, int x_dtype, int64_t n, float* amax_out, cudaStream_t s) {
+  if (cudaMemsetAsync(amax_out, 0, sizeof(float), s) != cudaSuccess) return TE_ERR_CUDA;
+  QuantizeArgs a;
+  a.x = x;
+  a.x_dtype = x_dtype;
+  a.n = n;
+  a.cast.store = 0;
+  a.cast.amax_out = amax_out;
+  return launch_quantize(a, s);
+}
+
+te_status launch_block_dequantize(const BlockDequantArgs& a, cudaStream_t s) {
+  const int64_t tiles = ceil_div(a.M, kTileRows) * ceil_div(a.N, 256);
+  if (tiles == 0) return TE_OK;
+  if (tiles > 0x7fffffff) return TE_ERR_UNSUPPORTED;
+  ProfileScope prof(TE_KERNEL_QUANTIZE, s);
+  switch (a.fmt) {
+    case TE_MXFP4: return launch_dequant_t<TE_MXFP4>(a, unsigned(tiles), s);
+    case TE_NVFP4: return launch_dequant_t<TE_NVFP4>(a, unsigned(tiles), s);
+    default: return launch_dequant_t<TE_MXFP8>(a, unsigned(tiles), s);
+  }
+}
+
+}  // namespace te

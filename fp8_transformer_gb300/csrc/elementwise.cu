@@ -373,9 +373,12 @@ te_status launch_dact_dbias(const DactArgs& a, cudaStream_t s) {
                  : a.dtype == TE_F32 ? launch_dact_t<float>(a, grid, s)
                                      : TE_ERR_UNSUPPORTED;
   if (st != TE_OK || !a.dbias) return st;
-  return launch_dependent(colsum_partials_kernel, dim3(unsigned(ceil_div(a.N_in, 128))),
-                          dim3(kColsumWarps * 32), s, static_cast<const float*>(a.partials),
-                          chunks, int64_t(a.N_in), a.dbias);
+  return launch_colsum(a.partials, chunks, a.N_in, a.dbias, s);
+}
+
+te_status launch_colsum(const float* partials, int chunks, int64_t n, float* out, cudaStream_t s) {
+  return launch_dependent(colsum_partials_kernel, dim3(unsigned(ceil_div(n, 128))),
+                          dim3(kColsumWarps * 32), s, partials, chunks, n, out);
 }
 
 te_status launch_transpose_f32(const float* src, int64_t R, int64_t C, float* dst, cudaStream_t s) {

@@ -70,6 +70,9 @@ te_status launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s);
 // Workspace of te_layernorm_mlp_fwd_host: device staging of x and out plus one forward's.
 size_t host_fwd_workspace(int64_t M, int64_t H, int64_t F, int dtype, int act);
 size_t norm_bwd_workspace(int64_t M, int64_t H);
+// Workspaces of the 4-bit dense layer, for either format.
+size_t dense_fp4_fwd_workspace(int64_t M, int64_t K);
+size_t dense_fp4_bwd_workspace(int64_t M, int64_t N);
 
 struct ActArgs {
   const void* x = nullptr;
@@ -95,6 +98,22 @@ struct DactArgs {
 te_status launch_dact_dbias(const DactArgs& a, cudaStream_t s);
 size_t dact_dbias_workspace(int64_t M, int64_t N_in);
 
+// The same from an 8-bit checkpoint of the activation's input, which also gives back act(h).
+struct DactCkptArgs {
+  const void* dy = nullptr;      // [M, n_out]
+  const void* codes = nullptr;   // [M, N_in] E4M3, MXFP8
+  const void* scales = nullptr;
+  int dtype = TE_BF16;
+  int64_t M = 0, N_in = 0;
+  int act = TE_GELU;
+  void* dx = nullptr;            // [M, N_in]
+  void* act_out = nullptr;       // [M, n_out] act(h) in dtype, or null
+  float* dbias = nullptr;
+  float* partials = nullptr;     // as for DactArgs
+  CastSpec cast;
+};
+te_status launch_dact_ckpt(const DactCkptArgs& a, cudaStream_t s);
+
 struct QuantizeArgs {
   const void* x = nullptr;
   int x_dtype = TE_BF16;
@@ -103,6 +122,53 @@ struct QuantizeArgs {
   CastSpec cast;
 };
 te_status launch_quantize(const QuantizeArgs& a, cudaStream_t s);
+
+// Block-scaled formats (te_block_format): elements in a block, and codes per byte.
+__host__ __device__ constexpr int block_len(int fmt) { return fmt == TE_NVFP4 ? 16 : 32; }
+__host__ __device__ constexpr int codes_per_byte(int fmt) { return fmt == TE_MXFP8 ? 1 : 2; }
+// Scale tiles along one row of tiles, and the bytes of a [rows, cols] tensor's scales.
+__host__ __device__ constexpr int64_t scale_groups(int fmt, int64_t cols) {
+  return (cols / block_len(fmt) + 3) / 4;
+}
+inline size_t block_scale_bytes(int fmt, int64_t rows, int64_t cols) {
+  return size_t((rows + 127) / 128) * size_t(scale_groups(fmt, cols)) * 512;
+}
+// Length of a packed transposed row: the rows of x in whole blocks of 32.
+inline int64_t pad32(int64_t n) { return (n + 31) / 32 * 32; }
+
+struct BlockQuantArgs {
+  const void* x = nullptr;  // [M, N]
+  int x_dtype = TE_BF16;
+  int64_t M = 0, N = 0;     // N a multiple of 32
+  int fmt = TE_MXFP4;
+  void* codes = nullptr;    // [M, N] packed along N, or null
+  void* scales = nullptr;
+  void* codes_t = nullptr;  // [N, pad32(M)] packed along M, or null
+  void* scales_t = nullptr;
+  const float* scale = nullptr;    // NVFP4: the tensor scale given (delayed scaling)
+  const float* amax_in = nullptr;  // NVFP4: derive the tensor scale from this amax
+  float* amax_out = nullptr;       // atomic max of |x| (zeroed by the caller)
+  float* scale_out = nullptr;      // written with the tensor scale used
+  float* scale_inv_out = nullptr;  // written with 1 / scale
+  float* partials = nullptr;       // column sums of each 128-row tile [ceil(M / 128), N], or null
+};
+te_status launch_block_quantize(const BlockQuantArgs& a, cudaStream_t s);
+// amax_out = max |x| of n elements (a multiple of 8), zeroed first.
+te_status launch_amax(const void* x, int x_dtype, int64_t n, float* amax_out, cudaStream_t s);
+// out[j] = sum over the chunks of partials[c][j], in a fixed order (n a multiple of 4); launched
+// as a programmatic dependent of the kernel that wrote the partials.
+te_status launch_colsum(const float* partials, int chunks, int64_t n, float* out, cudaStream_t s);
+
+struct BlockDequantArgs {
+  const void* codes = nullptr;
+  const void* scales = nullptr;
+  int fmt = TE_MXFP4;
+  const float* scale_inv = nullptr;  // NVFP4: the tensor's factor, or null (= 1)
+  int64_t M = 0, N = 0;
+  void* out = nullptr;
+  int out_dtype = TE_BF16;
+};
+te_status launch_block_dequantize(const BlockDequantArgs& a, cudaStream_t s);
 
 // dst[C, R] = transpose of src[R, C] (fp32): the tf32 tensor-core path takes K-major operands.
 te_status launch_transpose_f32(const float* src, int64_t R, int64_t C, float* dst, cudaStream_t s);
@@ -146,6 +212,26 @@ struct GemmArgs {
 te_status launch_gemm(const GemmArgs& g, cudaStream_t s);
 // Bytes of split_ws that launch_gemm would use for this GEMM on the current device (0: none).
 size_t gemm_split_workspace(int64_t M, int64_t N, int64_t K, int ab_dtype, int epilogue);
+
+// Product of two packed 4-bit operands: D[M, N] = alpha * A B^T + bias, A [M, K], B [N, K].
+struct BlockGemmArgs {
+  const void* A = nullptr;         // codes, K / 2 bytes a row
+  const void* a_scales = nullptr;
+  const void* B = nullptr;
+  const void* b_scales = nullptr;
+  int fmt = TE_MXFP4;
+  int64_t M = 0, N = 0, K = 0;     // K a multiple of 32, N of 16
+  const float* a_scale_inv = nullptr;
+  const float* b_scale_inv = nullptr;
+  const void* bias = nullptr;      // [N]
+  int bias_dtype = TE_F32;
+  void* D = nullptr;               // [M, N]
+  int d_dtype = TE_BF16;
+  // B and its scales were complete before the kernel that precedes this one on the stream began,
+  // so that their loads may start before that kernel has finished.
+  int b_ready = 0;
+};
+te_status launch_block_gemm(const BlockGemmArgs& a, cudaStream_t s);
 
 // Device status word (TE_OK or the first failure a kernel recorded).
 int* device_status_ptr();
@@ -211,6 +297,11 @@ class PerDevice {
 // box_inner x box_outer elements, 128-byte swizzle or none, out-of-bounds reads zero.
 bool make_tmap_2d(CUtensorMap* tm, const void* ptr, int dtype, uint64_t inner, uint64_t outer,
                   uint32_t box_inner, uint32_t box_outer, bool swizzle128);
+
+// 2-D TMA tensor map over block scales: rows of tiles by 512-byte tiles, boxes of box_rows rows
+// of tiles x box_tiles tiles, out-of-bounds reads zero.
+bool make_tmap_scales(CUtensorMap* tm, const void* ptr, uint64_t tiles, uint64_t tile_rows,
+                      uint32_t box_tiles, uint32_t box_rows);
 
 // Brackets one kernel launch with profiling events when te_profile_begin is active.
 class ProfileScope {

@@ -48,4 +48,18 @@ bool make_tmap_2d(CUtensorMap* tm, const void* ptr, int dtype, uint64_t inner, u
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Elements of 8 bytes, so that a box's inner extent (at most 256 elements) holds four tiles.
+bool make_tmap_scales(CUtensorMap* tm, const void* ptr, uint64_t tiles, uint64_t tile_rows,
+                      uint32_t box_tiles, uint32_t box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {tiles * 64, tile_rows};
+  cuuint64_t strides[1] = {tiles * 512};
+  cuuint32_t box[2] = {box_tiles * 64, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT64, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace te

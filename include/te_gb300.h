@@ -47,6 +47,9 @@ typedef enum {
 
 typedef enum { TE_F32 = 0, TE_BF16 = 1, TE_E4M3 = 2 } te_dtype;
 
+/* Block-scaled formats (see "Block-scaled tensors" below). */
+typedef enum { TE_MXFP8 = 0, TE_MXFP4 = 1, TE_NVFP4 = 2 } te_block_format;
+
 /* norm_type: "layernorm" or "rmsnorm" (LayerNorm MLP page, I/O Contract). */
 typedef enum { TE_LAYERNORM = 0, TE_RMSNORM = 1 } te_norm_type;
 
@@ -106,7 +109,9 @@ typedef enum {
   TE_OP_LAYERNORM_MLP_BWD = 6,
   TE_OP_LAYERNORM_DENSE_BWD = 7,
   TE_OP_LAYERNORM_MLP_FWD_HOST = 8,
-  TE_OP_GEMM = 9 /* dims = {M, K, N}, dtype = the operands' dtype */
+  TE_OP_GEMM = 9, /* dims = {M, K, N}, dtype = the operands' dtype */
+  TE_OP_DENSE_FP4_FWD = 10, /* dims = {M, K, N}; enough for either 4-bit format */
+  TE_OP_DENSE_FP4_BWD = 11  /* dims = {M, K, N}; enough for either 4-bit format */
 } te_op;
 
 /* Human-readable name of a status code (static storage, never NULL). */
@@ -374,6 +379,110 @@ te_status te_layernorm_dense_bwd(const void* dy, const void* x, const void* gamm
                                  te_dtype dtype, void* dx, float* dgamma, float* dbeta,
                                  void* dkernel, float* dbias, void* workspace, size_t ws_bytes,
                                  void* stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Block-scaled tensors (no counterpart on the pages; an addition of this library).  A tensor
+ * [rows, cols] is packed along its columns: every block of neighbours in a row shares a scale.
+ *   TE_MXFP4  E2M1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two to a byte with the
+ *             earlier column in the low half; blocks of 32 with an E8M0 scale, 2^(byte - 127).
+ *   TE_NVFP4  E2M1 codes; blocks of 16 with an E4M3 scale, and one fp32 scale s for the tensor.
+ *   TE_MXFP8  E4M3 codes, one to a byte; blocks of 32 with an E8M0 scale.
+ *   codes  [rows, cols / 2] bytes (MXFP8: [rows, cols]); cols a multiple of 32.
+ *   scales te_block_scale_bytes(format, rows, cols) bytes, in tiles of 128 rows x 4 blocks: the
+ *          tile of rows 128 i .. and blocks 4 j .. is the 512 bytes at (i * ceil(blocks / 4) + j)
+ *          * 512, and row r, block b of a tile is its byte (r % 32) * 16 + (r / 32) * 4 + b.
+ *          Bytes of rows and blocks that the tensor does not have are zero.
+ * Scales and codes of a block with largest magnitude a:
+ *   MX     scale = the smallest power of two with a / scale <= 6 (MXFP8: 448), at least 2^-127;
+ *          code = round-to-nearest-even of x / scale, which then never saturates.
+ *   NVFP4  scale = E4M3(fp32(fp32(a * s) / 6)); code = E2M1(fp32(x * fp32(s / scale))), saturating;
+ *          all zeros where the scale rounds to zero.  The value of a code is
+ *          fp32(code * scale * (1 / s)).
+ *   A block with an infinity or a NaN gets a NaN scale and zero codes: it reads as NaN.
+ */
+
+/* Bytes of the scales of a [rows, cols] tensor (0 for a bad format or size). */
+size_t te_block_scale_bytes(te_block_format format, int64_t rows, int64_t cols);
+
+/* te_block_quantize -- packs x [M, N] (TE_F32 / TE_BF16) in one pass.
+ *   codes, scales      x packed along N, or both NULL.
+ *   codes_t, scales_t  x^T [N, Mp] packed along the rows of x, Mp = M rounded up to a multiple of
+ *                      32 with zeros in the added columns, or both NULL (the operand of products
+ *                      that contract over the rows).  4-bit formats only.
+ *   q   NULL for the MX formats.  NVFP4: the tensor scale s: DELAYED reads *scale, CURRENT computes
+ *       s = 2688 / amax (1 if amax is 0 or not finite, FLT_MAX if the quotient overflows) and
+ *       writes *scale; both write scale_inv = 1 / s and amax (DELAYED: where not NULL; the largest
+ *       magnitude, blocks with a NaN left out).
+ * N must be a multiple of 32. */
+te_status te_block_quantize(const void* x, te_dtype x_dtype, int64_t M, int64_t N,
+                            te_block_format format, const te_quantizer* q, void* codes,
+                            void* scales, void* codes_t, void* scales_t, void* stream);
+
+/* te_block_dequantize -- the values of a packed [M, N] tensor in out_dtype (TE_F32 / TE_BF16).
+ *   scale_inv  NVFP4: device fp32 scalar 1 / s, or NULL (= 1); NULL for the MX formats. */
+te_status te_block_dequantize(const void* codes, const void* scales, te_block_format format,
+                              const float* scale_inv, int64_t M, int64_t N, void* out,
+                              te_dtype out_dtype, void* stream);
+
+/* te_block_gemm -- D = alpha * A B^T + bias on the tensor cores, the scales applied there.
+ *   A [M, K] and B [N, K] packed along K in one 4-bit format; products and sums in fp32.
+ *   a_scale_inv, b_scale_inv  device fp32 scalars or NULL (= 1); alpha is their product.
+ *   bias [N] in bias_dtype (TE_F32 / TE_BF16) or NULL; D [M, N] in d_dtype (TE_F32 / TE_BF16).
+ * The result does not vary between calls.  N a multiple of 16, K of 32; M, N, K below 2^31. */
+te_status te_block_gemm(const void* A, const void* a_scales, const void* B, const void* b_scales,
+                        te_block_format format, int64_t M, int64_t N, int64_t K,
+                        const float* a_scale_inv, const float* b_scale_inv, const void* bias,
+                        te_dtype bias_dtype, void* D, te_dtype d_dtype, void* stream);
+
+/* te_dense_fp4_fwd -- out = x @ kernel + bias with x packed on the way (LayerNorm Dense page,
+ * Description: both operands are quantized before the GEMM; here to 4 bits).
+ *   x [M, K], out [M, N], bias [N] or NULL in dtype (TE_F32 / TE_BF16).
+ *   kernel, kernel_scales  the kernel's transpose [N, K] packed along K (te_block_quantize's
+ *       codes_t of a kernel stored [K, N]); kernel_scale_inv its NVFP4 factor or NULL.
+ *   q   NVFP4: x's quantizer, scale_inv required.  MX: NULL.
+ *   saved_xt, saved_xt_scales  NULL, or where x^T packed along the rows of x goes (codes_t,
+ *       scales_t of te_block_quantize), for te_dense_fp4_bwd.
+ *   workspace  te_workspace_size(TE_OP_DENSE_FP4_FWD, M, K, N, ...) bytes, 16-byte aligned.
+ * K a multiple of 32, N of 16. */
+te_status te_dense_fp4_fwd(const void* x, te_dtype dtype, const void* kernel,
+                           const void* kernel_scales, te_block_format format,
+                           const te_quantizer* q, const float* kernel_scale_inv, const void* bias,
+                           int64_t M, int64_t K, int64_t N, void* out, void* saved_xt,
+                           void* saved_xt_scales, void* workspace, size_t ws_bytes, void* stream);
+
+/* te_dense_fp4_bwd -- dx = dy @ kernel^T, dkernel = x^T @ dy and dbias = the column sums of dy, with
+ * both products on 4-bit operands; dy is packed along both axes in one pass, which also sums its
+ * columns (fp32, unquantized, in a fixed order).
+ *   dy [M, N], dx [M, K], dkernel [K, N] in dtype (TE_F32 / TE_BF16); dbias [N] fp32 or NULL.
+ *   kernel, kernel_scales  the kernel [K, N] packed along N (te_block_quantize's codes).
+ *   saved_xt, saved_xt_scales  from te_dense_fp4_fwd, x_scale_inv its NVFP4 factor or NULL.
+ *   q   NVFP4: dy's quantizer, scale_inv required.  MX: NULL.
+ *   workspace  te_workspace_size(TE_OP_DENSE_FP4_BWD, M, K, N, ...) bytes, 16-byte aligned.
+ * K and N multiples of 32.  M = 0 zeroes dkernel and dbias. */
+te_status te_dense_fp4_bwd(const void* dy, te_dtype dtype, const void* kernel,
+                           const void* kernel_scales, const void* saved_xt,
+                           const void* saved_xt_scales, te_block_format format,
+                           const te_quantizer* q, const float* kernel_scale_inv,
+                           const float* x_scale_inv, int64_t M, int64_t K, int64_t N, void* dx,
+                           void* dkernel, float* dbias, void* workspace, size_t ws_bytes,
+                           void* stream);
+
+/* te_dact_dbias_ckpt -- te_dact_dbias_quantize from an 8-bit checkpoint of the activation's input,
+ * which also gives back the activation's output (the operand of the second kernel's gradient).
+ *   dy          [M, N_out] in dtype (TE_F32 / TE_BF16).
+ *   codes, scales  the activation input [M, N_in] in TE_MXFP8 (te_block_quantize, or a forward
+ *               that saved it).
+ *   act         any activation but TE_IDENTITY.
+ *   dx          [M, N_in] in dx_dtype: dy * act'(h) in fp32, then rounded or (TE_E4M3) quantized
+ *               with q, as in te_dact_dbias_quantize.
+ *   act_out     [M, N_out] act(h) in dtype, or NULL.
+ *   dbias       [N_in] fp32 column sums of the fp32 dx, in a fixed order, or NULL.
+ *   workspace   te_workspace_size(TE_OP_DACT_DBIAS, M, 0, N_in, ...) bytes, needed for dbias.
+ * N_out must be a multiple of 32. */
+te_status te_dact_dbias_ckpt(const void* dy, const void* codes, const void* scales, te_dtype dtype,
+                             int64_t M, int64_t N_in, te_act_type act, const te_quantizer* q,
+                             void* dx, te_dtype dx_dtype, void* act_out, float* dbias,
+                             void* workspace, size_t ws_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------------------
  * te_norm_bwd -- gradients of te_norm_fwd (LayerNorm MLP page, Description: the backward pass

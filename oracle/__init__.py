@@ -8,6 +8,7 @@ to it.
 
 Modules:
   numerics  fp32 / bf16 / E4M3 rounding and per-tensor scaling, from the formats' definitions
+  block_scaled  4- and 8-bit formats with one scale for a block of neighbours
   block     normalization, activations, GEMM + bias, the composed forward and backward passes
 
 Every function is pinned by tests under ``tests/test_oracle_*.py`` against something other
@@ -15,4 +16,4 @@ than itself: library routines (torch's layer_norm / rms_norm / autograd / float8
 conversions, scipy's erf), closed forms, identities, brute force and finite differences.
 """
 
-from . import block, numerics  # noqa: F401
+from . import block, block_scaled, numerics  # noqa: F401

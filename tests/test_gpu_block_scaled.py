@@ -1,0 +1,460 @@
+"""Block-scaled operators on the GPU against the float64 oracle (oracle/block_scaled.py).
+
+Packing is held to equality, byte for byte: codes, scales and the zeros that pad a scale tile.
+Products: the operands' values are exact, so what differs is the fp32 accumulation.  Each of the
+K / 64 tensor-core steps adds a dot product of 64 exact products to an fp32 accumulator; with the
+products aligned to the largest of them, a step may lose one unit in the last place per product and
+one for the sum: |err| <= (K / 64 + 64) * 2^-23 * sum |a b|, plus half a step of the output's type.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_transformer_gb300 as te
+from oracle import block as ob
+from oracle import block_scaled as bs
+from oracle import numerics as nx
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+GUARD = 0xA5
+
+
+def f64(t):
+    return t.detach().cpu().double().numpy()
+
+
+def u8(t):
+    return t.detach().cpu().numpy()
+
+
+def guarded(n):
+    """n bytes with a guard of 256 behind them, all set to GUARD."""
+    b = torch.full((n + 256,), GUARD, dtype=torch.uint8, device=DEV)
+    return b, b[:n]
+
+
+def draw(rows, cols, dtype, seed=0, std=1.0, spread=True):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(rows, cols, generator=g) * std
+    if spread:  # rows of very different sizes
+        x *= 2.0 ** torch.randint(-12, 12, (rows, 1), generator=g)
+    return x.to(dtype).to(DEV)
+
+
+def special(dtype):
+    """Zeros, infinities, NaN, subnormals, the type's largest, ties of E2M1 and of the MX scale."""
+    x = torch.zeros(40, 96)
+    x[1, 3] = float("inf")
+    x[2, 40] = float("-inf")
+    x[3, 95] = float("nan")
+    x[4] = 2.0 ** -133
+    x[5] = torch.finfo(dtype).max
+    x[6] = torch.tensor([0.25, -0.75, 1.25, -1.75, 2.5, -3.5, 5.0, 6.0] * 12)
+    x[7] = 6.0 * (1 + 2.0 ** -7)
+    x[8, ::32] = 448.0
+    x[9, ::32] = 450.0
+    x[10] = -0.0
+    x[11] = torch.finfo(dtype).tiny
+    x[12, 5] = 2.0 ** 100
+    x[12, 6] = 2.0 ** -100
+    x[32:36] = torch.linspace(-7, 7, 96)
+    return x.to(dtype).to(DEV)
+
+
+def quantize_checked(x, fmt, both, q=None, s=None):
+    """te_block_quantize of x against the oracle; returns the buffers."""
+    M, N = x.shape
+    mp = (M + 31) // 32 * 32
+    bufs = {}
+    sizes = {"codes": (M, N if fmt == "mxfp8" else N // 2)}
+    if both:
+        sizes["codes_t"] = (N, mp // 2)
+    for k, shape in sizes.items():
+        g, v = guarded(shape[0] * shape[1])
+        bufs[k] = (g, v.view(*shape))
+    for k, (r, c) in {"scales": (M, N), "scales_t": (N, mp)}.items():
+        if k == "scales" or both:
+            g, v = guarded(te.block_scale_bytes(fmt, r, c))
+            bufs[k] = (g, v)
+    te.te_block_quantize(x, fmt, q=q, **{k: v[1] for k, v in bufs.items()})
+    torch.cuda.synchronize()
+    for k, (g, v) in bufs.items():
+        assert (g[v.numel():] == GUARD).all(), f"{k}: written past its end"
+    xs = f64(x)
+    for sfx, src in (("", xs), ("_t", bs.pad_t(xs))):
+        if "codes" + sfx not in bufs:
+            continue
+        c, sc = bs.pack(src, fmt, s)
+        got_s, want_s = u8(bufs["scales" + sfx][1]), bs.tile_scales(sc)
+        assert np.array_equal(got_s, want_s), (fmt, sfx, np.flatnonzero(got_s != want_s)[:8])
+        got_c, want_c = u8(bufs["codes" + sfx][1]), bs.to_bytes(c, fmt)
+        assert np.array_equal(got_c, want_c), (fmt, sfx, np.argwhere(got_c != want_c)[:8])
+    return {k: v[1] for k, v in bufs.items()}
+
+
+SHAPES = [(1, 32), (33, 64), (128, 128), (77, 352), (257, 160), (300, 544)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt,both", [("mxfp4", False), ("mxfp4", True), ("mxfp8", False)])
+def test_mx_packing_is_exact(fmt, both, dtype):
+    for i, (m, n) in enumerate(SHAPES):
+        quantize_checked(draw(m, n, dtype, seed=i), fmt, both)
+    quantize_checked(special(dtype), fmt, both)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("both", [False, True])
+def test_nvfp4_packing_is_exact_with_either_scaling(both, dtype):
+    for i, (m, n) in enumerate(SHAPES):
+        x = draw(m, n, dtype, seed=i, spread=False)
+        amax = np.float32(np.abs(f64(x)).max())
+        q = te.Quantizer(mode="current")
+        s = bs.nv_scale(amax)
+        quantize_checked(x, "nvfp4", both, q, s)
+        assert q.amax.item() == amax and np.float32(q.scale.item()) == s
+        assert np.float32(q.scale_inv.item()) == np.float32(1) / s
+        q = te.Quantizer(scale=700.0)  # too large for some blocks: their scales saturate
+        quantize_checked(x, "nvfp4", both, q, 700.0)
+        assert q.amax.item() == amax and np.float32(q.scale_inv.item()) == np.float32(1) / np.float32(700)
+        quantize_checked(x, "nvfp4", both, te.Quantizer.from_tensors(q.scale, q.scale_inv, None), 700.0)
+    x = special(dtype)
+    quantize_checked(x, "nvfp4", both, te.Quantizer(scale=2.0), 2.0)
+    q = te.Quantizer(mode="current")
+    quantize_checked(x, "nvfp4", both, q, 1.0)  # an infinite amax: scale 1
+    assert q.scale.item() == 1.0
+    z = torch.zeros(33, 64, dtype=dtype, device=DEV)
+    quantize_checked(z, "nvfp4", both, te.Quantizer(mode="current"), 1.0)
+
+
+def test_transposed_alone():
+    x = draw(100, 96, torch.bfloat16)
+    ct, st = te.block_empty("mxfp4", 96, 128)
+    te.te_block_quantize(x, "mxfp4", codes_t=ct, scales_t=st)
+    c, s = bs.pack(bs.pad_t(f64(x)), "mxfp4")
+    assert np.array_equal(u8(ct), bs.to_bytes(c, "mxfp4")) and np.array_equal(u8(st), bs.tile_scales(s))
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "mxfp8"])
+def test_reading_back_is_exact(fmt):
+    for i, (m, n) in enumerate(SHAPES + [(40, 96)]):
+        x = special(torch.float32) if (m, n) == (40, 96) else draw(m, n, torch.bfloat16, seed=i, spread=fmt != "nvfp4")
+        codes, scales = te.block_empty(fmt, m, n)
+        q = te.Quantizer(scale=3.0) if fmt == "nvfp4" else None
+        te.te_block_quantize(x, fmt, codes, scales, q=q)
+        inv = q.scale_inv if q else None
+        want = bs.unpack(*bs.pack(f64(x), fmt, 3.0), fmt, np.float32(1) / np.float32(3) if q else None)
+        for dt in (torch.float32, torch.bfloat16):
+            out = torch.full((m + 1, n), 7.0, dtype=dt, device=DEV)
+            te.te_block_dequantize(codes, scales, fmt, out[:m], scale_inv=inv)
+            w = nx.bf16_round(want) if dt == torch.bfloat16 else nx.to_f32(want)
+            assert np.array_equal(f64(out[:m]), w, equal_nan=True), (fmt, m, n, dt)
+            assert (out[m] == 7.0).all()
+
+
+# ------------------------------------------------------------------------------- products ---
+
+
+def packed(rows, cols, fmt, seed, scale=64.0):
+    """(codes, scales, scale_inv, values) of a random packed tensor."""
+    x = draw(rows, cols, torch.bfloat16, seed, spread=fmt != "nvfp4")
+    codes, scales = te.block_empty(fmt, rows, cols)
+    q = te.Quantizer(scale=scale) if fmt == "nvfp4" else None
+    te.te_block_quantize(x, fmt, codes, scales, q=q)
+    inv = q.scale_inv if q else None
+    c, s = bs.pack(f64(x), fmt, scale)
+    return codes, scales, inv, bs.unpack(c, s, fmt), 1.0 if inv is None else inv.item()
+
+
+def product_bound(a, b, alpha, want, K, dtype):
+    return (K / 64 + 64) * 2.0 ** -23 * alpha * (np.abs(a) @ np.abs(b).T) + 2.0 ** -22 * np.abs(want) + \
+        HALF_STEP[dtype] * np.abs(want) + 1e-37
+
+
+def gemm_checked(M, N, K, fmt, bias=None, dtype=torch.bfloat16):
+    ca, sa, ia, va, fa = packed(M, K, fmt, 1)
+    cb, sb, ib, vb, fb = packed(N, K, fmt, 2, scale=300.0)
+    bz = None if bias is None else draw(1, N, bias, seed=3, spread=False)[0].contiguous()
+    out = torch.full((M + 1, N), 7.0, dtype=dtype, device=DEV)
+    te.te_block_gemm(ca, sa, cb, sb, out[:M], fmt, a_scale_inv=ia, b_scale_inv=ib, bias=bz)
+    torch.cuda.synchronize()
+    assert te.get_device_status() == 0
+    alpha = fa * fb
+    want = alpha * (va @ vb.T) + (0 if bz is None else f64(bz))
+    err = np.abs(f64(out[:M]) - want)
+    tol = product_bound(va, vb, alpha, want, K, dtype) + (0 if bz is None else 2.0 ** -22 * np.abs(f64(bz)))
+    assert (out[M] == 7.0).all(), "a row behind the last was written"
+    assert (err <= tol).all(), (M, N, K, fmt, float((err / tol).max()), np.argwhere(err > tol)[:4])
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M", [1, 16, 17, 33, 64, 100, 128])
+def test_product_of_few_rows(M, fmt):
+    gemm_checked(M, 128, 256, fmt)
+    gemm_checked(M, 16, 32, fmt, bias=torch.bfloat16)
+    gemm_checked(M, 176, 544, fmt, bias=torch.float32, dtype=torch.float32)
+    gemm_checked(M, 400, 4096, fmt, bias=torch.bfloat16)
+    gemm_checked(M, 1024, 96, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M", [129, 256, 300, 513])
+def test_product_of_many_rows(M, fmt):
+    gemm_checked(M, 256, 256, fmt)
+    gemm_checked(M, 16, 32, fmt, bias=torch.bfloat16)
+    gemm_checked(M, 272, 544, fmt, bias=torch.float32, dtype=torch.float32)
+    gemm_checked(M, 1040, 4128, fmt)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_product_with_more_tiles_than_sm_pairs(fmt):
+    gemm_checked(2100, 3344, 160, fmt, bias=torch.bfloat16)
+
+
+def test_product_is_the_same_on_every_call():
+    for M in (5, 300):
+        ca, sa, ia, _, _ = packed(M, 4096, "nvfp4", 1)
+        cb, sb, ib, _, _ = packed(512, 4096, "nvfp4", 2)
+        outs = [te.te_block_gemm(ca, sa, cb, sb, torch.empty(M, 512, device=DEV), "nvfp4", ia, ib) for _ in range(4)]
+        assert all(torch.equal(outs[0], o) for o in outs[1:])
+
+
+def test_a_bad_block_makes_its_row_nan_and_no_other():
+    for M in (7, 200):
+        x = draw(M, 512, torch.bfloat16, spread=False)
+        x[3, 100] = float("nan")
+        for fmt in ("mxfp4", "nvfp4"):
+            ca, sa = te.block_empty(fmt, M, 512)
+            q = te.Quantizer(scale=64.0) if fmt == "nvfp4" else None
+            te.te_block_quantize(x, fmt, ca, sa, q=q)
+            cb, sb, _, _, _ = packed(128, 512, fmt, 2)
+            out = te.te_block_gemm(ca, sa, cb, sb, torch.empty(M, 128, device=DEV), fmt)
+            bad = torch.isnan(out)
+            assert bad[3].all() and int(bad.sum()) == 128
+
+
+# ---------------------------------------------------------------------------- dense layer ---
+
+
+def values(x, fmt, s):
+    c, sc = bs.pack(x, fmt, s)
+    return bs.unpack(c, sc, fmt)
+
+
+@pytest.mark.parametrize("fmt,mode", [("mxfp4", None), ("nvfp4", "current"), ("nvfp4", "delayed")])
+@pytest.mark.parametrize("M,K,N,dtype", [(1, 64, 96, torch.bfloat16), (50, 544, 288, torch.float32),
+                                         (333, 320, 608, torch.bfloat16), (1, 4096, 320, torch.bfloat16)])
+def test_dense_forward_and_backward_together(fmt, mode, M, K, N, dtype):
+    """Weights packed once along both axes, the forward keeping x^T, the backward from that."""
+    x, dy = draw(M, K, dtype, 1, spread=False), draw(M, N, dtype, 2, spread=False)
+    w = draw(K, N, torch.float32, 3, std=0.05, spread=False)
+    bias = draw(1, N, dtype, 4, spread=False)[0].contiguous()
+    mp = (M + 31) // 32 * 32
+    new = (lambda: None) if mode is None else (lambda: te.Quantizer(scale=500.0, mode=mode))
+    qw, qx, qg = new(), new(), new()
+    wc, ws = te.block_empty(fmt, K, N)
+    wct, wst = te.block_empty(fmt, N, K)
+    te.te_block_quantize(w, fmt, wc, ws, wct, wst, q=qw)
+    xt, xts = te.block_empty(fmt, K, mp)
+    out = torch.empty(M, N, dtype=dtype, device=DEV)
+    inv = lambda q: None if q is None else q.scale_inv
+    te.te_dense_fp4_fwd(x, wct, wst, out, fmt, bias=bias, q=qx, kernel_scale_inv=inv(qw), saved_xt=xt,
+                        saved_xt_scales=xts)
+    dx = torch.empty(M, K, dtype=dtype, device=DEV)
+    dw = torch.empty(K, N, dtype=dtype, device=DEV)
+    db = torch.empty(N, dtype=torch.float32, device=DEV)
+    te.te_dense_fp4_bwd(dy, wc, ws, xt, xts, dx, dw, fmt, dbias=db, q=qg, kernel_scale_inv=inv(qw),
+                        x_scale_inv=inv(qx))
+    torch.cuda.synchronize()
+    assert te.get_device_status() == 0
+
+    def scale(t):
+        return None if mode is None else (bs.nv_scale(np.abs(t).max()) if mode == "current" else np.float32(500))
+    xs, ds, wv = f64(x), f64(dy), f64(w)
+    sx, sg, sw = scale(xs), scale(ds), scale(wv)
+    al = lambda *s: float(np.prod([1.0 if v is None else np.float64(np.float32(1) / np.float32(v)) for v in s]))
+    for name, got, a, b, alpha, add in (
+            ("out", out, values(xs, fmt, sx), values(wv.T, fmt, sw), al(sx, sw), f64(bias)),
+            ("dx", dx, values(ds, fmt, sg), values(wv, fmt, sw), al(sg, sw), 0.0),
+            ("dw", dw, values(bs.pad_t(xs), fmt, sx), values(bs.pad_t(ds), fmt, sg), al(sx, sg), 0.0)):
+        want = alpha * (a @ b.T) + add
+        tol = product_bound(a, b, alpha, want, a.shape[1], dtype) + 2.0 ** -22 * np.abs(add)
+        err = np.abs(f64(got) - want)
+        assert (err <= tol).all(), (name, float((err / tol).max()))
+    # fp32 sums of M values in any order: M roundings at most
+    assert (np.abs(f64(db) - ds.sum(0)) <= (M + 4) * 2.0 ** -24 * np.abs(ds).sum(0)).all()
+
+
+def test_dense_without_tokens():
+    fmt = "mxfp4"
+    x = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
+    wc, ws = te.block_empty(fmt, 64, 96)
+    wct, wst = te.block_empty(fmt, 96, 64)
+    xt, xts = te.block_empty(fmt, 64, 0)
+    out = torch.empty(0, 96, dtype=torch.bfloat16, device=DEV)
+    te.te_dense_fp4_fwd(x, wct, wst, out, fmt, saved_xt=xt, saved_xt_scales=xts)
+    dw = torch.full((64, 96), 3.0, dtype=torch.bfloat16, device=DEV)
+    db = torch.full((96,), 3.0, device=DEV)
+    te.te_dense_fp4_bwd(out, wc, ws, xt, xts, x.clone(), dw, fmt, dbias=db)
+    assert (dw == 0).all() and (db == 0).all()
+
+
+# ---------------------------------------------------------------------------- checkpoints ---
+
+ACTS = ["relu", "gelu", "silu", "swiglu", "geglu", "reglu"]
+
+
+def ckpt_oracle(act, h, dy):
+    """(dx, act(h)) in float64."""
+    return ob.act_bwd(dy, h, act), ob.act_fwd(h, act)
+
+
+def ckpt_checked(act, M, F, dtype, dx_kind, seed=0, mode="delayed", h_std=2.0):
+    gated = act in ("swiglu", "geglu", "reglu")
+    n_in = 2 * F if gated else F
+    h = draw(M, n_in, dtype, seed, std=h_std, spread=False)
+    dy = draw(M, F, dtype, seed + 1, spread=False)
+    codes, scales = te.block_empty("mxfp8", M, n_in)
+    te.te_block_quantize(h, "mxfp8", codes, scales)
+    out_dt = {"e4m3": torch.uint8, "same": dtype}[dx_kind]
+    dx = torch.zeros(M + 1, n_in, dtype=out_dt, device=DEV)
+    a = torch.zeros(M + 1, F, dtype=dtype, device=DEV)
+    db = torch.zeros(n_in, device=DEV)
+    q = te.Quantizer(scale=16.0, mode=mode) if dx_kind == "e4m3" else None
+    te.te_dact_dbias_ckpt(dy, codes, scales, act, dx[:M], dbias=db, act_out=a[:M], q=q)
+    torch.cuda.synchronize()
+    hv = bs.unpack(*bs.pack(f64(h), "mxfp8"), "mxfp8")
+    want, wa = ckpt_oracle(act, hv, f64(dy))
+    # the kernels' fp32 arithmetic: hardware exp2 and reciprocal, ~1e-6 relative of each factor; the
+    # derivative of gelu and silu cancels near its zero, where the error is relative to its terms
+    env = np.abs(f64(dy)) * 1.2 if not gated else np.concatenate(
+        [np.abs(f64(dy) * hv[:, F:]) * 1.2, np.abs(f64(dy)) * (np.abs(hv[:, :F]) + 1)], 1)
+    err = 1e-5 * env
+    assert (np.abs(f64(a[:M]) - wa) <= 1e-5 * np.abs(wa) + 1e-30 + HALF_STEP[dtype] * np.abs(wa)).all()
+    assert (np.abs(f64(db) - want.sum(0)) <= err.sum(0) + (M + 8) * 2.0 ** -24 * np.abs(want).sum(0)).all()
+    assert (dx[M] == 0).all() and (a[M] == 0).all()
+    if dx_kind == "same":
+        assert (np.abs(f64(dx[:M]) - want) <= err + HALF_STEP[dtype] * np.abs(want)).all()
+    else:
+        amax = np.abs(want).max()
+        assert abs(q.amax.item() - amax) <= err.max()
+        s = float(q.scale.item())
+        if mode == "current":
+            assert s == nx.compute_scale(q.amax.item())[0]
+        got = nx.e4m3_decode(u8(dx[:M]))
+        lo, hi = (nx.e4m3_decode(nx.e4m3_encode((want + k * err) * s)) for k in (-1, 1))
+        assert ((got >= np.minimum(lo, hi)) & (got <= np.maximum(lo, hi))).all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_gradient_from_checkpoint(act, dtype):
+    ckpt_checked(act, 1, 32, dtype, "same")
+    ckpt_checked(act, 130, 288, dtype, "same", seed=5)
+    ckpt_checked(act, 300, 544, dtype, "e4m3", seed=7)
+    ckpt_checked(act, 77, 160, dtype, "e4m3", seed=9, mode="current")
+
+
+@pytest.mark.parametrize("act", ["gelu", "silu", "swiglu", "geglu"])
+def test_gradient_from_checkpoint_far_from_zero(act):
+    """Pre-activations far out: the activation and its derivative reach their limits, never NaN."""
+    M, F = 4, 64
+    n_in = 2 * F if act in ("swiglu", "geglu") else F
+    big = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 30.0, -30.0, 1e4, -1e4, 1e20, -1e20, 1e30, -1e30] * 11)[:n_in]
+    h = big.sort().values.repeat(M, 1).to(DEV)
+    h[1] = h[1].flip(0)
+    dy = torch.ones(M, F, device=DEV)
+    codes, scales = te.block_empty("mxfp8", M, n_in)
+    te.te_block_quantize(h, "mxfp8", codes, scales)
+    dx, a = torch.empty(M, n_in, device=DEV), torch.empty(M, F, device=DEV)
+    te.te_dact_dbias_ckpt(dy, codes, scales, act, dx, act_out=a)
+    hv = bs.unpack(*bs.pack(f64(h), "mxfp8"), "mxfp8")
+    with np.errstate(all="ignore"):
+        g = hv[:, :F]
+        s = 1 / (1 + np.exp(-g)) if act in ("silu", "swiglu") else 1 / (1 + np.exp(-2 * 0.7978845608028654 * (g + 0.044715 * g ** 3)))
+        y = np.where(np.isfinite(g * s), g * s, 0.0)
+        lin = hv[:, F:] if n_in > F else 1.0
+        wa = y * lin
+    assert torch.isfinite(dx).all()
+    fin = np.abs(wa) < 3e38
+    assert (np.abs(f64(a) - wa)[fin] <= 1e-5 * np.abs(wa)[fin] + 1e-30).all()
+
+
+def test_gradient_from_checkpoint_by_differences():
+    """dx is the slope of sum(dy * act(h)) at the checkpointed h (central differences, float64)."""
+    for act in ("gelu", "silu", "swiglu", "geglu"):
+        M, F = 3, 32
+        n_in = 2 * F if act in ("swiglu", "geglu") else F
+        h, dy = draw(M, n_in, torch.float32, 1, spread=False), draw(M, F, torch.float32, 2, spread=False)
+        codes, scales = te.block_empty("mxfp8", M, n_in)
+        te.te_block_quantize(h, "mxfp8", codes, scales)
+        dx = torch.empty(M, n_in, device=DEV)
+        te.te_dact_dbias_ckpt(dy, codes, scales, act, dx)
+        hv, e = bs.unpack(*bs.pack(f64(h), "mxfp8"), "mxfp8"), 1e-5
+        for i, j in ((0, 0), (1, n_in - 1), (2, n_in // 2), (2, 5)):
+            d = np.zeros_like(hv)
+            d[i, j] = e
+            slope = ((f64(dy) * (ob.act_fwd(hv + d, act) - ob.act_fwd(hv - d, act))).sum()) / (2 * e)
+            assert abs(slope - dx[i, j].item()) <= 1e-5 * max(1.0, abs(slope)) + 1e-8
+
+
+# ---------------------------------------------------------------- streams, graphs, layout ---
+
+
+def test_captured_and_replayed_on_other_inputs():
+    M, K, N, fmt = 9, 512, 256, "nvfp4"
+    xs = [draw(M, K, torch.bfloat16, s, spread=False) for s in (1, 2)]
+    cb, sb, ib, _, _ = packed(N, K, fmt, 5)
+    q = te.Quantizer(mode="current")
+    ws = torch.empty(te.workspace_size(te.binding.TE_OP_DENSE_FP4_FWD, M, K, N), dtype=torch.uint8, device=DEV)
+    eager = [te.te_dense_fp4_fwd(x, cb, sb, torch.empty(M, N, dtype=torch.bfloat16, device=DEV), fmt, q=q,
+                                 kernel_scale_inv=ib) for x in xs]
+    x, out = xs[0].clone(), torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        te.te_dense_fp4_fwd(x, cb, sb, out, fmt, q=q, kernel_scale_inv=ib, workspace=ws)
+    for k in (0, 1, 0):
+        x.copy_(xs[k])
+        g.replay()
+        assert torch.equal(out, eager[k])
+
+
+def test_on_another_stream_without_a_workspace_of_its_own():
+    M, K, N, fmt = 200, 1024, 512, "mxfp4"
+    x = draw(M, K, torch.bfloat16, 1)
+    cb, sb, _, _, _ = packed(N, K, fmt, 2)
+    want = te.te_dense_fp4_fwd(x, cb, sb, torch.empty(M, N, dtype=torch.bfloat16, device=DEV), fmt)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = [torch.empty(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(8)]
+    for o in outs:
+        te.te_dense_fp4_fwd(x, cb, sb, o, fmt, stream=s)
+        torch.empty(M * K, dtype=torch.uint8, device=DEV).fill_(255)  # would land in a workspace freed too early
+    torch.cuda.synchronize()
+    assert all(torch.equal(want, o) for o in outs)
+
+
+def test_tensors_the_binding_refuses():
+    x = draw(32, 64, torch.bfloat16)
+    c, s = te.block_empty("mxfp4", 32, 64)
+    with pytest.raises(ValueError, match="contiguous"):
+        te.te_block_quantize(draw(64, 32, torch.bfloat16).t(), "mxfp4", c, s)
+    with pytest.raises(ValueError, match="codes: shape"):
+        te.te_block_quantize(x, "mxfp4", c[:, :16].contiguous(), s)
+    with pytest.raises(ValueError, match="scales"):
+        te.te_block_quantize(x, "mxfp4", c, s[:100])
+    with pytest.raises(ValueError, match="q:"):
+        te.te_block_quantize(x, "nvfp4", c, te.block_empty("nvfp4", 32, 64)[1])
+    with pytest.raises(ValueError, match="dtype"):
+        te.te_block_quantize(x.half(), "mxfp4", c, s)
+    with pytest.raises((ValueError, RuntimeError)):
+        te.te_block_quantize(x.cpu(), "mxfp4", c, s)
+    with pytest.raises(te.TEError):  # a row length that is not whole blocks
+        te.te_block_quantize(draw(4, 48, torch.bfloat16), "mxfp4", *te.block_empty("mxfp4", 4, 48))
+    with pytest.raises(te.TEError):  # 8-bit codes do not go into the 4-bit product
+        e, f = te.block_empty("mxfp8", 32, 64)
+        te.te_block_gemm(e, f, e, f, torch.empty(32, 32, device=DEV), "mxfp8")
