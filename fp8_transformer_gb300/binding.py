@@ -8,6 +8,7 @@ in the library's CUDA kernels; there is no fallback.  A missing or unbuildable l
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -191,8 +192,15 @@ def _dt(t) -> int:
     return _DTYPE[t.dtype]
 
 
+# The raw handle of a device's current stream without building a Stream object for it (2.9 us of a
+# call's host time on a Grace core).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -513,27 +521,79 @@ def dact_dbias_noalloc_capacity() -> int:
 # ------------------------------------------------------------------- block-scaled tensors ---
 
 
+# The checks below run on every call and each call is short, so they are written for few Python
+# operations: one pass over a tensor's properties, which also yields its address.
+
+_ACT_DTYPES = (torch.float32, torch.bfloat16)
+_F32 = (torch.float32,)
+_U8 = (torch.uint8,)
+_E4M3_BYTES = (torch.uint8, torch.float8_e4m3fn)
+
+
 def _format(fmt) -> int:
     return BLOCK_FORMATS[fmt] if isinstance(fmt, str) else int(fmt)
 
 
-def _on_device(*tensors):
-    """The tensors (None left out) lie on the current device, where the kernels are launched."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must live on the current device (cuda:{dev})")
-
-
-def _expect(name, t, shape, *dtypes):
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+def _arg(name, t, shape, dtypes, dev):
+    """Address of a tensor that is on the current device `dev`, dense, and of this shape and type."""
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensors must live on the current device (cuda:{dev})")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensors must be contiguous")
+    return t.data_ptr()
 
 
-_ACT_DTYPES = (torch.float32, torch.bfloat16)
-_BYTES = (torch.uint8, torch.float8_e4m3fn)
+def _scale_size(f, rows, cols):
+    return (rows + 127) // 128 * ((cols // (16 if f == TE_NVFP4 else 32) + 3) // 4) * 512
+
+
+def _packed(name, codes, scales, f, rows, cols, dev):
+    """Addresses of a packed [rows, cols] tensor's codes and scales."""
+    if f == TE_MXFP8:
+        c = _arg(name, codes, (rows, cols), _E4M3_BYTES, dev)
+    else:
+        c = _arg(name, codes, (rows, cols // 2), _U8, dev)
+    if scales is None or scales.dtype not in _E4M3_BYTES or scales.numel() < _scale_size(f, rows, cols) \
+            or scales.get_device() != dev or not scales.is_contiguous():
+        raise ValueError(f"{name}: its scales must be dense uint8 on cuda:{dev}, at least "
+                         f"block_scale_bytes(fmt, {rows}, {cols}) of them")
+    return c, scales.data_ptr()
+
+
+def _scalar(name, t, dev):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != 1 or t.get_device() != dev:
+        raise ValueError(f"{name}: a one-element float32 tensor on cuda:{dev}")
+    return t.data_ptr()
+
+
+def _tensor_scale(f, q, dev):
+    """The C quantizer of NVFP4's tensor scale (None for the MX formats)."""
+    if (f == TE_NVFP4) != (q is not None):
+        raise ValueError("q: the quantizer of nvfp4's tensor scale (None for the other formats)")
+    if q is None:
+        return None
+    return ctypes.byref(_Quantizer(_scalar("q.scale", q.scale, dev), _scalar("q.scale_inv", q.scale_inv, dev),
+                                   _scalar("q.amax", q.amax, dev), q.mode))
+
+
+_sized = functools.lru_cache(maxsize=1024)(workspace_size)
+
+
+def _workspace(op, M, H, N, like, workspace, stream):
+    """(tensor, address, bytes) of the given workspace, or of a new one."""
+    if workspace is None:
+        workspace = torch.empty(max(_sized(op, M, H, N), 1), dtype=torch.uint8, device=like.device)
+        if stream is not None:  # freed on return: kept from reuse until that stream has passed it
+            workspace.record_stream(stream)
+    elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        raise ValueError("workspace: dense, on the device of the other tensors")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def block_scale_bytes(fmt, rows, cols) -> int:
@@ -548,63 +608,30 @@ def block_empty(fmt, rows, cols, device="cuda"):
     return codes, torch.empty(block_scale_bytes(f, rows, cols), dtype=torch.uint8, device=device)
 
 
-def _expect_packed(name, f, codes, scales, rows, cols):
-    _expect(name, codes, (rows, cols if f == TE_MXFP8 else cols // 2),
-            *(_BYTES if f == TE_MXFP8 else _BYTES[:1]))
-    if scales is None or scales.dtype not in _BYTES or \
-            scales.numel() < lib().te_block_scale_bytes(f, rows, cols):
-        raise ValueError(f"{name}: its scales must be uint8 of at least block_scale_bytes(fmt, {rows}, {cols})")
-
-
-def _expect_scalar(name, t):
-    if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
-        raise ValueError(f"{name}: a one-element float32 tensor")
-
-
-def _expect_quantizer(f, q):
-    if (f == TE_NVFP4) != (q is not None):
-        raise ValueError("q: the quantizer of nvfp4's tensor scale (None for the other formats)")
-    if q is not None:
-        for name in ("scale", "scale_inv", "amax"):
-            _expect_scalar(f"q.{name}", getattr(q, name))
-        _on_device(q.scale, q.scale_inv, q.amax)
-
-
-def _workspace_for(op, M, H, N, device, workspace, stream):
-    if workspace is None:
-        workspace = _ws(workspace_size(op, M, H, N), device)
-        if stream is not None:  # freed on return: kept from reuse until that stream has passed it
-            workspace.record_stream(stream)
-    return workspace
-
-
 def te_block_quantize(x, fmt, codes=None, scales=None, codes_t=None, scales_t=None, q=None, stream=None):
     """Pack x [M, N] along N into codes / scales, and (or) x^T [N, M rounded up to 32] along M into
     codes_t / scales_t, in one pass.  fmt: "mxfp8", "mxfp4" or "nvfp4" (with q, its tensor scale)."""
-    f = _format(fmt)
+    f, dev = _format(fmt), torch.cuda.current_device()
     M, N = x.shape
-    _expect("x", x, (M, N), *_ACT_DTYPES)
+    px = _arg("x", x, (M, N), _ACT_DTYPES, dev)
+    pc = ps = pct = pst = None
     if codes is not None:
-        _expect_packed("codes", f, codes, scales, M, N)
+        pc, ps = _packed("codes", codes, scales, f, M, N, dev)
     if codes_t is not None:
-        _expect_packed("codes_t", f, codes_t, scales_t, N, (M + 31) // 32 * 32)
-    _expect_quantizer(f, q)
-    _on_device(x, codes, scales, codes_t, scales_t)
-    st = lib().te_block_quantize(_ptr(x), _dt(x), M, N, f, _qp(q), _ptr(codes), _ptr(scales),
-                                 _ptr(codes_t), _ptr(scales_t), _stream(stream))
+        pct, pst = _packed("codes_t", codes_t, scales_t, f, N, (M + 31) // 32 * 32, dev)
+    st = lib().te_block_quantize(px, _dt(x), M, N, f, _tensor_scale(f, q, dev), pc, ps, pct, pst,
+                                 _stream(stream))
     _check("te_block_quantize", st)
 
 
 def te_block_dequantize(codes, scales, fmt, out, scale_inv=None, stream=None):
     """out [M, N] (float32 / bfloat16): the values that packed codes stand for."""
-    f = _format(fmt)
+    f, dev = _format(fmt), torch.cuda.current_device()
     M, N = out.shape
-    _expect("out", out, (M, N), *_ACT_DTYPES)
-    _expect_packed("codes", f, codes, scales, M, N)
-    _expect_scalar("scale_inv", scale_inv)
-    _on_device(codes, scales, out, scale_inv)
-    st = lib().te_block_dequantize(_ptr(codes), _ptr(scales), f, _ptr(scale_inv), M, N, _ptr(out),
-                                   _dt(out), _stream(stream))
+    po = _arg("out", out, (M, N), _ACT_DTYPES, dev)
+    pc, ps = _packed("codes", codes, scales, f, M, N, dev)
+    st = lib().te_block_dequantize(pc, ps, f, _scalar("scale_inv", scale_inv, dev), M, N, po, _dt(out),
+                                   _stream(stream))
     _check("te_block_dequantize", st)
     return out
 
@@ -612,21 +639,16 @@ def te_block_dequantize(codes, scales, fmt, out, scale_inv=None, stream=None):
 def te_block_gemm(a, a_scales, b, b_scales, out, fmt, a_scale_inv=None, b_scale_inv=None, bias=None,
                   stream=None):
     """out [M, N] = alpha * A B^T + bias of packed 4-bit operands a [M, K / 2] and b [N, K / 2]."""
-    f = _format(fmt)
+    f, dev = _format(fmt), torch.cuda.current_device()
     M, N = out.shape
-    K = 2 * a.shape[1]
-    _expect("out", out, (M, N), *_ACT_DTYPES)
-    _expect_packed("a", f, a, a_scales, M, K if f != TE_MXFP8 else K // 2)
-    _expect_packed("b", f, b, b_scales, N, K if f != TE_MXFP8 else K // 2)
-    if bias is not None:
-        _expect("bias", bias, (N,), *_ACT_DTYPES)
-    _expect_scalar("a_scale_inv", a_scale_inv)
-    _expect_scalar("b_scale_inv", b_scale_inv)
-    _on_device(a, a_scales, b, b_scales, out, a_scale_inv, b_scale_inv, bias)
-    st = lib().te_block_gemm(_ptr(a), _ptr(a_scales), _ptr(b), _ptr(b_scales), f, M, N, K,
-                             _ptr(a_scale_inv), _ptr(b_scale_inv), _ptr(bias),
-                             _dt(bias) if bias is not None else TE_F32, _ptr(out), _dt(out),
-                             _stream(stream))
+    K = a.shape[1] * (1 if f == TE_MXFP8 else 2)
+    po = _arg("out", out, (M, N), _ACT_DTYPES, dev)
+    pa, psa = _packed("a", a, a_scales, f, M, K, dev)
+    pb, psb = _packed("b", b, b_scales, f, N, K, dev)
+    pz = None if bias is None else _arg("bias", bias, (N,), _ACT_DTYPES, dev)
+    st = lib().te_block_gemm(pa, psa, pb, psb, f, M, N, K, _scalar("a_scale_inv", a_scale_inv, dev),
+                             _scalar("b_scale_inv", b_scale_inv, dev), pz,
+                             TE_F32 if bias is None else _dt(bias), po, _dt(out), _stream(stream))
     _check("te_block_gemm", st)
     return out
 
@@ -635,24 +657,21 @@ def te_dense_fp4_fwd(x, kernel, kernel_scales, out, fmt, bias=None, q=None, kern
                      saved_xt=None, saved_xt_scales=None, workspace=None, stream=None):
     """out [M, N] = x [M, K] @ kernel + bias with x packed on the way; kernel: [N, K / 2], the
     transposed codes (codes_t) of a kernel stored [K, N]."""
-    f = _format(fmt)
+    f, dev = _format(fmt), torch.cuda.current_device()
     M, K = x.shape
     N = out.shape[1]
-    _expect("x", x, (M, K), *_ACT_DTYPES)
-    _expect("out", out, (M, N), x.dtype)
-    _expect_packed("kernel", f, kernel, kernel_scales, N, K)
-    if bias is not None:
-        _expect("bias", bias, (N,), x.dtype)
+    dt = (x.dtype,)
+    px = _arg("x", x, (M, K), _ACT_DTYPES, dev)
+    po = _arg("out", out, (M, N), dt, dev)
+    pk, psk = _packed("kernel", kernel, kernel_scales, f, N, K, dev)
+    pz = None if bias is None else _arg("bias", bias, (N,), dt, dev)
+    pt = pst = None
     if saved_xt is not None:
-        _expect_packed("saved_xt", f, saved_xt, saved_xt_scales, K, (M + 31) // 32 * 32)
-    _expect_quantizer(f, q)
-    _expect_scalar("kernel_scale_inv", kernel_scale_inv)
-    _on_device(x, kernel, kernel_scales, out, bias, kernel_scale_inv, saved_xt, saved_xt_scales, workspace)
-    workspace = _workspace_for(TE_OP_DENSE_FP4_FWD, M, K, N, x.device, workspace, stream)
-    st = lib().te_dense_fp4_fwd(_ptr(x), _dt(x), _ptr(kernel), _ptr(kernel_scales), f, _qp(q),
-                                _ptr(kernel_scale_inv), _ptr(bias), M, K, N, _ptr(out),
-                                _ptr(saved_xt), _ptr(saved_xt_scales), _ptr(workspace),
-                                workspace.numel(), _stream(stream))
+        pt, pst = _packed("saved_xt", saved_xt, saved_xt_scales, f, K, (M + 31) // 32 * 32, dev)
+    cq = _tensor_scale(f, q, dev)
+    workspace, pw, nw = _workspace(TE_OP_DENSE_FP4_FWD, M, K, N, x, workspace, stream)
+    st = lib().te_dense_fp4_fwd(px, _dt(x), pk, psk, f, cq, _scalar("kernel_scale_inv", kernel_scale_inv, dev),
+                                pz, M, K, N, po, pt, pst, pw, nw, _stream(stream))
     _check("te_dense_fp4_fwd", st)
     return out
 
@@ -661,26 +680,22 @@ def te_dense_fp4_bwd(dy, kernel, kernel_scales, saved_xt, saved_xt_scales, dx, d
                      q=None, kernel_scale_inv=None, x_scale_inv=None, workspace=None, stream=None):
     """dx = dy @ kernel^T, dkernel [K, N] = x^T @ dy and dbias from 4-bit operands; kernel: [K, N / 2],
     the codes of a kernel stored [K, N]; saved_xt from te_dense_fp4_fwd."""
-    f = _format(fmt)
+    f, dev = _format(fmt), torch.cuda.current_device()
     M, N = dy.shape
     K = dx.shape[1]
-    _expect("dy", dy, (M, N), *_ACT_DTYPES)
-    _expect("dx", dx, (M, K), dy.dtype)
-    _expect("dkernel", dkernel, (K, N), dy.dtype)
-    _expect_packed("kernel", f, kernel, kernel_scales, K, N)
-    _expect_packed("saved_xt", f, saved_xt, saved_xt_scales, K, (M + 31) // 32 * 32)
-    if dbias is not None:
-        _expect("dbias", dbias, (N,), torch.float32)
-    _expect_quantizer(f, q)
-    _expect_scalar("kernel_scale_inv", kernel_scale_inv)
-    _expect_scalar("x_scale_inv", x_scale_inv)
-    _on_device(dy, kernel, kernel_scales, saved_xt, saved_xt_scales, dx, dkernel, dbias, kernel_scale_inv,
-               x_scale_inv, workspace)
-    workspace = _workspace_for(TE_OP_DENSE_FP4_BWD, M, K, N, dy.device, workspace, stream)
-    st = lib().te_dense_fp4_bwd(_ptr(dy), _dt(dy), _ptr(kernel), _ptr(kernel_scales), _ptr(saved_xt),
-                                _ptr(saved_xt_scales), f, _qp(q), _ptr(kernel_scale_inv),
-                                _ptr(x_scale_inv), M, K, N, _ptr(dx), _ptr(dkernel), _ptr(dbias),
-                                _ptr(workspace), workspace.numel(), _stream(stream))
+    dt = (dy.dtype,)
+    py = _arg("dy", dy, (M, N), _ACT_DTYPES, dev)
+    px = _arg("dx", dx, (M, K), dt, dev)
+    pw = _arg("dkernel", dkernel, (K, N), dt, dev)
+    pk, psk = _packed("kernel", kernel, kernel_scales, f, K, N, dev)
+    pt, pst = _packed("saved_xt", saved_xt, saved_xt_scales, f, K, (M + 31) // 32 * 32, dev)
+    pz = None if dbias is None else _arg("dbias", dbias, (N,), _F32, dev)
+    cq = _tensor_scale(f, q, dev)
+    workspace, pws, nws = _workspace(TE_OP_DENSE_FP4_BWD, M, K, N, dy, workspace, stream)
+    st = lib().te_dense_fp4_bwd(py, _dt(dy), pk, psk, pt, pst, f, cq,
+                                _scalar("kernel_scale_inv", kernel_scale_inv, dev),
+                                _scalar("x_scale_inv", x_scale_inv, dev), M, K, N, px, pw, pz, pws, nws,
+                                _stream(stream))
     _check("te_dense_fp4_bwd", st)
     return dx
 
@@ -689,20 +704,19 @@ def te_dact_dbias_ckpt(dy, codes, scales, act, dx, dbias=None, act_out=None, q=N
                        stream=None):
     """te_dact_dbias_quantize from an 8-bit checkpoint (codes, scales: mxfp8) of the activation's
     input; act_out, when given, receives the recomputed activation output."""
-    a = _act_id(act)
+    a, dev = _act_id(act), torch.cuda.current_device()
     M, N_in = dx.shape
-    n_out = N_in // 2 if a in (TE_SWIGLU, TE_GEGLU, TE_REGLU) else N_in
-    _expect("dy", dy, (M, n_out), *_ACT_DTYPES)
-    _expect("dx", dx, (M, N_in), *_ACT_DTYPES, *_BYTES)
-    _expect_packed("codes", TE_MXFP8, codes, scales, M, N_in)
-    if act_out is not None:
-        _expect("act_out", act_out, (M, n_out), dy.dtype)
+    n_out = N_in // 2 if a >= TE_SWIGLU else N_in
+    py = _arg("dy", dy, (M, n_out), _ACT_DTYPES, dev)
+    px = _arg("dx", dx, (M, N_in), _ACT_DTYPES + _E4M3_BYTES, dev)
+    pc, ps = _packed("codes", codes, scales, TE_MXFP8, M, N_in, dev)
+    pa = None if act_out is None else _arg("act_out", act_out, (M, n_out), (dy.dtype,), dev)
+    pb = pws = None
+    nws = 0
     if dbias is not None:
-        _expect("dbias", dbias, (N_in,), torch.float32)
-        workspace = _workspace_for(TE_OP_DACT_DBIAS, M, 0, N_in, dy.device, workspace, stream)
-    _on_device(dy, codes, scales, dx, dbias, act_out, workspace)
-    st = lib().te_dact_dbias_ckpt(_ptr(dy), _ptr(codes), _ptr(scales), _dt(dy), M, N_in, a, _qp(q),
-                                  _ptr(dx), _dt(dx), _ptr(act_out), _ptr(dbias), _ptr(workspace),
-                                  0 if workspace is None else workspace.numel(), _stream(stream))
+        pb = _arg("dbias", dbias, (N_in,), _F32, dev)
+        workspace, pws, nws = _workspace(TE_OP_DACT_DBIAS, M, 0, N_in, dy, workspace, stream)
+    st = lib().te_dact_dbias_ckpt(py, pc, ps, _dt(dy), M, N_in, a, _qp(q), px, _dt(dx), pa, pb, pws, nws,
+                                  _stream(stream))
     _check("te_dact_dbias_ckpt", st)
     return dx

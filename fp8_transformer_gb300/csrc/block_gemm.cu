@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "block.cuh"
+#include "cast.cuh"
 #include "kernels.h"
 #include "sync.cuh"
 #include "umma.cuh"
@@ -79,11 +80,10 @@ __device__ __forceinline__ void scale_copy(uint32_t taddr, uint32_t smem) {
     asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// The MMAs of one stage: copies its scales, then 4 steps.  sa / sb: the stage's scale tiles in
-// shared memory, [row tiles of 128][groups]; RB: 128-row tiles of B's scales.
+// Copies a stage's scales to tensor memory.  sa / sb: its scale tiles in shared memory, [row tiles
+// of 128][groups]; RB: 128-row tiles of B's scales.
 template <int FMT, int CG, int RB>
-__device__ __forceinline__ void stage_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t sa, uint32_t sb,
-                                          uint32_t tsa, uint32_t tsb, uint32_t idesc, bool first) {
+__device__ __forceinline__ void stage_scales(uint32_t sa, uint32_t sb, uint32_t tsa, uint32_t tsb) {
   constexpr int G = stage_groups(FMT);
 #pragma unroll
   for (int g = 0; g < G; ++g) {
@@ -91,6 +91,12 @@ __device__ __forceinline__ void stage_mma(uint32_t d, uint32_t a, uint32_t b, ui
 #pragma unroll
     for (int r = 0; r < RB; ++r) scale_copy<CG>(tsb + (g * RB + r) * 4, sb + (r * G + g) * kTile);
   }
+}
+
+// The MMAs of one stage, 4 steps of 64 codes.
+template <int FMT, int CG, int RB>
+__device__ __forceinline__ void stage_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t tsa, uint32_t tsb,
+                                          uint32_t idesc, bool first) {
 #pragma unroll
   for (int j = 0; j < kSteps; ++j) {
     const int g = FMT == TE_NVFP4 ? j : j / 2;                       // the step's scale tile
@@ -117,6 +123,7 @@ struct BlockGemmDev {
 
 struct BlockGemmParams {
   CUtensorMap tmA, tmB, tmSA, tmSB;
+  CUtensorMap tmD;  // output boxes of 32 rows x 128 bytes (rows by the batch)
   BlockGemmDev g;
 };
 
@@ -139,8 +146,97 @@ __device__ __forceinline__ float load_bias(const void* bias, int dtype, int64_t 
                           : __ldg(static_cast<const float*>(bias) + j);
 }
 
+__device__ __forceinline__ void load_bias8(const void* bias, int dtype, int64_t j, float (&b)[8]) {
+  if (dtype == TE_BF16) {
+    Vec16<__nv_bfloat16>::load(bias, j, b);
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(bias) + j);
+    const float4 x = __ldg(p), y = __ldg(p + 1);
+    b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
+    b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
+  }
+}
+
+// r (32 consecutive columns from col on, of which those past N do not matter) times alpha plus bias.
+__device__ __forceinline__ void scale_and_bias(const BlockGemmDev& g, float alpha, int64_t col, uint32_t (&r)[32]) {
+  const f32x2 alpha2 = f2s(alpha);
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float b[8] = {};
+    if (g.bias && col + q * 8 < g.N) load_bias8(g.bias, g.bias_dtype, col + q * 8, b);  // N is a multiple of 16
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t* w = r + q * 8 + 2 * i;
+      const f32x2 v = fma2(f2(__uint_as_float(w[0]), __uint_as_float(w[1])), alpha2, f2(b[2 * i], b[2 * i + 1]));
+      w[0] = __float_as_uint(f2lo(v));
+      w[1] = __float_as_uint(f2hi(v));
+    }
+  }
+}
+
 __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
   return mbar_try_wait(bar, parity) || wait_bounded(bar, parity, abort_flag, status, kWaitLimitNs, true);
+}
+
+// Arrives at a barrier of the pair without ordering this thread's memory accesses: what these
+// signals hand over is tensor memory, whose accesses tcgen05.wait and the tcgen05 fences order.  A
+// release at cluster scope waits for the thread's global stores as well; it made an epilogue or scale
+// warp's turn about 0.7 us longer.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// All lanes of a warp wait for the phase; false after an abort.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, int* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  int ok = 1;
+  if ((threadIdx.x & 31) == 0) ok = wait_or_abort(bar, parity, abort_flag, status) ? 1 : 0;
+  if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+  while (!mbar_try_wait(bar, parity)) {
+  }
+  __syncwarp();
+  return true;
+}
+
+__device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+
+// Four consecutive columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, uint4 v) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+// tcgen05.wait::ld tied to the registers of the load it is for, so that no use moves above it.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// A tile from shared to global memory by the TMA engine (rows and columns past the end are left
+// out), and the waits for its reads and for all of it.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* tm, uint32_t src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(tm)),
+               "r"(src), "r"(c0), "r"(c1)
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+__device__ __forceinline__ void tma_store_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+__device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 // ------------------------------------------------------------------ rows by the batch -----
@@ -148,45 +244,54 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
 constexpr int BM = 128;  // accumulator rows of a CTA
 constexpr int BN = 256;  // accumulator columns
 constexpr int kEpiWarps = 8;
-constexpr int kBatchThreads = 32 * (2 + kEpiWarps);
+constexpr int kScaleWarps = 4;
+constexpr int kBatchThreads = 32 * (2 + kEpiWarps + kScaleWarps);
 
-template <int FMT, int CG>
+template <int FMT>
 struct BatchCfg {
   static constexpr int G = stage_groups(FMT);
-  static constexpr int kBRows = BN / CG;
+  static constexpr int kBRows = BN / 2;              // B rows that a CTA holds
   static constexpr int kA = BM * kRowBytes;
   static constexpr int kB = kBRows * kRowBytes;
   static constexpr int kSA = G * kTile;
-  static constexpr int kSB = 2 * G * kTile;  // the scales of all 256 columns, in each CTA
+  static constexpr int kSB = 2 * G * kTile;          // the scales of all 256 columns, in each CTA
   static constexpr int kStage = kA + kB + kSA + kSB;
-  static constexpr int kStages = (226 * 1024 - 2048) / kStage;
-  static constexpr size_t kSmem = size_t(kStages) * kStage + 1024 + 256;
-  static constexpr uint32_t kTsa = BN, kTsb = BN + 4 * G;  // tensor-memory columns of the scales
+  static constexpr int kOut = 32 * 128;              // an epilogue warp's output stage: 32 rows x 128 bytes
+  static constexpr int kStages = (225 * 1024 - kEpiWarps * kOut) / kStage;
+  static constexpr size_t kSmem = size_t(kStages) * kStage + kEpiWarps * kOut + 1024 + 512;
+  // tensor-memory columns of the scales: sets of A's (4 G) and B's (8 G) for one stage each, used
+  // in turn, as many as there are columns for: the way from a set's last MMA over its next scales
+  // to its next MMA takes about four stages' time
+  static constexpr uint32_t kSet = 12 * G, kSets = (512 - BN) / kSet;
 };
 
-template <int FMT, int CG>
+template <int FMT>
 __global__ void __launch_bounds__(kBatchThreads, 1)
     block_gemm_kernel(const __grid_constant__ BlockGemmParams p) {
-  using C = BatchCfg<FMT, CG>;
+  using C = BatchCfg<FMT>;
   constexpr int STAGES = C::kStages;
   const BlockGemmDev& g = p.g;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smA = smem_u32(smem), smB = smA + STAGES * C::kA;
-  const uint32_t smSA = smB + STAGES * C::kB, smSB = smSA + STAGES * C::kSA;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStage);
-  uint64_t* full = bars;
-  uint64_t* empty = bars + STAGES;
-  uint64_t* tfull = empty + STAGES;
+  const uint32_t smOut = smB + STAGES * C::kB;
+  const uint32_t smSA = smOut + kEpiWarps * C::kOut, smSB = smSA + STAGES * C::kSA;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStage + kEpiWarps * C::kOut);
+  uint64_t* full = bars;              // codes of a stage, both CTAs' (in the pair's even CTA)
+  uint64_t* empty = full + STAGES;    // the pair has consumed the stage
+  uint64_t* sload = empty + STAGES;   // scales of a stage, this CTA's
+  uint64_t* sready = sload + STAGES;  // a set of scale columns is written (in the even CTA)
+  uint64_t* sfree = sready + C::kSets;
+  uint64_t* tfull = sfree + C::kSets;
   uint64_t* tempty = tfull + 1;
   uint64_t* drain = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 1 ? 0u : cluster_rank();
+  const uint32_t rank = cluster_rank();
   const bool leader = rank == 0;
-  const int cluster_id = int(blockIdx.x) / CG, num_clusters = int(gridDim.x) / CG;
+  const int cluster_id = int(blockIdx.x) / 2, num_clusters = int(gridDim.x) / 2;
   const int num_tiles = g.num_m * g.num_n;
   // raster groups of group_m m-tiles, m fastest: a group's A stays in L2 while it sweeps B
   auto tile_of = [&](int t, int& tm, int& tn) {
@@ -200,23 +305,29 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
+      mbar_init(smem_u32(&sload[s]), 1);
+    }
+    for (uint32_t s = 0; s < C::kSets; ++s) {
+      mbar_init(smem_u32(&sready[s]), 2 * kScaleWarps);
+      mbar_init(smem_u32(&sfree[s]), 1);
     }
     mbar_init(smem_u32(tfull), 1);
-    mbar_init(smem_u32(tempty), 32 * kEpiWarps * CG);
+    mbar_init(smem_u32(tempty), 2 * kEpiWarps);
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     mbar_init_fence();
     prefetch_maps(p);
   }
-  if (warp == 1) tmem_alloc<CG>(smem_u32(tmem_slot), 512);
+  if (warp == 1) tmem_alloc<2>(smem_u32(tmem_slot), 512);
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();  // the peer's barriers exist before anyone signals them
+  cluster_sync();  // the peer's barriers exist before anyone signals them
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == 0) {
+    // ------------------------------------------------------------- TMA producer ----------
     if (lane == 0) {
       int stage = 0;
       uint32_t phase = 0, issued = 0, last_parity = 0;
@@ -224,22 +335,19 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
       for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
         int tm, tn;
         tile_of(t, tm, tn);
-        const int mt = tm * CG + int(rank);  // this CTA's 128 rows
+        const int mt = tm * 2 + int(rank);  // this CTA's 128 rows
         for (int kb = 0; kb < g.num_kb; ++kb) {
           if (!wait_or_abort(smem_u32(&empty[stage]), phase ^ 1, abort_flag, g.status)) {
             ok = false;
             break;
           }
-          const uint32_t fb = CG == 1 ? smem_u32(&full[stage]) : map_to_rank(smem_u32(&full[stage]), 0);
-          if (leader) mbar_expect_tx(smem_u32(&full[stage]), CG * C::kStage);
-          auto load = [&](uint32_t dst, const CUtensorMap* m, int c0, int c1) {
-            if constexpr (CG == 1) tma_load_2d(dst, m, fb, c0, c1);
-            else tma_load_2d_pair(dst, m, fb, c0, c1);
-          };
-          load(smA + stage * C::kA, &p.tmA, kb * kRowBytes, mt * BM);
-          load(smB + stage * C::kB, &p.tmB, kb * kRowBytes, tn * BN + int(rank) * C::kBRows);
-          load(smSA + stage * C::kSA, &p.tmSA, kb * C::G * 64, mt);
-          load(smSB + stage * C::kSB, &p.tmSB, kb * C::G * 64, tn * 2);
+          const uint32_t fb = map_to_rank(smem_u32(&full[stage]), 0), sb = smem_u32(&sload[stage]);
+          if (leader) mbar_expect_tx(smem_u32(&full[stage]), 2 * (C::kA + C::kB));
+          mbar_expect_tx(sb, C::kSA + C::kSB);
+          tma_load_2d(smSA + stage * C::kSA, &p.tmSA, sb, kb * C::G * 64, mt);
+          tma_load_2d(smSB + stage * C::kSB, &p.tmSB, sb, kb * C::G * 64, tn * 2);
+          tma_load_2d_pair(smA + stage * C::kA, &p.tmA, fb, kb * kRowBytes, mt * BM);
+          tma_load_2d_pair(smB + stage * C::kB, &p.tmB, fb, kb * kRowBytes, tn * BN + int(rank) * C::kBRows);
           issued |= 1u << stage;
           last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
           if (++stage == STAGES) {
@@ -248,112 +356,189 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
           }
         }
       }
-      if (leader) {
-        // copies still in flight (the pair's) complete before the CTAs may exit
-        for (int s = 0; s < STAGES; ++s)
-          if (issued & (1u << s))
-            wait_bounded(smem_u32(&full[s]), (last_parity >> s) & 1, abort_flag, g.status, kDrainLimitNs, false);
-      } else if (!ok) {
-        // the peer's copies signal the leader: after an abort give them time to land
+      // copies still in flight into this CTA, and the peer's signals to it, come before it may exit
+      for (int s = 0; s < STAGES; ++s)
+        if (issued & (1u << s)) {
+          const uint32_t parity = (last_parity >> s) & 1;
+          wait_bounded(smem_u32(&sload[s]), parity, abort_flag, g.status, kDrainLimitNs, false);
+          if (leader) wait_bounded(smem_u32(&full[s]), parity, abort_flag, g.status, kDrainLimitNs, false);
+          if (ok) wait_bounded(smem_u32(&empty[s]), parity, abort_flag, g.status, kWaitLimitNs, true);
+        }
+      if (!ok) {
+        // after an abort: copies that the peer issued or observes get time to land
         const uint64_t t0 = global_ns();
         while (global_ns() - t0 < 100000ull) {
         }
       }
     }
   } else if (warp == 1) {
+    // ------------------------------------------------------------- MMA issuer ------------
     if (lane == 0 && leader) {
-      constexpr uint32_t idesc = block_idesc<FMT>(BM * CG, BN);
+      constexpr uint32_t idesc = block_idesc<FMT>(2 * BM, BN);
       int stage = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t phase = 0, acc_phase = 0, set = 0, set_phase = 0;
       bool ok = true;
       for (int t = cluster_id; t < num_tiles && ok; t += num_clusters, acc_phase ^= 1) {
         if (!wait_or_abort(smem_u32(tempty), acc_phase ^ 1, abort_flag, g.status)) break;
         tc_fence_after();
         for (int kb = 0; kb < g.num_kb; ++kb) {
-          if (!wait_or_abort(smem_u32(&full[stage]), phase, abort_flag, g.status)) {
+          if (!wait_or_abort(smem_u32(&sready[set]), set_phase, abort_flag, g.status) ||
+              !wait_or_abort(smem_u32(&full[stage]), phase, abort_flag, g.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          stage_mma<FMT, CG, 2>(tmem, smA + stage * C::kA, smB + stage * C::kB, smSA + stage * C::kSA,
-                                smSB + stage * C::kSB, tmem + C::kTsa, tmem + C::kTsb, idesc, kb == 0);
-          if constexpr (CG == 1) umma_commit<1>(smem_u32(&empty[stage]));
-          else umma_commit_mc(smem_u32(&empty[stage]), 0x3);
+          const uint32_t ts = tmem + BN + set * C::kSet;
+          stage_mma<FMT, 2, 2>(tmem, smA + stage * C::kA, smB + stage * C::kB, ts, ts + 4 * C::G, idesc, kb == 0);
+          umma_commit_mc(smem_u32(&empty[stage]), 0x3);
+          umma_commit_mc(smem_u32(&sfree[set]), 0x3);
+          if (++set == C::kSets) {
+            set = 0;
+            set_phase ^= 1;
+          }
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        if constexpr (CG == 1) umma_commit<1>(smem_u32(tfull));
-        else umma_commit_mc(smem_u32(tfull), 0x3);
+        umma_commit_mc(smem_u32(tfull), 0x3);
       }
       // own MMAs complete before tensor memory is released
-      umma_commit<CG>(smem_u32(drain));
+      umma_commit<2>(smem_u32(drain));
       wait_bounded(smem_u32(drain), 0, abort_flag, g.status, kDrainLimitNs, false);
     }
-  } else {
-    const int quad = warp & 3, half = (warp - 2) >> 2;
+  } else if (warp < 2 + kEpiWarps) {
+    // ------------------------------------------------------------- epilogue --------------
+    // Warp w takes the lanes of quadrant w % 4 and 128 of the columns.  Results go through a
+    // swizzled stage of 32 rows x 128 bytes and a TMA store: from registers, with a row a thread, the
+    // stores of a tile took 5 us, more than the MMAs of a tile with K = 2048.
+    const int quad = warp & 3, cols = (warp - 2) >> 2;
     const float alpha = alpha_of(g);
-    const uint32_t tempty_leader = CG == 1 ? smem_u32(tempty) : map_to_rank(smem_u32(tempty), 0);
+    const uint32_t tempty_leader = map_to_rank(smem_u32(tempty), 0);
+    const uint32_t out = smOut + (warp - 2) * C::kOut + lane * 128;
+    auto stage16 = [&](int j, const uint32_t* w) {  // 16 bytes to place j of this thread's row
+      st_shared16(out + ((j ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+    };
     uint32_t phase = 0;
     for (int t = cluster_id; t < num_tiles; t += num_clusters, phase ^= 1) {
-      int ok = 1;
-      if (lane == 0) ok = wait_bounded(smem_u32(tfull), phase, abort_flag, g.status, kWaitLimitNs, true) ? 1 : 0;
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (!ok) break;
-      // the phase has completed; every lane observes it before touching tensor memory
-      while (!mbar_try_wait(smem_u32(tfull), phase)) {
-      }
-      __syncwarp();
+      if (!warp_wait(smem_u32(tfull), phase, abort_flag, g.status)) break;
       tc_fence_after();
       int tm, tn;
       tile_of(t, tm, tn);
-      const int64_t row = (int64_t(tm) * CG + rank) * BM + quad * 32 + lane;
-      const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(half * (BN / 2));
-      // this warp's half of the columns into registers, then the accumulator is free
-      uint32_t r[4][32];
+      const int row0 = (tm * 2 + int(rank)) * BM + quad * 32, col0 = tn * BN + cols * (BN / 2);
+      const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(cols * (BN / 2));
+      auto free_accumulator = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader);
+      };
+      auto send = [&](int col) {  // the stage, complete, to column `col` on
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && row0 < g.M && col < g.N)
+          tma_store_2d(&p.tmD, smOut + (warp - 2) * C::kOut, col, row0);
+      };
+      auto recycle = [&]() {  // the stage's last contents have been read
+        if (lane == 0) tma_store_wait_read();
+        __syncwarp();
+      };
+      if (g.d_dtype == TE_F32) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld32(taddr + c * 32, r);
+          recycle();
+          tmem_ld_wait32(r);
+          scale_and_bias(g, alpha, col0 + c * 32, r);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(taddr + c * 32, r[c]);
-      tmem_ld_wait();
-      tc_fence_before();
-      if constexpr (CG == 1) mbar_arrive(tempty_leader);
-      else mbar_arrive_cluster(tempty_leader);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int64_t col0 = int64_t(tn) * BN + half * (BN / 2) + c * 32;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {  // 8 columns at a time; N is a multiple of 16
-          const int64_t col = col0 + q * 8;
-          if (row < g.M && col < g.N) {
-            float v[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float b = g.bias ? load_bias(g.bias, g.bias_dtype, col + i) : 0.0f;
-              v[i] = fmaf(__uint_as_float(r[c][q * 8 + i]), alpha, b);
-            }
-            const int64_t at = row * g.N + col;
-            if (g.d_dtype == TE_F32) {
-              float4* o = reinterpret_cast<float4*>(static_cast<float*>(g.D) + at);
-              o[0] = make_float4(v[0], v[1], v[2], v[3]);
-              o[1] = make_float4(v[4], v[5], v[6], v[7]);
-            } else {
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(g.D) + at) =
-                  make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                             pack_bf16x2(v[6], v[7]));
-            }
-          }
+          for (int j = 0; j < 8; ++j) stage16(j, r + 4 * j);
+          if (c == 3) free_accumulator();
+          send(col0 + c * 32);
         }
+      } else {
+        // the first 64 columns go to the stage and the rest to registers, so that the accumulator is
+        // free before anything waits for a store
+        uint32_t r[2][32], w[16], keep[2][16];
+        tmem_ld32(taddr, r[0]);
+        recycle();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          tmem_ld_wait32(r[c & 1]);
+          if (c < 3) tmem_ld32(taddr + (c + 1) * 32, r[(c + 1) & 1]);
+          else free_accumulator();
+          scale_and_bias(g, alpha, col0 + c * 32, r[c & 1]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const uint32_t v = pack_bf16x2(__uint_as_float(r[c & 1][2 * i]), __uint_as_float(r[c & 1][2 * i + 1]));
+            if (c < 2) w[i] = v;
+            else keep[c - 2][i] = v;
+          }
+          if (c < 2)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) stage16(c * 4 + j, w + 4 * j);
+        }
+        send(col0);
+        recycle();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) stage16(j, keep[j / 4] + 4 * (j % 4));
+        send(col0 + 64);
+      }
+    }
+    if (lane == 0) tma_store_wait();
+  } else {
+    // ------------------------------------------------------------- scales ----------------
+    // Every warp writes its 32 lanes of a set: lane r takes the 16 bytes of row r of each tile.
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    int stage = 0;
+    uint32_t phase = 0, set = 0, set_phase = 0;
+    bool ok = true;
+    for (int t = cluster_id; t < num_tiles && ok; t += num_clusters)
+      for (int kb = 0; kb < g.num_kb; ++kb) {
+        if (!warp_wait(smem_u32(&sfree[set]), set_phase ^ 1, abort_flag, g.status) ||
+            !warp_wait(smem_u32(&sload[stage]), phase, abort_flag, g.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t ts = tmem + lanes + BN + set * C::kSet;
+        const uint32_t sa = smSA + stage * C::kSA + lane * 16, sb = smSB + stage * C::kSB + lane * 16;
+#pragma unroll
+        for (int q = 0; q < C::G; ++q) {
+          tmem_st4(ts + q * 4, ld_shared16(sa + q * kTile));
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+            tmem_st4(ts + (C::G + q * 2 + r) * 4, ld_shared16(sb + (r * C::G + q) * kTile));
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(&sready[set]), 0));
+        if (++set == C::kSets) {
+          set = 0;
+          set_phase ^= 1;
+        }
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+    // the last sets are handed back (signals to this CTA) before it may exit
+    for (uint32_t i = 0; i < C::kSets && ok; ++i) {
+      ok = warp_wait(smem_u32(&sfree[set]), set_phase ^ 1, abort_flag, g.status);
+      if (++set == C::kSets) {
+        set = 0;
+        set_phase ^= 1;
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if constexpr (CG == 2) cluster_sync();  // no MMA of the pair still writes this CTA's columns
+  cluster_sync();  // no MMA of the pair still writes this CTA's columns, no copy its memory
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc<CG>(tmem, 512);
+    tmem_dealloc<2>(tmem, 512);
   }
 }
 
@@ -368,7 +553,8 @@ struct FewCfg {
   static constexpr int kT = TOK * kRowBytes;  // the tokens
   static constexpr int kS = G * kTile;        // scales of either (tokens: one tile of 128 rows)
   static constexpr int kStage = kW + kT + 2 * kS;
-  static constexpr int kStages = (200 * 1024) / kStage < 10 ? (200 * 1024) / kStage : 10;
+  // two CTAs to an SM, so that the tiles of a wide weight are all resident at once
+  static constexpr int kStages = (113 * 1024 - 1024 - 256) / kStage;
   static constexpr size_t kSmem = size_t(kStages) * kStage + 1024 + 256;
   static constexpr uint32_t kTsw = TOK < 32 ? 32 : TOK, kTst = kTsw + 4 * G;
   static constexpr uint32_t kNeed = kTst + 4 * G;
@@ -390,7 +576,7 @@ __device__ __forceinline__ void store_one(const BlockGemmDev& g, int64_t at, flo
 // Grid: (clusters of `split` CTAs along K) x tiles of 128 weight rows; M <= TOK tokens.  Here the
 // MMA's A side is the weights (g's B operand).
 template <int FMT, int TOK>
-__global__ void __launch_bounds__(kFewThreads, 1)
+__global__ void __launch_bounds__(kFewThreads, 2)
     block_gemm_few_kernel(const __grid_constant__ BlockGemmParams p, int split) {
   using C = FewCfg<FMT, TOK>;
   constexpr int STAGES = C::kStages;
@@ -477,8 +663,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       for (int i = 0; i < nkb; ++i) {
         if (!wait_or_abort(smem_u32(&full[stage]), phase, abort_flag, g.status)) break;
         tc_fence_after();
-        stage_mma<FMT, 1, 1>(tmem, smW + stage * C::kW, smT + stage * C::kT, smSW + stage * C::kS,
-                             smST + stage * C::kS, tmem + C::kTsw, tmem + C::kTst, idesc, i == 0);
+        stage_scales<FMT, 1, 1>(smSW + stage * C::kS, smST + stage * C::kS, tmem + C::kTsw, tmem + C::kTst);
+        stage_mma<FMT, 1, 1>(tmem, smW + stage * C::kW, smT + stage * C::kT, tmem + C::kTsw, tmem + C::kTst, idesc,
+                             i == 0);
         umma_commit<1>(smem_u32(&empty[stage]));
         if (++stage == STAGES) {
           stage = 0;
@@ -595,26 +782,27 @@ bool code_map(CUtensorMap* tm, const void* ptr, int64_t rows, int64_t K, uint32_
   return make_tmap_2d(tm, ptr, TE_E4M3, uint64_t(K / 2), uint64_t(rows), kRowBytes, box_rows, true);
 }
 
-template <int FMT, int CG>
+template <int FMT>
 te_status launch_batch(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStream_t s) {
-  using C = BatchCfg<FMT, CG>;
+  using C = BatchCfg<FMT>;
   BlockGemmDev& g = prm.g;
   const uint64_t groups = uint64_t(scale_groups(FMT, a.K));
-  g.num_m = int(ceil_div(a.M, BM * CG));
+  g.num_m = int(ceil_div(a.M, BM * 2));
   g.num_n = int(ceil_div(a.N, BN));
   if (!code_map(&prm.tmA, a.A, a.M, a.K, BM) || !code_map(&prm.tmB, a.B, a.N, a.K, C::kBRows) ||
       !make_tmap_scales(&prm.tmSA, a.a_scales, groups, uint64_t(ceil_div(a.M, 128)), C::G, 1) ||
-      !make_tmap_scales(&prm.tmSB, a.b_scales, groups, uint64_t(ceil_div(a.N, 128)), C::G, 2))
+      !make_tmap_scales(&prm.tmSB, a.b_scales, groups, uint64_t(ceil_div(a.N, 128)), C::G, 2) ||
+      !make_tmap_2d(&prm.tmD, a.D, a.d_dtype, uint64_t(a.N), uint64_t(a.M), a.d_dtype == TE_F32 ? 32 : 64, 32, true))
     return TE_ERR_CUDA;
-  const int64_t tile_bytes = int64_t(BM) * CG * a.K / 2;
+  const int64_t tile_bytes = int64_t(BM) * 2 * a.K / 2;
   const int64_t gm = (48ll << 20) / tile_bytes;  // A rows that a raster group may keep in L2
   g.group_m = int(gm < 4 ? 4 : gm < g.num_m ? gm : g.num_m);
-  const int64_t tiles = int64_t(g.num_m) * g.num_n, slots = num_sms() / CG;
+  const int64_t tiles = int64_t(g.num_m) * g.num_n, slots = num_sms() / 2;
   if (tiles > 0x3fffffff) return TE_ERR_UNSUPPORTED;
   static PerDevice<bool> set;
-  if (!allow_smem(block_gemm_kernel<FMT, CG>, C::kSmem, set)) return TE_ERR_CUDA;
-  return launch_clusters(block_gemm_kernel<FMT, CG>, int(tiles < slots ? tiles : slots) * CG, kBatchThreads,
-                         C::kSmem, CG, s, prm, 0);
+  if (!allow_smem(block_gemm_kernel<FMT>, C::kSmem, set)) return TE_ERR_CUDA;
+  return launch_clusters(block_gemm_kernel<FMT>, int(tiles < slots ? tiles : slots) * 2, kBatchThreads, C::kSmem,
+                         2, s, prm, 0);
 }
 
 template <int FMT, int TOK>
@@ -627,9 +815,9 @@ te_status launch_few(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStream_t 
     return TE_ERR_CUDA;
   const int64_t tiles = ceil_div(a.N, BM);
   if (tiles > 0x0fffffff) return TE_ERR_UNSUPPORTED;
-  // K is split while the SMs outnumber the tiles and every CTA keeps two stages of K
+  // K is split while all CTAs still fit on the device at once and each keeps two stages of K
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= num_sms() && split * 4 <= prm.g.num_kb) split *= 2;
+  while (split < 8 && tiles * split * 2 <= 2 * num_sms() && split * 4 <= prm.g.num_kb) split *= 2;
   static PerDevice<bool> set;
   if (!allow_smem(block_gemm_few_kernel<FMT, TOK>, C::kSmem, set)) return TE_ERR_CUDA;
   return launch_clusters(block_gemm_few_kernel<FMT, TOK>, int(tiles) * split, kFewThreads, C::kSmem, split, s,
@@ -642,7 +830,7 @@ te_status launch_fmt(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStream_t 
   if (a.M <= 32) return launch_few<FMT, 32>(a, prm, s);
   if (a.M <= 64) return launch_few<FMT, 64>(a, prm, s);
   if (a.M <= 128) return launch_few<FMT, 128>(a, prm, s);
-  return launch_batch<FMT, 2>(a, prm, s);
+  return launch_batch<FMT>(a, prm, s);
 }
 
 }  // namespace

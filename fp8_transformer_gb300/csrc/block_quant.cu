@@ -144,8 +144,19 @@ __global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs
   const int64_t pitch = a.N / codes_per_byte(FMT);
   uint8_t* codes = static_cast<uint8_t*>(a.codes) + r0 * pitch + (c0 + cl) / codes_per_byte(FMT);
   uint32_t amax = 0;
+  // the passes that have rows; the scales of the others are zero (the column path needs its whole
+  // tile written)
+  int passes = kPasses;
+  if constexpr (!COL) {
+    if (a.M - r0 < kTileRows) {
+      passes = int(a.M - r0 + kRowsPass - 1) / kRowsPass;
+      for (int i = int(threadIdx.x) * 16; i < kScaleBytes; i += kThreads * 16)
+        *reinterpret_cast<uint4*>(rs + i) = make_uint4(0u, 0u, 0u, 0u);
+      __syncthreads();
+    }
+  }
 #pragma unroll 1
-  for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
+  for (int p0 = 0; p0 < passes; p0 += kBatch) {
     Eight<T> e[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {

@@ -114,3 +114,10 @@ def test_checkpoint_refusals():
                dict(db=P, ws=ODD, n=1 << 20)):
         assert f(**kw) == b.TE_ERR_UNSUPPORTED, kw
     assert f(db=P) == b.TE_ERR_WORKSPACE and f(db=P, ws=P, n=16) == b.TE_ERR_WORKSPACE
+
+
+def test_the_bindings_scale_size_is_the_librarys():
+    for f in range(3):
+        for rows in (0, 1, 127, 128, 129, 1000):
+            for cols in (32, 64, 96, 128, 160, 4096):
+                assert b._scale_size(f, rows, cols) == te.lib().te_block_scale_bytes(f, rows, cols)
