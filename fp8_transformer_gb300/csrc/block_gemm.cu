@@ -26,7 +26,6 @@
 #include <type_traits>
 
 #include "block.cuh"
-#include "cast.cuh"
 #include "kernels.h"
 #include "sync.cuh"
 #include "umma.cuh"
@@ -146,31 +145,15 @@ __device__ __forceinline__ float load_bias(const void* bias, int dtype, int64_t 
                           : __ldg(static_cast<const float*>(bias) + j);
 }
 
-__device__ __forceinline__ void load_bias8(const void* bias, int dtype, int64_t j, float (&b)[8]) {
-  if (dtype == TE_BF16) {
-    Vec16<__nv_bfloat16>::load(bias, j, b);
+// r (32 consecutive columns) times alpha plus their bias, of which lane i of the warp holds column i's.
+__device__ __forceinline__ void scale_and_bias(float alpha, bool have_bias, float bias, uint32_t (&r)[32]) {
+  if (have_bias) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      r[i] = __float_as_uint(fmaf(__uint_as_float(r[i]), alpha, __shfl_sync(0xffffffffu, bias, i)));
   } else {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(bias) + j);
-    const float4 x = __ldg(p), y = __ldg(p + 1);
-    b[0] = x.x; b[1] = x.y; b[2] = x.z; b[3] = x.w;
-    b[4] = y.x; b[5] = y.y; b[6] = y.z; b[7] = y.w;
-  }
-}
-
-// r (32 consecutive columns from col on, of which those past N do not matter) times alpha plus bias.
-__device__ __forceinline__ void scale_and_bias(const BlockGemmDev& g, float alpha, int64_t col, uint32_t (&r)[32]) {
-  const f32x2 alpha2 = f2s(alpha);
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float b[8] = {};
-    if (g.bias && col + q * 8 < g.N) load_bias8(g.bias, g.bias_dtype, col + q * 8, b);  // N is a multiple of 16
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      uint32_t* w = r + q * 8 + 2 * i;
-      const f32x2 v = fma2(f2(__uint_as_float(w[0]), __uint_as_float(w[1])), alpha2, f2(b[2 * i], b[2 * i + 1]));
-      w[0] = __float_as_uint(f2lo(v));
-      w[1] = __float_as_uint(f2hi(v));
-    }
+    for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * alpha);
   }
 }
 
@@ -184,6 +167,13 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
 // warp's turn about 0.7 us longer.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // All lanes of a warp wait for the phase; false after an abort.
@@ -243,9 +233,11 @@ __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t 
 
 constexpr int BM = 128;  // accumulator rows of a CTA
 constexpr int BN = 256;  // accumulator columns
+constexpr int kOutRow = 64;  // bytes of a row of an output stage (32 bf16 or 16 fp32 columns)
 constexpr int kEpiWarps = 8;
 constexpr int kScaleWarps = 4;
-constexpr int kBatchThreads = 32 * (2 + kEpiWarps + kScaleWarps);
+constexpr int kScaleProducer = 2 + kEpiWarps + kScaleWarps;  // the warp that loads the scales
+constexpr int kBatchThreads = 32 * (kScaleProducer + 1);
 
 template <int FMT>
 struct BatchCfg {
@@ -255,35 +247,37 @@ struct BatchCfg {
   static constexpr int kB = kBRows * kRowBytes;
   static constexpr int kSA = G * kTile;
   static constexpr int kSB = 2 * G * kTile;          // the scales of all 256 columns, in each CTA
-  static constexpr int kStage = kA + kB + kSA + kSB;
-  static constexpr int kOut = 32 * 128;              // an epilogue warp's output stage: 32 rows x 128 bytes
-  static constexpr int kStages = (225 * 1024 - kEpiWarps * kOut) / kStage;
-  static constexpr size_t kSmem = size_t(kStages) * kStage + kEpiWarps * kOut + 1024 + 512;
-  // tensor-memory columns of the scales: sets of A's (4 G) and B's (8 G) for one stage each, used
-  // in turn, as many as there are columns for: the way from a set's last MMA over its next scales
-  // to its next MMA takes about four stages' time
-  static constexpr uint32_t kSet = 12 * G, kSets = (512 - BN) / kSet;
+  static constexpr int kOut = 32 * kOutRow;          // an epilogue warp's output stage: 32 rows
+  // Codes and scales have rings of their own.  A stage of either comes round again after its
+  // release, a TMA load and its use, about 1.7 us, in which the tensor cores want five of them.
+  static constexpr int kStages = FMT == TE_NVFP4 ? 5 : 6;
+  static constexpr int kScaleStages = FMT == TE_NVFP4 ? 7 : 5;
+  static constexpr int kBytes = kStages * (kA + kB) + kEpiWarps * kOut + kScaleStages * (kSA + kSB);
+  static constexpr size_t kSmem = size_t(kBytes) + 1024 + 512;
+  static_assert(kSmem <= 227 * 1024, "shared memory");
+  // tensor-memory columns of the scales: for each stage a set of A's (4 G) and B's (8 G)
+  static constexpr uint32_t kSet = 12 * G;
+  static_assert(BN + kStages * kSet <= 512, "tensor memory");
 };
 
 template <int FMT>
 __global__ void __launch_bounds__(kBatchThreads, 1)
     block_gemm_kernel(const __grid_constant__ BlockGemmParams p) {
   using C = BatchCfg<FMT>;
-  constexpr int STAGES = C::kStages;
+  constexpr int STAGES = C::kStages, SSTAGES = C::kScaleStages;
   const BlockGemmDev& g = p.g;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t smA = smem_u32(smem), smB = smA + STAGES * C::kA;
   const uint32_t smOut = smB + STAGES * C::kB;
-  const uint32_t smSA = smOut + kEpiWarps * C::kOut, smSB = smSA + STAGES * C::kSA;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::kStage + kEpiWarps * C::kOut);
-  uint64_t* full = bars;              // codes of a stage, both CTAs' (in the pair's even CTA)
-  uint64_t* empty = full + STAGES;    // the pair has consumed the stage
-  uint64_t* sload = empty + STAGES;   // scales of a stage, this CTA's
-  uint64_t* sready = sload + STAGES;  // a set of scale columns is written (in the even CTA)
-  uint64_t* sfree = sready + C::kSets;
-  uint64_t* tfull = sfree + C::kSets;
+  const uint32_t smSA = smOut + kEpiWarps * C::kOut, smSB = smSA + SSTAGES * C::kSA;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBytes);
+  uint64_t* full = bars;              // a stage's codes and scale columns, both CTAs' (even CTA)
+  uint64_t* empty = full + STAGES;    // the pair has consumed the stage and its scale columns
+  uint64_t* sload = empty + STAGES;   // scales of a scale stage, this CTA's
+  uint64_t* sempty = sload + SSTAGES;
+  uint64_t* tfull = sempty + SSTAGES;
   uint64_t* tempty = tfull + 1;
   uint64_t* drain = tempty + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -303,13 +297,12 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&full[s]), 1 + 2 * kScaleWarps);
       mbar_init(smem_u32(&empty[s]), 1);
-      mbar_init(smem_u32(&sload[s]), 1);
     }
-    for (uint32_t s = 0; s < C::kSets; ++s) {
-      mbar_init(smem_u32(&sready[s]), 2 * kScaleWarps);
-      mbar_init(smem_u32(&sfree[s]), 1);
+    for (int s = 0; s < SSTAGES; ++s) {
+      mbar_init(smem_u32(&sload[s]), 1);
+      mbar_init(smem_u32(&sempty[s]), kScaleWarps);
     }
     mbar_init(smem_u32(tfull), 1);
     mbar_init(smem_u32(tempty), 2 * kEpiWarps);
@@ -341,11 +334,8 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t fb = map_to_rank(smem_u32(&full[stage]), 0), sb = smem_u32(&sload[stage]);
+          const uint32_t fb = map_to_rank(smem_u32(&full[stage]), 0);
           if (leader) mbar_expect_tx(smem_u32(&full[stage]), 2 * (C::kA + C::kB));
-          mbar_expect_tx(sb, C::kSA + C::kSB);
-          tma_load_2d(smSA + stage * C::kSA, &p.tmSA, sb, kb * C::G * 64, mt);
-          tma_load_2d(smSB + stage * C::kSB, &p.tmSB, sb, kb * C::G * 64, tn * 2);
           tma_load_2d_pair(smA + stage * C::kA, &p.tmA, fb, kb * kRowBytes, mt * BM);
           tma_load_2d_pair(smB + stage * C::kB, &p.tmB, fb, kb * kRowBytes, tn * BN + int(rank) * C::kBRows);
           issued |= 1u << stage;
@@ -360,7 +350,6 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
       for (int s = 0; s < STAGES; ++s)
         if (issued & (1u << s)) {
           const uint32_t parity = (last_parity >> s) & 1;
-          wait_bounded(smem_u32(&sload[s]), parity, abort_flag, g.status, kDrainLimitNs, false);
           if (leader) wait_bounded(smem_u32(&full[s]), parity, abort_flag, g.status, kDrainLimitNs, false);
           if (ok) wait_bounded(smem_u32(&empty[s]), parity, abort_flag, g.status, kWaitLimitNs, true);
         }
@@ -373,40 +362,43 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------- MMA issuer ------------
-    if (lane == 0 && leader) {
+    // The whole warp walks the loop, so that descriptors and addresses stay in uniform registers, and
+    // one elected lane issues.
+    if (leader) {
       constexpr uint32_t idesc = block_idesc<FMT>(2 * BM, BN);
+      const bool issuer = elect_one();
       int stage = 0;
-      uint32_t phase = 0, acc_phase = 0, set = 0, set_phase = 0;
+      uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int t = cluster_id; t < num_tiles && ok; t += num_clusters, acc_phase ^= 1) {
-        if (!wait_or_abort(smem_u32(tempty), acc_phase ^ 1, abort_flag, g.status)) break;
+        if (!warp_wait(smem_u32(tempty), acc_phase ^ 1, abort_flag, g.status)) break;
         tc_fence_after();
         for (int kb = 0; kb < g.num_kb; ++kb) {
-          if (!wait_or_abort(smem_u32(&sready[set]), set_phase, abort_flag, g.status) ||
-              !wait_or_abort(smem_u32(&full[stage]), phase, abort_flag, g.status)) {
+          if (!warp_wait(smem_u32(&full[stage]), phase, abort_flag, g.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t ts = tmem + BN + set * C::kSet;
-          stage_mma<FMT, 2, 2>(tmem, smA + stage * C::kA, smB + stage * C::kB, ts, ts + 4 * C::G, idesc, kb == 0);
-          umma_commit_mc(smem_u32(&empty[stage]), 0x3);
-          umma_commit_mc(smem_u32(&sfree[set]), 0x3);
-          if (++set == C::kSets) {
-            set = 0;
-            set_phase ^= 1;
+          const uint32_t ts = tmem + BN + stage * C::kSet;
+          if (issuer) {
+            stage_mma<FMT, 2, 2>(tmem, smA + stage * C::kA, smB + stage * C::kB, ts, ts + 4 * C::G, idesc, kb == 0);
+            umma_commit_mc(smem_u32(&empty[stage]), 0x3);
           }
+          __syncwarp();
           if (++stage == STAGES) {
             stage = 0;
             phase ^= 1;
           }
         }
         if (!ok) break;
-        umma_commit_mc(smem_u32(tfull), 0x3);
+        if (issuer) umma_commit_mc(smem_u32(tfull), 0x3);
+        __syncwarp();
       }
       // own MMAs complete before tensor memory is released
-      umma_commit<2>(smem_u32(drain));
-      wait_bounded(smem_u32(drain), 0, abort_flag, g.status, kDrainLimitNs, false);
+      if (issuer) {
+        umma_commit<2>(smem_u32(drain));
+        wait_bounded(smem_u32(drain), 0, abort_flag, g.status, kDrainLimitNs, false);
+      }
     }
   } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------- epilogue --------------
@@ -416,17 +408,22 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
     const int quad = warp & 3, cols = (warp - 2) >> 2;
     const float alpha = alpha_of(g);
     const uint32_t tempty_leader = map_to_rank(smem_u32(tempty), 0);
-    const uint32_t out = smOut + (warp - 2) * C::kOut + lane * 128;
+    const uint32_t out = smOut + (warp - 2) * C::kOut + lane * kOutRow;
     auto stage16 = [&](int j, const uint32_t* w) {  // 16 bytes to place j of this thread's row
-      st_shared16(out + ((j ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+      st_shared16(out + ((j ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
     };
     uint32_t phase = 0;
     for (int t = cluster_id; t < num_tiles; t += num_clusters, phase ^= 1) {
-      if (!warp_wait(smem_u32(tfull), phase, abort_flag, g.status)) break;
-      tc_fence_after();
       int tm, tn;
       tile_of(t, tm, tn);
       const int row0 = (tm * 2 + int(rank)) * BM + quad * 32, col0 = tn * BN + cols * (BN / 2);
+      float bias[4] = {};  // of columns col0 + 32 c + lane, under way while the MMAs run
+      if (g.bias)
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (col0 + c * 32 + lane < g.N) bias[c] = load_bias(g.bias, g.bias_dtype, col0 + c * 32 + lane);
+      if (!warp_wait(smem_u32(tfull), phase, abort_flag, g.status)) break;
+      tc_fence_after();
       const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16) + uint32_t(cols * (BN / 2));
       auto free_accumulator = [&]() {
         tc_fence_before();
@@ -448,89 +445,115 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
         for (int c = 0; c < 4; ++c) {
           uint32_t r[32];
           tmem_ld32(taddr + c * 32, r);
-          recycle();
           tmem_ld_wait32(r);
-          scale_and_bias(g, alpha, col0 + c * 32, r);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) stage16(j, r + 4 * j);
           if (c == 3) free_accumulator();
-          send(col0 + c * 32);
+          scale_and_bias(alpha, g.bias != nullptr, c == 0 ? bias[0] : c == 1 ? bias[1] : c == 2 ? bias[2] : bias[3], r);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            recycle();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) stage16(j, r + 16 * h + 4 * j);
+            send(col0 + c * 32 + h * 16);
+          }
         }
       } else {
-        // the first 64 columns go to the stage and the rest to registers, so that the accumulator is
-        // free before anything waits for a store
-        uint32_t r[2][32], w[16], keep[2][16];
+        // rounded to registers, so that the accumulator is free before anything waits for a store
+        uint32_t r[2][32], w[4][16];
         tmem_ld32(taddr, r[0]);
-        recycle();
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           tmem_ld_wait32(r[c & 1]);
           if (c < 3) tmem_ld32(taddr + (c + 1) * 32, r[(c + 1) & 1]);
           else free_accumulator();
-          scale_and_bias(g, alpha, col0 + c * 32, r[c & 1]);
+          scale_and_bias(alpha, g.bias != nullptr, bias[c], r[c & 1]);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint32_t v = pack_bf16x2(__uint_as_float(r[c & 1][2 * i]), __uint_as_float(r[c & 1][2 * i + 1]));
-            if (c < 2) w[i] = v;
-            else keep[c - 2][i] = v;
-          }
-          if (c < 2)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) stage16(c * 4 + j, w + 4 * j);
+          for (int i = 0; i < 16; ++i)
+            w[c][i] = pack_bf16x2(__uint_as_float(r[c & 1][2 * i]), __uint_as_float(r[c & 1][2 * i + 1]));
         }
-        send(col0);
-        recycle();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) stage16(j, keep[j / 4] + 4 * (j % 4));
-        send(col0 + 64);
+        for (int c = 0; c < 4; ++c) {
+          recycle();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) stage16(j, w[c] + 4 * j);
+          send(col0 + c * 32);
+        }
       }
     }
     if (lane == 0) tma_store_wait();
+  } else if (warp == kScaleProducer) {
+    // ------------------------------------------------------------- scale producer --------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, last_parity = 0;
+      bool ok = true;
+      for (int t = cluster_id; t < num_tiles && ok; t += num_clusters) {
+        int tm, tn;
+        tile_of(t, tm, tn);
+        for (int kb = 0; kb < g.num_kb; ++kb) {
+          if (!wait_or_abort(smem_u32(&sempty[stage]), phase ^ 1, abort_flag, g.status)) {
+            ok = false;
+            break;
+          }
+          const uint32_t sb = smem_u32(&sload[stage]);
+          mbar_expect_tx(sb, C::kSA + C::kSB);
+          tma_load_2d(smSA + stage * C::kSA, &p.tmSA, sb, kb * C::G * 64, tm * 2 + int(rank));
+          tma_load_2d(smSB + stage * C::kSB, &p.tmSB, sb, kb * C::G * 64, tn * 2);
+          issued |= 1u << stage;
+          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == SSTAGES) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      for (int s = 0; s < SSTAGES; ++s)  // copies in flight land before the CTA may exit
+        if (issued & (1u << s))
+          wait_bounded(smem_u32(&sload[s]), (last_parity >> s) & 1, abort_flag, g.status, kDrainLimitNs, false);
+    }
   } else {
     // ------------------------------------------------------------- scales ----------------
     // Every warp writes its 32 lanes of a set: lane r takes the 16 bytes of row r of each tile.
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    int stage = 0;
-    uint32_t phase = 0, set = 0, set_phase = 0;
+    int stage = 0, sstage = 0;
+    uint32_t phase = 0, sphase = 0;
     bool ok = true;
     for (int t = cluster_id; t < num_tiles && ok; t += num_clusters)
       for (int kb = 0; kb < g.num_kb; ++kb) {
-        if (!warp_wait(smem_u32(&sfree[set]), set_phase ^ 1, abort_flag, g.status) ||
-            !warp_wait(smem_u32(&sload[stage]), phase, abort_flag, g.status)) {
+        if (!warp_wait(smem_u32(&sload[sstage]), sphase, abort_flag, g.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t sa = smSA + sstage * C::kSA + lane * 16, sb = smSB + sstage * C::kSB + lane * 16;
+        uint4 v[3 * C::G];  // in the order of the set's columns: A's tiles, B's by block and row tile
+#pragma unroll
+        for (int q = 0; q < C::G; ++q) {
+          v[q] = ld_shared16(sa + q * kTile);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) v[C::G + q * 2 + r] = ld_shared16(sb + (r * C::G + q) * kTile);
+        }
+        // the set's last MMAs are done
+        if (!warp_wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag, g.status)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t ts = tmem + lanes + BN + set * C::kSet;
-        const uint32_t sa = smSA + stage * C::kSA + lane * 16, sb = smSB + stage * C::kSB + lane * 16;
+        const uint32_t ts = tmem + lanes + BN + stage * C::kSet;
 #pragma unroll
-        for (int q = 0; q < C::G; ++q) {
-          tmem_st4(ts + q * 4, ld_shared16(sa + q * kTile));
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
-            tmem_st4(ts + (C::G + q * 2 + r) * 4, ld_shared16(sb + (r * C::G + q) * kTile));
-        }
+        for (int q = 0; q < 3 * C::G; ++q) tmem_st4(ts + q * 4, v[q]);
+        if (lane == 0) mbar_arrive(smem_u32(&sempty[sstage]));
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(&sready[set]), 0));
-        if (++set == C::kSets) {
-          set = 0;
-          set_phase ^= 1;
-        }
+        if (lane == 0) mbar_arrive_cluster_relaxed(map_to_rank(smem_u32(&full[stage]), 0));
         if (++stage == STAGES) {
           stage = 0;
           phase ^= 1;
         }
+        if (++sstage == SSTAGES) {
+          sstage = 0;
+          sphase ^= 1;
+        }
       }
-    // the last sets are handed back (signals to this CTA) before it may exit
-    for (uint32_t i = 0; i < C::kSets && ok; ++i) {
-      ok = warp_wait(smem_u32(&sfree[set]), set_phase ^ 1, abort_flag, g.status);
-      if (++set == C::kSets) {
-        set = 0;
-        set_phase ^= 1;
-      }
-    }
   }
   tc_fence_before();
   __syncthreads();
@@ -779,7 +802,7 @@ bool allow_smem(Kernel kernel, size_t smem, PerDevice<bool>& set) {
 
 // Codes as bytes: 128-byte rows of 256 codes, `rows` rows to a box.
 bool code_map(CUtensorMap* tm, const void* ptr, int64_t rows, int64_t K, uint32_t box_rows) {
-  return make_tmap_2d(tm, ptr, TE_E4M3, uint64_t(K / 2), uint64_t(rows), kRowBytes, box_rows, true);
+  return make_tmap_2d(tm, ptr, TE_E4M3, uint64_t(K / 2), uint64_t(rows), kRowBytes, box_rows, 128);
 }
 
 template <int FMT>
@@ -792,7 +815,7 @@ te_status launch_batch(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStream_
   if (!code_map(&prm.tmA, a.A, a.M, a.K, BM) || !code_map(&prm.tmB, a.B, a.N, a.K, C::kBRows) ||
       !make_tmap_scales(&prm.tmSA, a.a_scales, groups, uint64_t(ceil_div(a.M, 128)), C::G, 1) ||
       !make_tmap_scales(&prm.tmSB, a.b_scales, groups, uint64_t(ceil_div(a.N, 128)), C::G, 2) ||
-      !make_tmap_2d(&prm.tmD, a.D, a.d_dtype, uint64_t(a.N), uint64_t(a.M), a.d_dtype == TE_F32 ? 32 : 64, 32, true))
+      !make_tmap_2d(&prm.tmD, a.D, a.d_dtype, uint64_t(a.N), uint64_t(a.M), a.d_dtype == TE_F32 ? 16 : 32, 32, kOutRow))
     return TE_ERR_CUDA;
   const int64_t tile_bytes = int64_t(BM) * 2 * a.K / 2;
   const int64_t gm = (48ll << 20) / tile_bytes;  // A rows that a raster group may keep in L2

@@ -912,12 +912,12 @@ te_status launch_gemm(const GemmArgs& a, cudaStream_t s) {
   GemmParams prm;
   memset(&prm, 0, sizeof(prm));
   // A: op(A) is [M, K]; each CTA loads 128 rows.
-  bool ok = a.a_kmajor ? make_tmap_2d(&prm.tmA, a.A, a.ab_dtype, a.K, a.M, epr, BM, true)
-                       : make_tmap_2d(&prm.tmA, a.A, a.ab_dtype, a.M, a.K, epr, epr, true);
+  bool ok = a.a_kmajor ? make_tmap_2d(&prm.tmA, a.A, a.ab_dtype, a.K, a.M, epr, BM, 128)
+                       : make_tmap_2d(&prm.tmA, a.A, a.ab_dtype, a.M, a.K, epr, epr, 128);
   // B: op(B) is [K, N]; a K-major box holds the B columns one CTA loads at a time.
   const uint32_t b_rows = (gated || cg == 2) ? BN / 2 : BN;
-  ok = ok && (a.b_kmajor ? make_tmap_2d(&prm.tmB, a.B, a.ab_dtype, a.K, a.N, epr, b_rows, true)
-                         : make_tmap_2d(&prm.tmB, a.B, a.ab_dtype, a.N, a.K, epr, epr, true));
+  ok = ok && (a.b_kmajor ? make_tmap_2d(&prm.tmB, a.B, a.ab_dtype, a.K, a.N, epr, b_rows, 128)
+                         : make_tmap_2d(&prm.tmB, a.B, a.ab_dtype, a.N, a.K, epr, epr, 128));
   if (!ok) return TE_ERR_CUDA;
   GemmDev& g = prm.g;
   g.M = a.M;

@@ -294,9 +294,9 @@ class PerDevice {
 };
 
 // 2-D TMA tensor map over a row-major [outer, inner] matrix of dtype, boxes of
-// box_inner x box_outer elements, 128-byte swizzle or none, out-of-bounds reads zero.
+// box_inner x box_outer elements, a swizzle of 128 or 64 bytes or none (0), out-of-bounds reads zero.
 bool make_tmap_2d(CUtensorMap* tm, const void* ptr, int dtype, uint64_t inner, uint64_t outer,
-                  uint32_t box_inner, uint32_t box_outer, bool swizzle128);
+                  uint32_t box_inner, uint32_t box_outer, int swizzle);
 
 // 2-D TMA tensor map over block scales: rows of tiles by 512-byte tiles, boxes of box_rows rows
 // of tiles x box_tiles tiles, out-of-bounds reads zero.

@@ -31,7 +31,7 @@ EncodeTiledFn encode_fn() {
 }  // namespace
 
 bool make_tmap_2d(CUtensorMap* tm, const void* ptr, int dtype, uint64_t inner, uint64_t outer,
-                  uint32_t box_inner, uint32_t box_outer, bool swizzle128) {
+                  uint32_t box_inner, uint32_t box_outer, int swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   CUtensorMapDataType dt = dtype == TE_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -44,7 +44,9 @@ bool make_tmap_2d(CUtensorMap* tm, const void* ptr, int dtype, uint64_t inner, u
   cuuint32_t estr[2] = {1, 1};
   return fn(tm, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr,
             CU_TENSOR_MAP_INTERLEAVE_NONE,
-            swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+            swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+            : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                            : CU_TENSOR_MAP_SWIZZLE_NONE,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
