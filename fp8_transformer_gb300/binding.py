@@ -147,6 +147,8 @@ def lib_path() -> str:
 def lib(build_if_stale: bool = True) -> ctypes.CDLL:
     """The loaded library; compiles it first when it is missing or older than its sources."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if build_if_stale and not _build.up_to_date():

@@ -15,8 +15,8 @@
 //    back before they convert and store, so only that copy is not hidden behind the next tile.
 //  * block_gemm_few_kernel, for few rows (tokens): bound by the bytes of the weights.  The
 //    weights take the 128-row side of the MMA and the tokens its short side, so no tensor-core row
-//    is wasted on absent tokens, and a cluster of CTAs splits K; their partial tiles are added
-//    through distributed shared memory in rank order, so the result does not vary.
+//    is wasted on absent tokens, and a cluster of CTAs splits K; their partial sums are
+//    added through distributed shared memory in rank order, so the result does not vary.
 //
 // Every wait is bounded, as in the other GEMM.
 #include <cuda.h>
@@ -569,6 +569,8 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
 
 constexpr int kFewThreads = 192;  // producer, MMA, four epilogue warps
 
+constexpr int kMaxSplit = 8;  // CTAs of a cluster that share a tile's K
+
 template <int FMT, int TOK>
 struct FewCfg {
   static constexpr int G = stage_groups(FMT);
@@ -585,19 +587,30 @@ struct FewCfg {
   static_assert(kNeed <= 256 && kStages * kStage >= BM * TOK * 4, "columns; room for the partial tile");
 };
 
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
-__device__ __forceinline__ void store_one(const BlockGemmDev& g, int64_t at, float v) {
-  if (g.d_dtype == TE_F32) static_cast<float*>(g.D)[at] = v;
-  else static_cast<__nv_bfloat16*>(g.D)[at] = __float2bfloat16_rn(v);
+// Four neighbouring outputs of one token (those past N left out).
+__device__ __forceinline__ void store_four(const BlockGemmDev& g, int64_t token, int64_t n, const float (&v)[4]) {
+  if (n >= g.N) return;  // N is a multiple of 16
+  const int64_t at = token * g.N + n;
+  if (g.d_dtype == TE_F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(g.D) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  else
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(g.D) + at) =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
 // Grid: (clusters of `split` CTAs along K) x tiles of 128 weight rows; M <= TOK tokens.  Here the
-// MMA's A side is the weights (g's B operand).
+// MMA's A side is the weights (g's B operand).  Rank t % split adds up token t: it reads the
+// partial sums from every rank's shared memory, 16 bytes a thread and all ranks' at once, and adds
+// them in rank order.  (Sending them to that rank instead took 4 us more at 33 x 4096 x 14336.)
 template <int FMT, int TOK>
 __global__ void __launch_bounds__(kFewThreads, 2)
     block_gemm_few_kernel(const __grid_constant__ BlockGemmParams p, int split) {
@@ -619,7 +632,18 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const int rank = int(blockIdx.x) % split, tile = int(blockIdx.x) / split;
   const int kb0 = int(int64_t(g.num_kb) * rank / split), kb1 = int(int64_t(g.num_kb) * (rank + 1) / split);
   const int nkb = kb1 - kb0;  // at least 1: split <= num_kb
+  const int tokens = int(g.M);
+  float* part = reinterpret_cast<float*>(smem);
+  auto load_w = [&](int stage, int kb) {
+    const uint32_t fb = smem_u32(&full[stage]);
+    mbar_expect_tx(fb, C::kStage);
+    tma_load_2d(smW + stage * C::kW, &p.tmB, fb, kb * kRowBytes, tile * BM);
+    tma_load_2d(smSW + stage * C::kS, &p.tmSB, fb, kb * C::G * 64, tile);
+  };
 
+  // The weights of the first stages are under way before anything else, and (b_ready) before the
+  // kernel that packs the tokens is done.
+  int early = 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(smem_u32(&full[s]), 1);
@@ -628,39 +652,26 @@ __global__ void __launch_bounds__(kFewThreads, 2)
     mbar_init(smem_u32(done), 1);
     *abort_flag = 0;
     mbar_init_fence();
-    prefetch_maps(p);
+    if (!g.b_ready) asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (; early < nkb && early < STAGES; ++early) load_w(early, kb0 + early);
   }
   if (warp == 1) tmem_alloc<1>(smem_u32(tmem_slot), C::kCols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   if (warp == 0) {
     if (lane == 0) {
-      auto load_w = [&](int stage, int kb) {
-        const uint32_t fb = smem_u32(&full[stage]);
-        mbar_expect_tx(fb, C::kStage);
-        tma_load_2d(smW + stage * C::kW, &p.tmB, fb, kb * kRowBytes, tile * BM);
-        tma_load_2d(smSW + stage * C::kS, &p.tmSB, fb, kb * C::G * 64, tile);
-      };
-      auto load_t = [&](int stage, int kb) {
-        const uint32_t fb = smem_u32(&full[stage]);
-        tma_load_2d(smT + stage * C::kT, &p.tmA, fb, kb * kRowBytes, 0);
-        tma_load_2d(smST + stage * C::kS, &p.tmSA, fb, kb * C::G * 64, 0);
-      };
-      // the weights of the first stages may be on their way before the kernel that packs the
-      // tokens is done
-      int early = 0;
-      if (g.b_ready)
-        for (; early < nkb && early < STAGES; ++early) load_w(early, kb0 + early);
-      asm volatile("griddepcontrol.wait;" ::: "memory");
       int stage = 0, issued = 0;
       uint32_t phase = 0;
       for (int i = 0; i < nkb; ++i) {
         if (!wait_or_abort(smem_u32(&empty[stage]), phase ^ 1, abort_flag, g.status)) break;
         if (i >= early) load_w(stage, kb0 + i);
-        load_t(stage, kb0 + i);
+        const uint32_t fb = smem_u32(&full[stage]);
+        tma_load_2d(smT + stage * C::kT, &p.tmA, fb, (kb0 + i) * kRowBytes, 0);
+        tma_load_2d(smST + stage * C::kS, &p.tmSA, fb, (kb0 + i) * C::G * 64, 0);
         issued = i + 1;
         if (++stage == STAGES) {
           stage = 0;
@@ -677,84 +688,83 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
       }
     }
+    __syncwarp();
   } else if (warp == 1) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (lane == 0) {
-      constexpr uint32_t idesc = block_idesc<FMT>(BM, TOK);
-      int stage = 0;
-      uint32_t phase = 0;
-      for (int i = 0; i < nkb; ++i) {
-        if (!wait_or_abort(smem_u32(&full[stage]), phase, abort_flag, g.status)) break;
-        tc_fence_after();
+    constexpr uint32_t idesc = block_idesc<FMT>(BM, TOK);
+    const bool issuer = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < nkb; ++i) {
+      if (!warp_wait(smem_u32(&full[stage]), phase, abort_flag, g.status)) break;
+      tc_fence_after();
+      if (issuer) {
         stage_scales<FMT, 1, 1>(smSW + stage * C::kS, smST + stage * C::kS, tmem + C::kTsw, tmem + C::kTst);
         stage_mma<FMT, 1, 1>(tmem, smW + stage * C::kW, smT + stage * C::kT, tmem + C::kTsw, tmem + C::kTst, idesc,
                              i == 0);
         umma_commit<1>(smem_u32(&empty[stage]));
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1;
-        }
       }
+      __syncwarp();
+      if (++stage == STAGES) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (issuer) {
       umma_commit<1>(smem_u32(done));
       wait_bounded(smem_u32(done), 0, abort_flag, g.status, kDrainLimitNs, false);
     }
+    __syncwarp();
   } else {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const int quad = warp & 3, row = quad * 32 + lane;
-    const int64_t n = int64_t(tile) * BM + row;
-    const float alpha = alpha_of(g);
-    const float bias = (g.bias && n < g.N) ? load_bias(g.bias, g.bias_dtype, n) : 0.0f;
-    const int tokens = int(g.M);
-    int ok = 1;
-    if (lane == 0) ok = wait_bounded(smem_u32(done), 0, abort_flag, g.status, kWaitLimitNs, true) ? 1 : 0;
-    ok = __shfl_sync(0xffffffffu, ok, 0);
-    if (ok) {
-      while (!mbar_try_wait(smem_u32(done), 0)) {
-      }
-      __syncwarp();
-    }
+    const bool ok = warp_wait(smem_u32(done), 0, abort_flag, g.status);
     tc_fence_after();
-    // the partial tile, [token][128 rows] fp32, over the pipeline's buffers: every stage has been
+    // the partial tile, [token][128 weight rows], over the pipeline's buffers: every stage has been
     // consumed (`done` follows the last MMA)
-    float* part = reinterpret_cast<float*>(smem);
     const uint32_t taddr = tmem + (uint32_t(quad * 32) << 16);
 #pragma unroll 1
-    for (int c = 0; c < (TOK + 31) / 32; ++c) {
+    for (int c = 0; c * 32 < tokens && ok; ++c) {
       uint32_t r[32];
       tmem_ld32(taddr + c * 32, r);
-      tmem_ld_wait();
-      if (!ok) break;
-      if (split == 1) {
+      tmem_ld_wait32(r);
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c * 32 + i < tokens && n < g.N)
-            store_one(g, int64_t(c * 32 + i) * g.N + n, fmaf(__uint_as_float(r[i]), alpha, bias));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c * 32 + i < TOK) part[(c * 32 + i) * BM + row] = __uint_as_float(r[i]);
-      }
+      for (int i = 0; i < 32; ++i)
+        if (c * 32 + i < tokens) part[(c * 32 + i) * BM + row] = __uint_as_float(r[i]);
     }
     tc_fence_before();
-    if (split > 1) {
-      cluster_sync();
-      // tokens go round the ranks; each sums its tokens' columns in rank order
-      if (ok)
-        for (int t = rank; t < tokens; t += split) {
-          const uint32_t at = smem_u32(part + t * BM + row);
-          float s = 0.0f;
-          for (int k = 0; k < split; ++k) s += ld_cluster(map_to_rank(at, uint32_t(k)));
-          if (n < g.N) store_one(g, int64_t(t) * g.N + n, fmaf(s, alpha, bias));
+  }
+  if (split > 1) cluster_sync();
+  else __syncthreads();
+  if (warp >= 2 && *abort_flag == 0) {
+    // a warp on a token, 4 weight rows a thread
+    const float alpha = alpha_of(g);
+    const int64_t n = int64_t(tile) * BM + lane * 4;
+    float b[4] = {};
+    if (g.bias && n < g.N)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[i] = load_bias(g.bias, g.bias_dtype, n + i);
+    for (int t = rank + (warp - 2) * split; t < tokens; t += 4 * split) {
+      const uint32_t at = smem_u32(part + t * BM + lane * 4);
+      float4 v[kMaxSplit];
+#pragma unroll
+      for (int k = 0; k < kMaxSplit; ++k)
+        if (k < split) v[k] = ld_cluster4(map_to_rank(at, uint32_t(k)));
+      float a[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int k = 1; k < kMaxSplit; ++k)
+        if (k < split) {
+          a[0] += v[k].x;
+          a[1] += v[k].y;
+          a[2] += v[k].z;
+          a[3] += v[k].w;
         }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) a[i] = fmaf(a[i], alpha, b[i]);
+      store_four(g, t, n, a);
     }
   }
   if (split > 1) {
-    if (warp < 2) {
-      __syncwarp();
-      cluster_sync();  // the partial tiles are written
-    }
     __syncwarp();
-    cluster_sync();  // and read, before any CTA of the cluster exits
+    cluster_sync();  // the partial tiles are read before any CTA of the cluster exits
   }
   tc_fence_before();
   __syncthreads();
@@ -840,7 +850,7 @@ te_status launch_few(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStream_t 
   if (tiles > 0x0fffffff) return TE_ERR_UNSUPPORTED;
   // K is split while all CTAs still fit on the device at once and each keeps two stages of K
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= 2 * num_sms() && split * 4 <= prm.g.num_kb) split *= 2;
+  while (split < kMaxSplit && tiles * split * 2 <= 2 * num_sms() && split * 4 <= prm.g.num_kb) split *= 2;
   static PerDevice<bool> set;
   if (!allow_smem(block_gemm_few_kernel<FMT, TOK>, C::kSmem, set)) return TE_ERR_CUDA;
   return launch_clusters(block_gemm_few_kernel<FMT, TOK>, int(tiles) * split, kFewThreads, C::kSmem, split, s,
@@ -851,6 +861,7 @@ template <int FMT>
 te_status launch_fmt(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStream_t s) {
   if (a.M <= 16) return launch_few<FMT, 16>(a, prm, s);
   if (a.M <= 32) return launch_few<FMT, 32>(a, prm, s);
+  if (a.M <= 48) return launch_few<FMT, 48>(a, prm, s);
   if (a.M <= 64) return launch_few<FMT, 64>(a, prm, s);
   if (a.M <= 128) return launch_few<FMT, 128>(a, prm, s);
   return launch_batch<FMT>(a, prm, s);

@@ -111,12 +111,15 @@ template <typename T>
 __host__ __device__ constexpr size_t col_smem() { return size_t(kTileRows) * tile_pitch<T>() + kColTile * kStagePitch; }
 
 // TC: columns of a tile (256 when only the rows are packed, for whole 128-byte runs of codes).
-template <typename T, int FMT, int TC, bool COL>
+// SUB: rows of the tile that a CTA takes, 128, or 32 (rows only) so that few rows still occupy many
+// SMs; such a CTA writes the 4 bytes of each 16 of a scale tile that are its rows'.
+template <typename T, int FMT, int TC, bool COL, int SUB>
 __global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs a) {
+  static_assert(SUB == kTileRows || (SUB == 32 && !COL), "rows of a CTA");
   constexpr int kBlk = block_len(FMT);
   constexpr int kLanes = TC / 8;                 // lanes on one row
   constexpr int kRowsPass = kThreads / kLanes;   // rows a CTA takes at a time
-  constexpr int kPasses = kTileRows / kRowsPass;
+  constexpr int kPasses = SUB / kRowsPass;
   constexpr int kBatch = 4;                      // passes whose loads are in flight together
   constexpr int kScaleBytes = kTileRows * (TC / kBlk);
   __shared__ __align__(16) uint8_t rs[kScaleBytes];
@@ -134,8 +137,10 @@ __global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs
     }
   }
   const int64_t tiles_c = (a.N + TC - 1) / TC;
-  const int64_t rt = blockIdx.x / tiles_c, ct = blockIdx.x % tiles_c;
-  const int64_t r0 = rt * kTileRows, c0 = ct * TC;
+  const int64_t st = blockIdx.x / tiles_c, ct = blockIdx.x % tiles_c;
+  const int64_t rt = st / (kTileRows / SUB);
+  const int sub = int(st % (kTileRows / SUB));
+  const int64_t r0 = st * SUB, c0 = ct * TC;
   const int cl = int(threadIdx.x) % kLanes * 8;  // this lane's column within the tile
   const bool col_ok = c0 + cl < a.N;             // N is a multiple of 32: whole blocks
   const int rl = int(threadIdx.x) / kLanes;
@@ -144,19 +149,8 @@ __global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs
   const int64_t pitch = a.N / codes_per_byte(FMT);
   uint8_t* codes = static_cast<uint8_t*>(a.codes) + r0 * pitch + (c0 + cl) / codes_per_byte(FMT);
   uint32_t amax = 0;
-  // the passes that have rows; the scales of the others are zero (the column path needs its whole
-  // tile written)
-  int passes = kPasses;
-  if constexpr (!COL) {
-    if (a.M - r0 < kTileRows) {
-      passes = int(a.M - r0 + kRowsPass - 1) / kRowsPass;
-      for (int i = int(threadIdx.x) * 16; i < kScaleBytes; i += kThreads * 16)
-        *reinterpret_cast<uint4*>(rs + i) = make_uint4(0u, 0u, 0u, 0u);
-      __syncthreads();
-    }
-  }
 #pragma unroll 1
-  for (int p0 = 0; p0 < passes; p0 += kBatch) {
+  for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
     Eight<T> e[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
@@ -193,8 +187,13 @@ __global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs
     const int64_t g0 = c0 / kBlk / 4;
     const int n = int(min(int64_t(kScaleBytes), (groups - g0) * 512));
     uint8_t* dst = static_cast<uint8_t*>(a.scales) + (rt * groups + g0) * 512;
-    for (int i = int(threadIdx.x) * 16; i < n; i += kThreads * 16)
-      *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(rs + i);
+    if constexpr (SUB == kTileRows) {
+      for (int i = int(threadIdx.x) * 16; i < n; i += kThreads * 16)
+        *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(rs + i);
+    } else {  // the rows r % 32 lie in words 0, 4, 8, ... of rs
+      for (int i = int(threadIdx.x) * 16; i < n; i += kThreads * 16)
+        *reinterpret_cast<uint32_t*>(dst + i + sub * 4) = *reinterpret_cast<const uint32_t*>(rs + i);
+    }
   }
   if constexpr (COL) {
     constexpr int kC = Column<T>::kCols;
@@ -269,22 +268,26 @@ te_status launch_quant_t(const BlockQuantArgs& a, cudaStream_t s) {
   const bool col = a.codes_t != nullptr;
   const int64_t tc = col ? kColTile : 256;
   const int64_t tiles = ceil_div(a.M, kTileRows) * ceil_div(a.N, tc);
-  if (tiles > 0x7fffffff) return TE_ERR_UNSUPPORTED;
+  if (tiles > 0x1fffffff) return TE_ERR_UNSUPPORTED;
   if (!col) {
-    block_quantize_kernel<T, FMT, 256, false><<<unsigned(tiles), kThreads, 0, s>>>(a);
+    // whole tiles once they give every SM two CTAs (128 x 14336 in bf16, 56 tiles: 10 us with them)
+    if (tiles < 2 * num_sms())
+      block_quantize_kernel<T, FMT, 256, false, 32><<<unsigned(tiles * 4), kThreads, 0, s>>>(a);
+    else
+      block_quantize_kernel<T, FMT, 256, false, kTileRows><<<unsigned(tiles), kThreads, 0, s>>>(a);
   } else if constexpr (FMT == TE_MXFP8) {
     return TE_ERR_UNSUPPORTED;  // checkpoints are read along their rows only
   } else {
     static PerDevice<bool> attr_set;
     bool ok = false;
     if (!attr_set.get(&ok, [](bool* v) {
-          *v = cudaFuncSetAttribute(block_quantize_kernel<T, FMT, kColTile, true>,
+          *v = cudaFuncSetAttribute(block_quantize_kernel<T, FMT, kColTile, true, kTileRows>,
                                     cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     int(col_smem<T>())) == cudaSuccess;
           return *v;
         }))
       return TE_ERR_CUDA;
-    block_quantize_kernel<T, FMT, kColTile, true><<<unsigned(tiles), kThreads, col_smem<T>(), s>>>(a);
+    block_quantize_kernel<T, FMT, kColTile, true, kTileRows><<<unsigned(tiles), kThreads, col_smem<T>(), s>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? TE_OK : TE_ERR_CUDA;
 }

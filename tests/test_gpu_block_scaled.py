@@ -191,7 +191,7 @@ def gemm_checked(M, N, K, fmt, bias=None, dtype=torch.bfloat16):
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
-@pytest.mark.parametrize("M", [1, 16, 17, 33, 64, 100, 128])
+@pytest.mark.parametrize("M", [1, 16, 17, 33, 48, 64, 100, 128])
 def test_product_of_few_rows(M, fmt):
     gemm_checked(M, 128, 256, fmt)
     gemm_checked(M, 16, 32, fmt, bias=torch.bfloat16)
