@@ -585,12 +585,24 @@ def _tensor_scale(f, q, dev):
 
 
 _sized = functools.lru_cache(maxsize=1024)(workspace_size)
+_SMALL_WORKSPACE = 1 << 20
+_small = threading.local()
 
 
 def _workspace(op, M, H, N, like, workspace, stream):
-    """(tensor, address, bytes) of the given workspace, or of a new one."""
+    """(tensor, address, bytes) of the given workspace, or of a new one.  Small ones of eager calls
+    are kept, one for each host thread and stream, whose calls run one after another: an allocation
+    costs a short call 5 to 7 us of host time, as much as its launches."""
     if workspace is None:
-        workspace = torch.empty(max(_sized(op, M, H, N), 1), dtype=torch.uint8, device=like.device)
+        n = max(_sized(op, M, H, N), 1)
+        if n <= _SMALL_WORKSPACE and stream is None and not torch.cuda.is_current_stream_capturing():
+            key = (like.get_device(), _stream(None))
+            kept = _small.__dict__.setdefault("kept", {})
+            workspace = kept.get(key)
+            if workspace is None:
+                workspace = kept[key] = torch.empty(_SMALL_WORKSPACE, dtype=torch.uint8, device=like.device)
+            return workspace, workspace.data_ptr(), _SMALL_WORKSPACE
+        workspace = torch.empty(n, dtype=torch.uint8, device=like.device)
         if stream is not None:  # freed on return: kept from reuse until that stream has passed it
             workspace.record_stream(stream)
     elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
@@ -671,7 +683,9 @@ def te_dense_fp4_fwd(x, kernel, kernel_scales, out, fmt, bias=None, q=None, kern
     if saved_xt is not None:
         pt, pst = _packed("saved_xt", saved_xt, saved_xt_scales, f, K, (M + 31) // 32 * 32, dev)
     cq = _tensor_scale(f, q, dev)
-    workspace, pw, nw = _workspace(TE_OP_DENSE_FP4_FWD, M, K, N, x, workspace, stream)
+    pw, nw = None, 0
+    if M > 8 or saved_xt is not None or workspace is not None:
+        workspace, pw, nw = _workspace(TE_OP_DENSE_FP4_FWD, M, K, N, x, workspace, stream)
     st = lib().te_dense_fp4_fwd(px, _dt(x), pk, psk, f, cq, _scalar("kernel_scale_inv", kernel_scale_inv, dev),
                                 pz, M, K, N, po, pt, pst, pw, nw, _stream(stream))
     _check("te_dense_fp4_fwd", st)

@@ -98,4 +98,68 @@ __device__ __forceinline__ float nv_scale_from_amax(float amax) {
   return isfinite(s) ? s : 3.4028234663852886e38f;
 }
 
+// 8 neighbours of T as fp32.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const void* p) { u = __ldg(static_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void to_smem(void* p) const { *static_cast<uint4*>(p) = u; }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
+    v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
+  }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    constexpr uint32_t k = 0x7fff7fffu;
+    const uint32_t m = __vmaxu2(__vmaxu2(u.x & k, u.y & k), __vmaxu2(u.z & k, u.w & k));
+    return max(m & 0xffffu, m >> 16) << 16;
+  }
+};
+template <>
+struct Eight<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const void* p) {
+    a = __ldg(static_cast<const uint4*>(p));
+    b = __ldg(static_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void to_smem(void* p) const {
+    static_cast<uint4*>(p)[0] = a;
+    static_cast<uint4*>(p)[1] = b;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z);
+    v[3] = __uint_as_float(a.w); v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
+    v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+  }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    constexpr uint32_t k = 0x7fffffffu;
+    return max(max(max(a.x & k, a.y & k), max(a.z & k, a.w & k)),
+               max(max(b.x & k, b.y & k), max(b.z & k, b.w & k)));
+  }
+};
+
+// Codes of 8 neighbours: 4 bytes (x) of E2M1 or 8 bytes of E4M3.
+template <int FMT>
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], const BlockScale& b) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 p = mul2(f2(x[2 * i], x[2 * i + 1]), f2s(b.mul));
+    v[2 * i] = f2lo(p);
+    v[2 * i + 1] = f2hi(p);
+  }
+  uint2 r = make_uint2(0u, 0u);
+  if (b.bad) return r;
+  if constexpr (FMT == TE_MXFP8) {
+    r.x = pack_e4m3x4(v[0], v[1], v[2], v[3]);
+    r.y = pack_e4m3x4(v[4], v[5], v[6], v[7]);
+  } else {
+    r.x = pack_e2m1x8(v);
+  }
+  return r;
+}
+
 }  // namespace te

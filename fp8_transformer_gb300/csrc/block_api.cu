@@ -20,9 +20,9 @@ bool format_quantizer_ok(int f, const te_quantizer* q) {
   return f == TE_NVFP4 ? enabled(q) && quantizer_ok(q) : q == nullptr;
 }
 
-// Packs x; NVFP4 finds this call's amax first when the scale is to come from it.
-te_status block_quantize(BlockQuantArgs a, const te_quantizer* q, cudaStream_t s) {
-  if (a.M == 0) return TE_OK;
+// Gives a its tensor scale's places; NVFP4 finds this call's amax first when the scale is to come
+// from it.
+te_status take_tensor_scale(BlockQuantArgs& a, const te_quantizer* q, cudaStream_t s) {
   if (a.fmt == TE_NVFP4) {
     if (q->mode == TE_SCALING_CURRENT) {
       const te_status st = launch_amax(a.x, a.x_dtype, a.M * a.N, q->amax, s);
@@ -37,7 +37,13 @@ te_status block_quantize(BlockQuantArgs a, const te_quantizer* q, cudaStream_t s
     }
     a.scale_inv_out = q->scale_inv;
   }
-  return launch_block_quantize(a, s);
+  return TE_OK;
+}
+
+te_status block_quantize(BlockQuantArgs a, const te_quantizer* q, cudaStream_t s) {
+  if (a.M == 0) return TE_OK;
+  const te_status st = take_tensor_scale(a, q, s);
+  return st == TE_OK ? launch_block_quantize(a, s) : st;
 }
 
 // A packed tensor in the workspace, large enough for either 4-bit format.
@@ -98,7 +104,7 @@ te_status te_block_quantize(const void* x, te_dtype x_dtype, int64_t M, int64_t 
       !format_quantizer_ok(format, q) || !codes != !scales || !codes_t != !scales_t ||
       (!codes && !codes_t) || (M > 0 && !x))
     return TE_ERR_INVALID_ARG;
-  if (N % 32 || (codes_t && format == TE_MXFP8)) return TE_ERR_UNSUPPORTED;
+  if (N % (codes ? 32 : 16) || (codes_t && format == TE_MXFP8)) return TE_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(codes_t) ||
       !aligned16(scales_t))
     return TE_ERR_UNSUPPORTED;
@@ -180,9 +186,6 @@ te_status te_dense_fp4_fwd(const void* x, te_dtype dtype, const void* kernel,
       !aligned16(workspace) || !aligned4(kernel_scale_inv))
     return TE_ERR_UNSUPPORTED;
   if (M == 0) return TE_OK;
-  Carver c(workspace);
-  const Packed xq = take_packed(c, M, K);
-  if (!workspace || ws_bytes < c.used) return TE_ERR_WORKSPACE;
   cudaStream_t s = as_stream(stream);
   BlockQuantArgs a;
   a.x = x;
@@ -190,27 +193,36 @@ te_status te_dense_fp4_fwd(const void* x, te_dtype dtype, const void* kernel,
   a.M = M;
   a.N = K;
   a.fmt = format;
-  a.codes = xq.codes;
-  a.scales = xq.scales;
-  a.codes_t = saved_xt;
-  a.scales_t = saved_xt_scales;
-  const te_status st = block_quantize(a, q, s);
-  if (st != TE_OK) return st;
   BlockGemmArgs g;
-  g.A = xq.codes;
-  g.a_scales = xq.scales;
   g.B = kernel;
   g.b_scales = kernel_scales;
   g.fmt = format;
   g.M = M;
   g.N = N;
   g.K = K;
-  g.a_scale_inv = q ? q->scale_inv : nullptr;
   g.b_scale_inv = kernel_scale_inv;
   g.bias = bias;
   g.bias_dtype = dtype;
   g.D = out;
   g.d_dtype = dtype;
+  if (M <= kFewPacked && !saved_xt) {
+    const te_status st = take_tensor_scale(a, q, s);
+    if (st != TE_OK) return st;
+    g.b_ready = a.amax_in != nullptr;  // only the search for the amax precedes the product
+    return launch_block_gemm_packing(g, a, s);
+  }
+  Carver c(workspace);
+  const Packed xq = take_packed(c, M, K);
+  if (!workspace || ws_bytes < c.used) return TE_ERR_WORKSPACE;
+  a.codes = xq.codes;
+  a.scales = xq.scales;
+  a.codes_t = saved_xt;
+  a.scales_t = saved_xt_scales;
+  const te_status st = block_quantize(a, q, s);
+  if (st != TE_OK) return st;
+  g.A = xq.codes;
+  g.a_scales = xq.scales;
+  g.a_scale_inv = q ? q->scale_inv : nullptr;
   g.b_ready = 1;  // only the packing of x lies between the caller's work and this product
   return launch_block_gemm(g, s);
 }

@@ -139,7 +139,7 @@ inline int64_t pad32(int64_t n) { return (n + 31) / 32 * 32; }
 struct BlockQuantArgs {
   const void* x = nullptr;  // [M, N]
   int x_dtype = TE_BF16;
-  int64_t M = 0, N = 0;     // N a multiple of 32
+  int64_t M = 0, N = 0;     // N a multiple of 32 (16 without codes)
   int fmt = TE_MXFP4;
   void* codes = nullptr;    // [M, N] packed along N, or null
   void* scales = nullptr;
@@ -232,6 +232,11 @@ struct BlockGemmArgs {
   int b_ready = 0;
 };
 te_status launch_block_gemm(const BlockGemmArgs& a, cudaStream_t s);
+// The product with its A operand packed inside the kernel: x is q.x [M, K] with q's tensor scale
+// (q.codes and the other outputs unused), g.A, g.a_scales and g.a_scale_inv unset.  For rows up to
+// kFewPacked only (TE_ERR_UNSUPPORTED beyond).
+constexpr int64_t kFewPacked = 8;
+te_status launch_block_gemm_packing(const BlockGemmArgs& g, const BlockQuantArgs& q, cudaStream_t s);
 
 // Device status word (TE_OK or the first failure a kernel recorded).
 int* device_status_ptr();

@@ -413,7 +413,7 @@ size_t te_block_scale_bytes(te_block_format format, int64_t rows, int64_t cols);
  *       s = 2688 / amax (1 if amax is 0 or not finite, FLT_MAX if the quotient overflows) and
  *       writes *scale; both write scale_inv = 1 / s and amax (DELAYED: where not NULL; the largest
  *       magnitude, blocks with a NaN left out).
- * N must be a multiple of 32. */
+ * N must be a multiple of 32, or of 16 where only x^T is asked for. */
 te_status te_block_quantize(const void* x, te_dtype x_dtype, int64_t M, int64_t N,
                             te_block_format format, const te_quantizer* q, void* codes,
                             void* scales, void* codes_t, void* scales_t, void* stream);
@@ -442,7 +442,8 @@ te_status te_block_gemm(const void* A, const void* a_scales, const void* B, cons
  *   q   NVFP4: x's quantizer, scale_inv required.  MX: NULL.
  *   saved_xt, saved_xt_scales  NULL, or where x^T packed along the rows of x goes (codes_t,
  *       scales_t of te_block_quantize), for te_dense_fp4_bwd.
- *   workspace  te_workspace_size(TE_OP_DENSE_FP4_FWD, M, K, N, ...) bytes, 16-byte aligned.
+ *   workspace  te_workspace_size(TE_OP_DENSE_FP4_FWD, M, K, N, ...) bytes, 16-byte aligned; not
+ *       used, and may be NULL, for M up to 8 without saved_xt (the product packs x itself).
  * K a multiple of 32, N of 16. */
 te_status te_dense_fp4_fwd(const void* x, te_dtype dtype, const void* kernel,
                            const void* kernel_scales, te_block_format format,

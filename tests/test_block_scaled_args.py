@@ -49,7 +49,7 @@ def test_quantize_invalid(kw):
     assert quantize(**kw) == b.TE_ERR_INVALID_ARG
 
 
-@pytest.mark.parametrize("kw", [dict(N=48), dict(x=ODD), dict(c=ODD), dict(s=ODD), dict(ct=ODD, st=P),
+@pytest.mark.parametrize("kw", [dict(N=48), dict(N=40, c=None, s=None, ct=P, st=P), dict(x=ODD), dict(c=ODD), dict(s=ODD), dict(ct=ODD, st=P),
                                 dict(f=b.TE_MXFP8, ct=P, st=P)])
 def test_quantize_unsupported(kw):
     assert quantize(**kw) == b.TE_ERR_UNSUPPORTED
@@ -92,7 +92,8 @@ def test_dense_refusals():
         assert fwd(**kw) == b.TE_ERR_INVALID_ARG, kw
     for kw in (dict(fmt=b.TE_MXFP8), dict(K=48), dict(N=24), dict(x=ODD), dict(xt=ODD, xts=P), dict(ws=ODD)):
         assert fwd(**kw) == b.TE_ERR_UNSUPPORTED, kw
-    assert fwd(ws=None) == b.TE_ERR_WORKSPACE and fwd(n=100) == b.TE_ERR_WORKSPACE
+    assert fwd(M=9, ws=None) == b.TE_ERR_WORKSPACE and fwd(M=9, n=100) == b.TE_ERR_WORKSPACE
+    assert fwd(xt=P, xts=P, ws=None) == b.TE_ERR_WORKSPACE
     assert fwd(M=0) == b.TE_OK
 
     def bwd(dy=P, dw=P, fmt=b.TE_MXFP4, q=None, M=4, K=64, N=64, db=None, ws=P, n=big):

@@ -288,6 +288,48 @@ def test_dense_forward_and_backward_together(fmt, mode, M, K, N, dtype):
     assert (np.abs(f64(db) - ds.sum(0)) <= (M + 4) * 2.0 ** -24 * np.abs(ds).sum(0)).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt,mode", [("mxfp4", None), ("nvfp4", "current"), ("nvfp4", "delayed")])
+@pytest.mark.parametrize("M,K,N", [(1, 32, 16), (1, 4096, 320), (3, 544, 128), (8, 4128, 2064), (9, 96, 400), (17, 1056, 144),
+                                   (33, 4096, 256), (40, 288, 2064), (64, 800, 176), (65, 800, 176)])
+def test_dense_forward_alone(fmt, mode, dtype, M, K, N):
+    """Up to 8 rows the product packs x itself; the row past the last is left as it was, a row with a
+    NaN spoils no other, and the result does not vary."""
+    x = draw(M, K, dtype, 1, spread=mode is None)
+    w = draw(K, N, torch.float32, 3, std=0.05, spread=False)
+    bias = draw(1, N, dtype, 4, spread=False)[0].contiguous()
+    q = None if mode is None else te.Quantizer(scale=500.0, mode=mode)
+    qw = None if mode is None else te.Quantizer(mode="current")
+    wct, wst = te.block_empty(fmt, N, K)
+    te.te_block_quantize(w, fmt, codes_t=wct, scales_t=wst, q=qw)
+    out = torch.full((M + 1, N), 7.0, dtype=dtype, device=DEV)
+    call = lambda o: te.te_dense_fp4_fwd(x, wct, wst, o, fmt, bias=bias, q=q,
+                                         kernel_scale_inv=None if qw is None else qw.scale_inv)
+    call(out[:M])
+    again = call(torch.empty(M, N, dtype=dtype, device=DEV))
+    torch.cuda.synchronize()
+    assert te.get_device_status() == 0
+    assert torch.equal(out[:M], again) and (out[M] == 7.0).all()
+    xs, wv = f64(x), f64(w)
+    sx = sw = None
+    alpha = 1.0
+    if mode is not None:
+        sx = bs.nv_scale(np.abs(xs).max()) if mode == "current" else np.float32(500)
+        sw = bs.nv_scale(np.abs(wv).max())
+        alpha = float(np.float32(1) / sx) * float(np.float32(1) / sw)
+        assert np.float32(q.scale.item()) == sx and np.float32(q.scale_inv.item()) == np.float32(1) / sx
+        assert q.amax.item() == np.float32(np.abs(xs).max())
+    a, b = values(xs, fmt, sx), values(wv.T, fmt, sw)
+    want = alpha * (a @ b.T) + f64(bias)
+    tol = product_bound(a, b, alpha, want, K, dtype) + 2.0 ** -22 * np.abs(f64(bias))
+    err = np.abs(f64(out[:M]) - want)
+    assert (err <= tol).all(), (float((err / tol).max()), np.argwhere(err > tol)[:4])
+    if mode != "current":
+        x[M - 1, K // 2] = float("nan")
+        bad = torch.isnan(call(out[:M]))
+        assert bad[M - 1].all() and not bad[:M - 1].any()
+
+
 def test_dense_without_tokens():
     fmt = "mxfp4"
     x = torch.empty(0, 64, dtype=torch.bfloat16, device=DEV)
