@@ -68,16 +68,33 @@ struct BlockScale {
   bool bad;  // the block holds an infinity or a NaN
 };
 
+// t / 6 rounded as division rounds it, by Markstein's method (a quotient from the rounded
+// reciprocal, corrected once by its exact remainder), for 0 <= t <= 2^100; below 2^-100 the result is
+// only near, which its rounding to E4M3 does not see.
+__device__ __forceinline__ float sixth(float t) {
+  constexpr float y = 1.0f / 6.0f;
+  const float q = t * y;
+  return fmaf(fmaf(-6.0f, q, t), y, q);
+}
+
+// NVFP4's factors fp32(s / scale) by the scale's byte, made once by the threads of a CTA (a division
+// a block costs as much as the rest of its packing).  Entry 0 is 0: such a block holds zeros.
+constexpr int kNvFactors = 128;
+__device__ __forceinline__ void nv_factors(float* table, float s, int thread, int threads) {
+  for (int i = thread; i < kNvFactors; i += threads)
+    table[i] = i == 0 || i == 0x7f ? 0.0f : __fdiv_rn(s, unpack_e4m3x2(uint16_t(i)).x);
+}
+
+// factors: nv_factors' table of s (NVFP4 only).
 template <int FMT>
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float s) {
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float s, const float* factors) {
   BlockScale r;
   r.bad = amax_bits >= kInfBits;
   if constexpr (FMT == TE_NVFP4) {
-    const float t = __fdiv_rn(__fmul_rn(__uint_as_float(amax_bits), s), 6.0f);
-    const uint32_t sb = pack_e4m3x2(t, 0.0f) & 0xffu;
-    const float sf = unpack_e4m3x2(uint16_t(sb)).x;
+    const float t = fminf(__fmul_rn(__uint_as_float(amax_bits), s), 65536.0f);  // saturates far below
+    const uint32_t sb = pack_e4m3x2(sixth(t), 0.0f) & 0xffu;
     r.byte = r.bad ? 0x7fu : sb;
-    r.mul = sb ? __fdiv_rn(s, sf) : 0.0f;
+    r.mul = factors[sb];
   } else {
     // 6 = 1.5 * 2^2 and 448 = 1.75 * 2^8: one more when the mantissa is above the top's
     constexpr int kTopExp = FMT == TE_MXFP4 ? 2 : 8;

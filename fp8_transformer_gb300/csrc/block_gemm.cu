@@ -677,12 +677,15 @@ __global__ void __launch_bounds__(kFewThreads, 2)
   const uint32_t tmem = *tmem_slot;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float tensor_scale = 1.0f;  // of the tokens packed here
+  __shared__ float factors[kPack && FMT == TE_NVFP4 ? kNvFactors : 1];
   if constexpr (kPack && FMT == TE_NVFP4) {
     tensor_scale = p.q.amax_in ? nv_scale_from_amax(*p.q.amax_in) : *p.q.scale;
     if (blockIdx.x == 0 && threadIdx.x == 0) {
       if (p.q.scale_out) *p.q.scale_out = tensor_scale;
       if (p.q.scale_inv_out) *p.q.scale_inv_out = __fdiv_rn(1.0f, tensor_scale);
     }
+    nv_factors(factors, tensor_scale, int(threadIdx.x), kFewThreads);
+    __syncthreads();
   }
 
   if (warp == 0) {
@@ -765,7 +768,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
           m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
           if constexpr (kBlk == 32) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
           amax = max(amax, m <= kInfBits ? m : 0u);
-          const BlockScale b = block_scale<FMT>(m, tensor_scale);
+          const BlockScale b = block_scale<FMT>(m, tensor_scale, factors);
           float v[8];
           e[r].get(v);
           *reinterpret_cast<uint32_t*>(codes + r * kRowBytes + (((lane >> 2) ^ (r & 7)) << 4)) = codes8<FMT>(v, b).x;

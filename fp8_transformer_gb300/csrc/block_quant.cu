@@ -18,23 +18,42 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kTileRows = 128;
 
-// One element of a tile held in shared memory, columns c (and c + 1 for bf16) of row r.
+// 32 rows of a tile held in shared memory, of the kCols neighbouring columns that a thread walks.
 template <typename T>
-struct Column;  // kCols columns a thread walks at once
+struct Strip;
 template <>
-struct Column<__nv_bfloat16> {
+struct Strip<__nv_bfloat16> {
   static constexpr int kCols = 2;
-  __device__ __forceinline__ static void get(const uint8_t* p, float (&v)[2]) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(p);
-    v[0] = bf16_lo(w);
-    v[1] = bf16_hi(w);
+  uint32_t w[32];  // both columns of a row
+  __device__ __forceinline__ void load(const uint8_t* p, int pitch) {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) w[r] = *reinterpret_cast<const uint32_t*>(p + r * pitch);
+  }
+  __device__ __forceinline__ float at(int k, int r) const { return k ? bf16_hi(w[r]) : bf16_lo(w[r]); }
+  // bits of the largest magnitudes of rows [r0, r0 + N), one a column
+  template <int N>
+  __device__ __forceinline__ void amax_bits(int r0, uint32_t (&m)[2]) const {
+    uint32_t t = 0;
+#pragma unroll
+    for (int r = 0; r < N; ++r) t = __vmaxu2(t, w[r0 + r] & 0x7fff7fffu);
+    m[0] = t << 16;
+    m[1] = t & 0xffff0000u;
   }
 };
 template <>
-struct Column<float> {
+struct Strip<float> {
   static constexpr int kCols = 1;
-  __device__ __forceinline__ static void get(const uint8_t* p, float (&v)[1]) {
-    v[0] = *reinterpret_cast<const float*>(p);
+  float v[32];
+  __device__ __forceinline__ void load(const uint8_t* p, int pitch) {
+#pragma unroll
+    for (int r = 0; r < 32; ++r) v[r] = *reinterpret_cast<const float*>(p + r * pitch);
+  }
+  __device__ __forceinline__ float at(int, int r) const { return v[r]; }
+  template <int N>
+  __device__ __forceinline__ void amax_bits(int r0, uint32_t (&m)[1]) const {
+    m[0] = 0;
+#pragma unroll
+    for (int r = 0; r < N; ++r) m[0] = max(m[0], __float_as_uint(v[r0 + r]) & 0x7fffffffu);
   }
 };
 
@@ -46,21 +65,27 @@ __host__ __device__ constexpr int tile_pitch() { return kColTile * int(sizeof(T)
 template <typename T>
 __host__ __device__ constexpr size_t col_smem() { return size_t(kTileRows) * tile_pitch<T>() + kColTile * kStagePitch; }
 
+// Threads of a CTA: for tiles packed along their columns a strip of 32 rows each.
+template <typename T, bool COL>
+__host__ __device__ constexpr int quant_threads() { return COL && sizeof(T) == 4 ? 512 : kThreads; }
+
 // TC: columns of a tile (256 when only the rows are packed, for whole 128-byte runs of codes).
 // SUB: rows of the tile that a CTA takes, 128, or 32 (rows only) so that few rows still occupy many
 // SMs; such a CTA writes the 4 bytes of each 16 of a scale tile that are its rows'.
 template <typename T, int FMT, int TC, bool COL, int SUB>
-__global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs a) {
+__global__ void __launch_bounds__(quant_threads<T, COL>()) block_quantize_kernel(BlockQuantArgs a) {
+  constexpr int THREADS = quant_threads<T, COL>();
   static_assert(SUB == kTileRows || (SUB == 32 && !COL), "rows of a CTA");
   constexpr int kBlk = block_len(FMT);
   constexpr int kLanes = TC / 8;                 // lanes on one row
-  constexpr int kRowsPass = kThreads / kLanes;   // rows a CTA takes at a time
+  constexpr int kRowsPass = THREADS / kLanes;   // rows a CTA takes at a time
   constexpr int kPasses = SUB / kRowsPass;
   constexpr int kBatch = 4;                      // passes whose loads are in flight together
   constexpr int kScaleBytes = kTileRows * (TC / kBlk);
   __shared__ __align__(16) uint8_t rs[kScaleBytes];
   __shared__ __align__(16) uint8_t cs[COL ? kScaleBytes : 16];
   __shared__ float sums[COL ? 4 : 1][COL ? kColTile : 1];
+  __shared__ float factors[FMT == TE_NVFP4 ? kNvFactors : 1];
   extern __shared__ __align__(16) uint8_t dyn[];
   // the kernel after this one may launch its setup now (it waits for this grid's completion)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -71,6 +96,8 @@ __global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs
       if (a.scale_out) *a.scale_out = s;
       if (a.scale_inv_out) *a.scale_inv_out = __fdiv_rn(1.0f, s);
     }
+    nv_factors(factors, s, int(threadIdx.x), THREADS);
+    __syncthreads();
   }
   const int64_t tiles_c = (a.N + TC - 1) / TC;
   const int64_t st = blockIdx.x / tiles_c, ct = blockIdx.x % tiles_c;
@@ -104,7 +131,7 @@ __global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs
       amax = max(amax, m <= kInfBits ? m : 0u);  // blocks with a NaN left out
       if (!COL || a.codes) {
         const bool in = col_ok && r0 + r < a.M;
-        BlockScale b = block_scale<FMT>(m, s);
+        BlockScale b = block_scale<FMT>(m, s, factors);
         if (in) {
           float v[8];
           e[j].get(v);
@@ -124,56 +151,50 @@ __global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs
     const int n = int(min(int64_t(kScaleBytes), (groups - g0) * 512));
     uint8_t* dst = static_cast<uint8_t*>(a.scales) + (rt * groups + g0) * 512;
     if constexpr (SUB == kTileRows) {
-      for (int i = int(threadIdx.x) * 16; i < n; i += kThreads * 16)
+      for (int i = int(threadIdx.x) * 16; i < n; i += THREADS * 16)
         *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(rs + i);
     } else {  // the rows r % 32 lie in words 0, 4, 8, ... of rs
-      for (int i = int(threadIdx.x) * 16; i < n; i += kThreads * 16)
+      for (int i = int(threadIdx.x) * 16; i < n; i += THREADS * 16)
         *reinterpret_cast<uint32_t*>(dst + i + sub * 4) = *reinterpret_cast<const uint32_t*>(rs + i);
     }
   }
   if constexpr (COL) {
-    constexpr int kC = Column<T>::kCols;
+    constexpr int kC = Strip<T>::kCols;
     uint8_t* stage = dyn + kTileRows * tile_pitch<T>();
-    // (column(s), 32 rows) for every thread; fp32 takes two turns
-    for (int u = int(threadIdx.x); u < kColTile / kC * 4; u += kThreads) {
-      const int c = u % (kColTile / kC) * kC, rb = u / (kColTile / kC);
-      const uint8_t* src = tile + rb * 32 * tile_pitch<T>() + c * int(sizeof(T));
-      float v[kC][32];
-#pragma unroll
-      for (int r = 0; r < 32; ++r) {
-        float w[kC];
-        Column<T>::get(src + r * tile_pitch<T>(), w);
-#pragma unroll
-        for (int k = 0; k < kC; ++k) v[k][r] = w[k];
-      }
+    // (column(s), 32 rows) for every thread
+    static_assert(kColTile / kC * 4 == THREADS, "one strip a thread");
+    const int c = int(threadIdx.x) % (kColTile / kC) * kC, rb = int(threadIdx.x) / (kColTile / kC);
+    Strip<T> v;
+    v.load(tile + rb * 32 * tile_pitch<T>() + c * int(sizeof(T)), tile_pitch<T>());
+    const bool rows_in = r0 + rb * 32 < a.M;
+    if (a.partials) {
 #pragma unroll
       for (int k = 0; k < kC; ++k) {
-        if (a.partials) {
-          float t = 0.0f;
+        float t = 0.0f;
 #pragma unroll
-          for (int r = 0; r < 32; ++r) t += v[k][r];
-          sums[rb][c + k] = t;
+        for (int r = 0; r < 32; ++r) t += v.at(k, r);
+        sums[rb][c + k] = t;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 32 / kBlk; ++h) {
+      uint32_t m[kC];
+      v.template amax_bits<kBlk>(h * kBlk, m);
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        const BlockScale b = block_scale<FMT>(m[k], s, factors);
+        cs[scale_offset(c + k, rb * (32 / kBlk) + h)] = rows_in && c0 + c + k < a.N ? uint8_t(b.byte) : uint8_t(0);
+        uint32_t q[kBlk / 8];
+#pragma unroll
+        for (int g = 0; g < kBlk / 8; ++g) {
+          float w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) w[i] = v.at(k, h * kBlk + g * 8 + i);
+          q[g] = codes8<FMT>(w, b).x;
         }
-        const bool in = c0 + c + k < a.N && r0 + rb * 32 < a.M;
-#pragma unroll
-        for (int h = 0; h < 32 / kBlk; ++h) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int r = 0; r < kBlk; ++r) m = max(m, __float_as_uint(v[k][h * kBlk + r]) & 0x7fffffffu);
-          const BlockScale b = block_scale<FMT>(m, s);
-          cs[scale_offset(c + k, rb * (32 / kBlk) + h)] = in ? uint8_t(b.byte) : uint8_t(0);
-          uint32_t q[kBlk / 8];
-#pragma unroll
-          for (int g = 0; g < kBlk / 8; ++g) {
-            float w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) w[i] = v[k][h * kBlk + g * 8 + i];
-            q[g] = codes8<FMT>(w, b).x;
-          }
-          uint8_t* d = stage + (c + k) * kStagePitch + rb * 16 + h * 8;
-          if constexpr (kBlk == 32) *reinterpret_cast<uint4*>(d) = make_uint4(q[0], q[1], q[2], q[3]);
-          else *reinterpret_cast<uint2*>(d) = make_uint2(q[0], q[1]);
-        }
+        uint8_t* d = stage + (c + k) * kStagePitch + rb * 16 + h * 8;
+        if constexpr (kBlk == 32) *reinterpret_cast<uint4*>(d) = make_uint4(q[0], q[1], q[2], q[3]);
+        else *reinterpret_cast<uint2*>(d) = make_uint2(q[0], q[1]);
       }
     }
     __syncthreads();
@@ -182,17 +203,17 @@ __global__ void __launch_bounds__(kThreads) block_quantize_kernel(BlockQuantArgs
     const int64_t g0 = r0 / kBlk / 4;
     const int n = int(min(int64_t(kScaleBytes), (groups - g0) * 512));
     uint8_t* dst = static_cast<uint8_t*>(a.scales_t) + (ct * groups + g0) * 512;
-    for (int i = int(threadIdx.x) * 16; i < n; i += kThreads * 16)
+    for (int i = int(threadIdx.x) * 16; i < n; i += THREADS * 16)
       *reinterpret_cast<uint4*>(dst + i) = *reinterpret_cast<const uint4*>(cs + i);
     // 16 bytes of codes (32 rows) for each of 4 lanes on a transposed row
-    for (int u = int(threadIdx.x); u < kColTile * 4; u += kThreads) {
+    for (int u = int(threadIdx.x); u < kColTile * 4; u += THREADS) {
       const int c = u / 4, rb = u % 4;
       if (c0 + c < a.N && r0 + rb * 32 < mp)
         *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.codes_t) + ((c0 + c) * mp + r0) / 2 + rb * 16) =
             *reinterpret_cast<const uint4*>(stage + c * kStagePitch + rb * 16);
     }
     if (a.partials)
-      for (int c = int(threadIdx.x); c < kColTile; c += kThreads)
+      for (int c = int(threadIdx.x); c < kColTile; c += THREADS)
         if (c0 + c < a.N)
           a.partials[rt * a.N + c0 + c] = ((sums[0][c] + sums[1][c]) + sums[2][c]) + sums[3][c];
   }
@@ -223,7 +244,8 @@ te_status launch_quant_t(const BlockQuantArgs& a, cudaStream_t s) {
           return *v;
         }))
       return TE_ERR_CUDA;
-    block_quantize_kernel<T, FMT, kColTile, true, kTileRows><<<unsigned(tiles), kThreads, col_smem<T>(), s>>>(a);
+    block_quantize_kernel<T, FMT, kColTile, true, kTileRows>
+        <<<unsigned(tiles), quant_threads<T, true>(), col_smem<T>(), s>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? TE_OK : TE_ERR_CUDA;
 }
