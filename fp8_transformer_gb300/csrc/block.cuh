@@ -128,10 +128,17 @@ struct Eight<__nv_bfloat16> {
     v[0] = bf16_lo(u.x); v[1] = bf16_hi(u.x); v[2] = bf16_lo(u.y); v[3] = bf16_hi(u.y);
     v[4] = bf16_lo(u.z); v[5] = bf16_hi(u.z); v[6] = bf16_lo(u.w); v[7] = bf16_hi(u.w);
   }
+  // the largest magnitude, NaN ignored
+  __device__ __forceinline__ float amax() const {
+    auto abs2 = [](uint32_t w) { return __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)); };
+    const __nv_bfloat162 t = __hmax2(__hmax2(abs2(u.x), abs2(u.y)), __hmax2(abs2(u.z), abs2(u.w)));
+    return fmaxf(__low2float(t), __high2float(t));
+  }
+  // its bits, those of a NaN above all others
   __device__ __forceinline__ uint32_t amax_bits() const {
     constexpr uint32_t k = 0x7fff7fffu;
     const uint32_t m = __vmaxu2(__vmaxu2(u.x & k, u.y & k), __vmaxu2(u.z & k, u.w & k));
-    return max(m & 0xffffu, m >> 16) << 16;
+    return max(m << 16, m & 0xffff0000u);
   }
 };
 template <>
@@ -150,6 +157,11 @@ struct Eight<float> {
     v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z);
     v[3] = __uint_as_float(a.w); v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
     v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+  }
+  __device__ __forceinline__ float amax() const {
+    auto f = [](uint32_t w) { return fabsf(__uint_as_float(w)); };
+    return fmaxf(fmaxf(fmaxf(f(a.x), f(a.y)), fmaxf(f(a.z), f(a.w))),
+                 fmaxf(fmaxf(f(b.x), f(b.y)), fmaxf(f(b.z), f(b.w))));
   }
   __device__ __forceinline__ uint32_t amax_bits() const {
     constexpr uint32_t k = 0x7fffffffu;
