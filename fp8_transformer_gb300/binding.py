@@ -49,7 +49,8 @@ EXPORTED = ["te_status_string", "te_version", "te_get_device_status", "te_worksp
             "te_dact_dbias_noalloc_capacity", "te_selftest_wait_timeout",
             "te_layernorm_mlp_fwd_host", "te_update_scales", "te_stream_probe",
             "te_block_scale_bytes", "te_block_quantize", "te_block_dequantize", "te_block_gemm",
-            "te_dense_fp4_fwd", "te_dense_fp4_bwd", "te_dact_dbias_ckpt"]
+            "te_dense_fp4_fwd", "te_dense_fp4_bwd", "te_dact_dbias_ckpt",
+            "te_layernorm_mlp_fwd_ckpt", "te_layernorm_mlp_bwd_ckpt"]
 KERNEL_KINDS = ["norm_fwd", "quantize", "act_lu", "dact_dbias", "gemm", "gemm_act", "norm_bwd",
                 "transpose"]
 
@@ -138,6 +139,10 @@ _SIGS = {
     "te_dact_dbias_ckpt": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int, _i64, _i64, ctypes.c_int,
                                           _QP, _vp, ctypes.c_int, _vp, _vp, _vp, _sz, _vp]),
 }
+# the checkpoint forms have two pointers (codes, scales) in the place of saved_h
+for _name, _at in (("te_layernorm_mlp_fwd", 17), ("te_layernorm_mlp_bwd", 6)):
+    _res, _args = _SIGS[_name]
+    _SIGS[_name + "_ckpt"] = (_res, _args[:_at] + [_vp] + _args[_at:])
 
 
 def lib_path() -> str:
@@ -735,4 +740,56 @@ def te_dact_dbias_ckpt(dy, codes, scales, act, dx, dbias=None, act_out=None, q=N
     st = lib().te_dact_dbias_ckpt(py, pc, ps, _dt(dy), M, N_in, a, _qp(q), px, _dt(dx), pa, pb, pws, nws,
                                   _stream(stream))
     _check("te_dact_dbias_ckpt", st)
+    return dx
+
+
+def te_layernorm_mlp_fwd_ckpt(x, gamma, beta, kernel1, kernel2, bias1, bias2, out, h_codes, h_scales,
+                              norm_type="layernorm", zero_centered_gamma=False, epsilon=1e-6,
+                              activation_type=("relu",), quantizer_set=None, saved_ln_out=None, mu=None,
+                              rsigma=None, workspace=None, stream=None, saved_act=None):
+    """te_layernorm_mlp_fwd that keeps the activation's input as an 8-bit checkpoint (h_codes, h_scales:
+    block_empty("mxfp8", M, F')) for te_layernorm_mlp_bwd_ckpt."""
+    M, H = x.shape
+    F = kernel2.shape[0]
+    act, dt, kd, dev = _act_id(activation_type), _dt(x), _dt(kernel1), torch.cuda.current_device()
+    pc, ps = _packed("h_codes", h_codes, h_scales, TE_MXFP8, M, 2 * F if act >= TE_SWIGLU else F, dev)
+    if workspace is None:
+        workspace = _ws(workspace_size(TE_OP_LAYERNORM_MLP_FWD, M, H, F, dt, quantizer_set is not None, kd, act),
+                        x.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    qs = quantizer_set.c() if quantizer_set is not None else None
+    st = lib().te_layernorm_mlp_fwd_ckpt(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(kernel1), _ptr(kernel2), kd,
+                                         _ptr(bias1), _ptr(bias2), _norm_id(norm_type),
+                                         int(bool(zero_centered_gamma)), float(epsilon), act,
+                                         ctypes.byref(qs) if qs is not None else None, M, H, F, dt, _ptr(out),
+                                         pc, ps, _ptr(saved_act), _ptr(saved_ln_out), _ptr(mu), _ptr(rsigma),
+                                         _ptr(workspace), workspace.numel(), _stream(stream))
+    _check("te_layernorm_mlp_fwd_ckpt", st)
+    return out
+
+
+def te_layernorm_mlp_bwd_ckpt(dy, x, gamma, kernel1, kernel2, h_codes, h_scales, saved_ln_out, mu, rsigma, dx,
+                              dgamma, dkernel1, dkernel2, dbeta=None, dbias1=None, dbias2=None,
+                              norm_type="layernorm", zero_centered_gamma=False, activation_type=("relu",),
+                              quantizer_set=None, workspace=None, stream=None, saved_dh=None):
+    """te_layernorm_mlp_bwd from the 8-bit checkpoint that te_layernorm_mlp_fwd_ckpt wrote."""
+    M, H = x.shape
+    F = kernel2.shape[0]
+    act, dt, kd, dev = _act_id(activation_type), _dt(x), _dt(kernel1), torch.cuda.current_device()
+    pc, ps = _packed("h_codes", h_codes, h_scales, TE_MXFP8, M, 2 * F if act >= TE_SWIGLU else F, dev)
+    if workspace is None:
+        workspace = _ws(workspace_size(TE_OP_LAYERNORM_MLP_BWD, M, H, F, dt, quantizer_set is not None, kd, act),
+                        x.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    qs = quantizer_set.c() if quantizer_set is not None else None
+    st = lib().te_layernorm_mlp_bwd_ckpt(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(kernel1), _ptr(kernel2), kd, pc, ps,
+                                         _ptr(saved_ln_out), _ptr(mu), _ptr(rsigma), _norm_id(norm_type),
+                                         int(bool(zero_centered_gamma)), act,
+                                         ctypes.byref(qs) if qs is not None else None, M, H, F, dt, _ptr(dx),
+                                         _ptr(dgamma), _ptr(dbeta), _ptr(dkernel1), _ptr(dkernel2), _ptr(dbias1),
+                                         _ptr(dbias2), _ptr(saved_dh), _ptr(workspace), workspace.numel(),
+                                         _stream(stream))
+    _check("te_layernorm_mlp_bwd_ckpt", st)
     return dx

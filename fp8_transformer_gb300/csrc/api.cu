@@ -163,6 +163,383 @@ te_status quantize_into(const void* x, int dtype, int64_t n, const te_quantizer*
   });
 }
 
+// What the forward keeps of GEMM1's output for the backward: [M, F'] in dtype, or an 8-bit checkpoint.
+struct MlpPreact {
+  void* saved = nullptr;
+  void* codes = nullptr;
+  void* scales = nullptr;
+};
+
+te_status mlp_fwd(const void* x, const void* gamma, const void* beta,
+                  const void* kernel1, const void* kernel2, te_dtype kernel_dtype,
+                  const void* bias1, const void* bias2, te_norm_type norm_type,
+                  int zero_centered_gamma, float epsilon, te_act_type act,
+                  const te_quantizer_set* qset, int64_t M, int64_t H, int64_t F,
+                  te_dtype dtype, void* out, const MlpPreact& h, void* saved_act,
+                  void* saved_ln_out, float* mu, float* rsigma, void* workspace,
+                  size_t ws_bytes, void* stream) {
+  if (M < 0 || H <= 0 || F <= 0 || !is_act_dtype(dtype) || act == TE_IDENTITY ||
+      !valid_act(act) || (norm_type != TE_LAYERNORM && norm_type != TE_RMSNORM))
+    return TE_ERR_INVALID_ARG;
+  const bool quant = qset != nullptr;
+  if (quant) {
+    if (!enabled(&qset->x) || !enabled(&qset->act) || !quantizer_ok(&qset->x) ||
+        !quantizer_ok(&qset->act) || !quantizer_ok(&qset->kernel1) || !quantizer_ok(&qset->kernel2))
+      return TE_ERR_INVALID_ARG;
+    if (kernel_dtype == TE_E4M3
+            ? (!qset->kernel1.scale_inv || !qset->kernel2.scale_inv)
+            : (kernel_dtype != dtype || !enabled(&qset->kernel1) || !enabled(&qset->kernel2)))
+      return TE_ERR_INVALID_ARG;
+  } else if (kernel_dtype != dtype) {
+    return TE_ERR_INVALID_ARG;
+  }
+  if (M > 0 && (!x || !gamma || !kernel1 || !kernel2 || !out)) return TE_ERR_INVALID_ARG;
+  if (H % 16 || F % (h.codes ? 32 : 16) || H * int64_t(esize(dtype)) > 16384) return TE_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(gamma) || !opt_aligned16(beta) || !aligned16(kernel1) ||
+      !aligned16(kernel2) || !opt_aligned16(bias1) || !opt_aligned16(bias2) || !aligned16(out) ||
+      !opt_aligned16(h.saved) || !opt_aligned16(h.codes) || !opt_aligned16(h.scales) || !opt_aligned16(saved_act) || !opt_aligned16(saved_ln_out) ||
+      !aligned16(workspace) || !aligned4(mu) || !aligned4(rsigma))
+    return TE_ERR_UNSUPPORTED;
+  if (M == 0) return TE_OK;
+  const bool gated = is_gated(act);
+  const int64_t F1 = gated ? 2 * F : F;
+  FwdLayout L = mlp_layout(workspace, M, H, F, dtype, quant, kernel_dtype, act,
+                           saved_ln_out != nullptr);
+  if (!workspace || ws_bytes < L.split.required) return TE_ERR_WORKSPACE;
+  cudaStream_t s = as_stream(stream);
+  void* ln = saved_ln_out ? saved_ln_out : L.ln;
+  void* a2 = saved_act ? saved_act : L.a2;  // GEMM2's A operand
+  // The activation's amax (GEMM1's epilogue accumulates into it) is zeroed before the norm rather
+  // than between the norm and GEMM1, where the memset would keep GEMM1 from launching as the
+  // norm's programmatic dependent; unless it shares storage with an amax written before GEMM1.
+  const bool act_zero_first =
+      quant && qset->act.amax && qset->act.amax != qset->x.amax &&
+      (kernel_dtype == TE_E4M3 ||
+       (qset->act.amax != qset->kernel1.amax && qset->act.amax != qset->kernel2.amax));
+  // the places of a scale tile that the checkpoint does not have are zero
+  if (h.codes && (M % 128 || F1 % 128) &&
+      cudaMemsetAsync(h.scales, 0, block_scale_bytes(TE_MXFP8, M, F1), s) != cudaSuccess)
+    return TE_ERR_CUDA;
+  te_status st = act_zero_first ? zero_scalar(qset->act.amax, s) : TE_OK;
+  if (st != TE_OK) return st;
+  // (1) normalization, written once in GEMM1's operand dtype
+  st = norm_into(x, dtype, M, H, gamma, beta, norm_type, zero_centered_gamma, epsilon,
+                 quant ? &qset->x : nullptr, ln, quant ? TE_E4M3 : dtype, mu, rsigma, s);
+  if (st != TE_OK) return st;
+  const void* w1 = kernel1;
+  const void* w2 = kernel2;
+  int b_kmajor = 0;
+  if (quant && kernel_dtype != TE_E4M3) {
+    st = quantize_into(kernel1, dtype, H * F1, &qset->kernel1, L.kq1, s);
+    if (st != TE_OK) return st;
+    st = quantize_into(kernel2, dtype, F * H, &qset->kernel2, L.kq2, s);
+    if (st != TE_OK) return st;
+    w1 = L.kq1;
+    w2 = L.kq2;
+  } else if (!quant && dtype == TE_F32) {
+    st = launch_transpose_f32(static_cast<const float*>(kernel1), H, F1, static_cast<float*>(L.kt1), s);
+    if (st != TE_OK) return st;
+    st = launch_transpose_f32(static_cast<const float*>(kernel2), F, H, static_cast<float*>(L.kt2), s);
+    if (st != TE_OK) return st;
+    w1 = L.kt1;
+    w2 = L.kt2;
+    b_kmajor = 1;
+  }
+  // (2)+(3) GEMM1 + bias1 -> round -> activation [-> amax, E4M3], one kernel
+  GemmArgs g1;
+  g1.A = ln;
+  g1.B = w1;
+  g1.ab_dtype = quant ? TE_E4M3 : dtype;
+  g1.a_kmajor = 1;
+  g1.b_kmajor = b_kmajor;
+  g1.M = M;
+  g1.N = F1;
+  g1.K = H;
+  g1.a_scale_inv = quant ? qset->x.scale_inv : nullptr;
+  g1.b_scale_inv = quant ? qset->kernel1.scale_inv : nullptr;
+  g1.epilogue = gated ? EPI_BIAS_GATED : EPI_BIAS_ACT;
+  g1.act = act;
+  g1.bias = bias1;
+  g1.bias_dtype = dtype;
+  g1.h_dtype = dtype;
+  g1.saved_h = h.saved;
+  g1.h_codes = h.codes;
+  g1.h_scales = h.scales;
+  const bool act_current = quant && qset->act.mode == TE_SCALING_CURRENT;
+  if (quant) {
+    if (!act_zero_first) {
+      st = zero_scalar(qset->act.amax, s);
+      if (st != TE_OK) return st;
+    }
+    g1.cast.amax_out = qset->act.amax;
+    if (act_current) {
+      g1.D = L.a2_hi;
+      g1.cast.out_dtype = TE_F32;
+    } else {
+      g1.D = a2;
+      g1.cast.out_dtype = TE_E4M3;
+      g1.cast.scale = qset->act.scale;
+      g1.cast.scale_inv_out = qset->act.scale_inv;
+    }
+  } else {
+    g1.D = a2;
+    g1.cast.out_dtype = dtype;
+  }
+  give_split(g1, L.split, workspace, ws_bytes);
+  st = launch_gemm(g1, s);
+  if (st != TE_OK) return st;
+  if (act_current) {
+    // The amax is already known from GEMM1's epilogue: one cast pass.
+    QuantizeArgs qa;
+    qa.x = L.a2_hi;
+    qa.x_dtype = TE_F32;
+    qa.n = M * F;
+    qa.out = a2;
+    qa.cast.out_dtype = TE_E4M3;
+    qa.cast.amax_in = qset->act.amax;
+    qa.cast.scale_out = qset->act.scale;
+    qa.cast.scale_inv_out = qset->act.scale_inv;
+    st = launch_quantize(qa, s);
+    if (st != TE_OK) return st;
+  }
+  // (4) GEMM2 + bias2
+  GemmArgs g2;
+  g2.A = a2;
+  g2.B = w2;
+  g2.ab_dtype = quant ? TE_E4M3 : dtype;
+  g2.a_kmajor = 1;
+  g2.b_kmajor = b_kmajor;
+  g2.M = M;
+  g2.N = H;
+  g2.K = F;
+  g2.a_scale_inv = quant ? qset->act.scale_inv : nullptr;
+  g2.b_scale_inv = quant ? qset->kernel2.scale_inv : nullptr;
+  g2.epilogue = EPI_BIAS;
+  g2.bias = bias2;
+  g2.bias_dtype = dtype;
+  g2.D = out;
+  g2.cast.out_dtype = dtype;
+  give_split(g2, L.split, workspace, ws_bytes);
+  return launch_gemm(g2, s);
+}
+
+te_status mlp_bwd(const void* dy, const void* x, const void* gamma,
+                  const void* kernel1, const void* kernel2, te_dtype kernel_dtype,
+                  const MlpPreact& h, const void* saved_ln_out, const float* mu,
+                  const float* rsigma, te_norm_type norm_type,
+                  int zero_centered_gamma, te_act_type act,
+                  const te_quantizer_set* qset, int64_t M, int64_t H, int64_t F,
+                  te_dtype dtype, void* dx, float* dgamma, float* dbeta,
+                  void* dkernel1, void* dkernel2, float* dbias1, float* dbias2,
+                  void* saved_dh, void* workspace, size_t ws_bytes, void* stream) {
+  if (M < 0 || H <= 0 || F <= 0 || dtype != TE_BF16 || act == TE_IDENTITY || !valid_act(act) ||
+      (norm_type != TE_LAYERNORM && norm_type != TE_RMSNORM))
+    return dtype == TE_F32 ? TE_ERR_UNSUPPORTED : TE_ERR_INVALID_ARG;
+  const bool quant = qset != nullptr;
+  if (quant) {
+    if (!enabled(&qset->grad) || !quantizer_ok(&qset->grad) || !qset->x.scale_inv ||
+        !quantizer_ok(&qset->kernel1))
+      return TE_ERR_INVALID_ARG;
+    if (kernel_dtype == TE_E4M3 ? !qset->kernel1.scale_inv
+                                : (kernel_dtype != dtype || !enabled(&qset->kernel1)))
+      return TE_ERR_INVALID_ARG;
+  } else if (kernel_dtype != dtype) {
+    return TE_ERR_INVALID_ARG;
+  }
+  if (!gamma || !dgamma || (M > 0 && (!dy || !x || !kernel1 || !kernel2 || (!h.saved && (!h.codes || !h.scales)) ||
+                                      !saved_ln_out || !rsigma || !dx || !dkernel1 || !dkernel2)) ||
+      (M > 0 && norm_type == TE_LAYERNORM && !mu))
+    return TE_ERR_INVALID_ARG;
+  if (H % 16 || F % (h.codes ? 32 : 16) || H * int64_t(esize(dtype)) > 16384) return TE_ERR_UNSUPPORTED;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(gamma) || !aligned16(kernel1) ||
+      !aligned16(kernel2) || !opt_aligned16(h.saved) || !opt_aligned16(h.codes) || !opt_aligned16(h.scales) || !aligned16(saved_ln_out) || !aligned16(dx) ||
+      !aligned16(dkernel1) || !aligned16(dkernel2) || !aligned16(workspace) || !aligned4(mu) ||
+      !aligned4(rsigma) || !aligned4(dgamma) || !aligned4(dbeta) || !aligned4(dbias1) ||
+      !aligned4(dbias2) || !opt_aligned16(saved_dh))
+    return TE_ERR_UNSUPPORTED;
+  cudaStream_t s = as_stream(stream);
+  const bool gated = is_gated(act);
+  const int64_t F1 = gated ? 2 * F : F;
+  if (M == 0) {
+    // no tokens: every gradient is zero
+    const std::pair<void*, size_t> z[] = {{dgamma, size_t(H) * 4}, {dbeta, size_t(H) * 4},
+                                          {dbias1, size_t(F1) * 4}, {dbias2, size_t(H) * 4},
+                                          {dkernel1, size_t(H) * F1 * esize(dtype)},
+                                          {dkernel2, size_t(F) * H * esize(dtype)}};
+    for (const auto& e : z)
+      if (e.first && cudaMemsetAsync(e.first, 0, e.second, s) != cudaSuccess) return TE_ERR_CUDA;
+    return TE_OK;
+  }
+  BwdLayout L = bwd_layout(workspace, M, H, F, dtype, quant, kernel_dtype, act);
+  if (!workspace || ws_bytes < L.split.required) return TE_ERR_WORKSPACE;
+  float* partials = static_cast<float*>(L.partials);
+  void* dh = saved_dh ? saved_dh : L.dh;  // the dgrad / wgrad GEMMs' operand
+  te_status st;
+  // dbias2 = column sums of dy
+  if (dbias2) {
+    DactArgs d;
+    d.dy = dy;
+    d.dtype = dtype;
+    d.M = M;
+    d.N_in = H;
+    d.act = TE_IDENTITY;
+    d.dx = nullptr;
+    d.dbias = dbias2;
+    d.partials = partials;
+    st = launch_dact_dbias(d, s);
+    if (st != TE_OK) return st;
+  }
+  // recompute the activation output (what GEMM2 consumed, in dtype); from a checkpoint the gradient
+  // step below gives it
+  if (!h.codes) {
+    ActArgs aa;
+    aa.x = h.saved;
+    aa.x_dtype = dtype;
+    aa.M = M;
+    aa.N_in = F1;
+    aa.act = act;
+    aa.out = L.a;
+    aa.cast.out_dtype = dtype;
+    st = launch_act_lu(aa, s);
+    if (st != TE_OK) return st;
+  }
+  // dkernel2 = a^T dy   ([F, H], contraction over tokens)
+  auto dkernel2_product = [&]() {
+    GemmArgs g;
+    g.A = L.a;
+    g.B = dy;
+    g.ab_dtype = dtype;
+    g.a_kmajor = 0;
+    g.b_kmajor = 0;
+    g.M = F;
+    g.N = H;
+    g.K = M;
+    g.D = dkernel2;
+    g.cast.out_dtype = dtype;
+    give_split(g, L.split, workspace, ws_bytes);
+    return launch_gemm(g, s);
+  };
+  if (!h.codes) {
+    st = dkernel2_product();
+    if (st != TE_OK) return st;
+  }
+  // da = dy kernel2^T   ([M, F], contraction over H)
+  {
+    GemmArgs g;
+    g.A = dy;
+    g.B = kernel2;
+    g.ab_dtype = dtype;
+    g.a_kmajor = 1;
+    g.b_kmajor = 1;
+    g.M = M;
+    g.N = F;
+    g.K = H;
+    g.D = L.da;
+    g.cast.out_dtype = dtype;
+    give_split(g, L.split, workspace, ws_bytes);
+    st = launch_gemm(g, s);
+    if (st != TE_OK) return st;
+  }
+  // dH = da * act'(h), dbias1, quantized with the grad quantizer in FP8 mode
+  if (h.codes) {
+    DactCkptArgs d;
+    d.dy = L.da;
+    d.codes = h.codes;
+    d.scales = h.scales;
+    d.dtype = dtype;
+    d.M = M;
+    d.N_in = F1;
+    d.act = act;
+    d.dx = dh;
+    d.partials = partials;
+    st = dact_ckpt_cast(d, quant ? &qset->grad : nullptr, quant ? int(TE_E4M3) : int(dtype), L.a, dbias1, s);
+    if (st == TE_OK) st = dkernel2_product();
+  } else {
+    st = run_cast(quant ? &qset->grad : nullptr, quant ? TE_E4M3 : dtype, 0, s,
+                [&](const CastSpec& c) {
+                  DactArgs d;
+                  d.dy = L.da;
+                  d.x = h.saved;
+                  d.dtype = dtype;
+                  d.M = M;
+                  d.N_in = F1;
+                  d.act = act;
+                  d.dx = dh;
+                  const bool two_pass = quant && qset->grad.mode == TE_SCALING_CURRENT;
+                  d.dbias = (two_pass ? c.store == 0 : true) ? dbias1 : nullptr;
+                  d.partials = partials;
+                  d.cast = c;
+                  return launch_dact_dbias(d, s);
+                });
+  }
+  if (st != TE_OK) return st;
+  const void* w1 = kernel1;
+  if (quant && kernel_dtype != TE_E4M3) {
+    st = quantize_into(kernel1, dtype, H * F1, &qset->kernel1, L.kq1, s);
+    if (st != TE_OK) return st;
+    w1 = L.kq1;
+  }
+  // dln = dH kernel1^T   ([M, H], contraction over F')
+  {
+    GemmArgs g;
+    g.A = dh;
+    g.B = w1;
+    g.ab_dtype = quant ? TE_E4M3 : dtype;
+    g.a_kmajor = 1;
+    g.b_kmajor = 1;
+    g.M = M;
+    g.N = H;
+    g.K = F1;
+    g.a_scale_inv = quant ? qset->grad.scale_inv : nullptr;
+    g.b_scale_inv = quant ? qset->kernel1.scale_inv : nullptr;
+    g.D = L.dln;
+    g.cast.out_dtype = dtype;
+    give_split(g, L.split, workspace, ws_bytes);
+    st = launch_gemm(g, s);
+    if (st != TE_OK) return st;
+  }
+  // dkernel1 = ln^T dH   ([H, F'], contraction over tokens)
+  {
+    GemmArgs g;
+    g.A = saved_ln_out;
+    g.B = dh;
+    g.ab_dtype = quant ? TE_E4M3 : dtype;
+    g.a_kmajor = 0;
+    g.b_kmajor = 0;
+    g.M = H;
+    g.N = F1;
+    g.K = M;
+    g.a_scale_inv = quant ? qset->x.scale_inv : nullptr;
+    g.b_scale_inv = quant ? qset->grad.scale_inv : nullptr;
+    g.D = dkernel1;
+    g.cast.out_dtype = dtype;
+    give_split(g, L.split, workspace, ws_bytes);
+    st = launch_gemm(g, s);
+    if (st != TE_OK) return st;
+  }
+  // norm backward
+  NormBwdArgs nb;
+  nb.dz = L.dln;
+  nb.x = x;
+  nb.mu = mu;
+  nb.rsigma = rsigma;
+  nb.gamma = gamma;
+  nb.dtype = dtype;
+  nb.M = M;
+  nb.H = H;
+  nb.norm_type = norm_type;
+  nb.zero_centered_gamma = zero_centered_gamma;
+  nb.dx = dx;
+  nb.dgamma = dgamma;
+  nb.dbeta = norm_type == TE_LAYERNORM ? dbeta : nullptr;
+  nb.partials = partials;
+  // RMSNorm has no shift: the gradient of an (ignored) beta is zero
+  if (norm_type == TE_RMSNORM && dbeta &&
+      cudaMemsetAsync(dbeta, 0, size_t(H) * sizeof(float), s) != cudaSuccess)
+    return TE_ERR_CUDA;
+  return launch_norm_bwd(nb, s);
+}
+
 }  // namespace
 }  // namespace te
 
@@ -433,143 +810,29 @@ te_status te_layernorm_mlp_fwd(const void* x, const void* gamma, const void* bet
                                te_dtype dtype, void* out, void* saved_h, void* saved_act,
                                void* saved_ln_out, float* mu, float* rsigma, void* workspace,
                                size_t ws_bytes, void* stream) {
-  if (M < 0 || H <= 0 || F <= 0 || !is_act_dtype(dtype) || act == TE_IDENTITY ||
-      !valid_act(act) || (norm_type != TE_LAYERNORM && norm_type != TE_RMSNORM))
-    return TE_ERR_INVALID_ARG;
-  const bool quant = qset != nullptr;
-  if (quant) {
-    if (!enabled(&qset->x) || !enabled(&qset->act) || !quantizer_ok(&qset->x) ||
-        !quantizer_ok(&qset->act) || !quantizer_ok(&qset->kernel1) || !quantizer_ok(&qset->kernel2))
-      return TE_ERR_INVALID_ARG;
-    if (kernel_dtype == TE_E4M3
-            ? (!qset->kernel1.scale_inv || !qset->kernel2.scale_inv)
-            : (kernel_dtype != dtype || !enabled(&qset->kernel1) || !enabled(&qset->kernel2)))
-      return TE_ERR_INVALID_ARG;
-  } else if (kernel_dtype != dtype) {
-    return TE_ERR_INVALID_ARG;
-  }
-  if (M > 0 && (!x || !gamma || !kernel1 || !kernel2 || !out)) return TE_ERR_INVALID_ARG;
-  if (H % 16 || F % 16 || H * int64_t(esize(dtype)) > 16384) return TE_ERR_UNSUPPORTED;
-  if (!aligned16(x) || !aligned16(gamma) || !opt_aligned16(beta) || !aligned16(kernel1) ||
-      !aligned16(kernel2) || !opt_aligned16(bias1) || !opt_aligned16(bias2) || !aligned16(out) ||
-      !opt_aligned16(saved_h) || !opt_aligned16(saved_act) || !opt_aligned16(saved_ln_out) ||
-      !aligned16(workspace) || !aligned4(mu) || !aligned4(rsigma))
-    return TE_ERR_UNSUPPORTED;
-  if (M == 0) return TE_OK;
-  const bool gated = is_gated(act);
-  const int64_t F1 = gated ? 2 * F : F;
-  FwdLayout L = mlp_layout(workspace, M, H, F, dtype, quant, kernel_dtype, act,
-                           saved_ln_out != nullptr);
-  if (!workspace || ws_bytes < L.split.required) return TE_ERR_WORKSPACE;
-  cudaStream_t s = as_stream(stream);
-  void* ln = saved_ln_out ? saved_ln_out : L.ln;
-  void* a2 = saved_act ? saved_act : L.a2;  // GEMM2's A operand
-  // The activation's amax (GEMM1's epilogue accumulates into it) is zeroed before the norm rather
-  // than between the norm and GEMM1, where the memset would keep GEMM1 from launching as the
-  // norm's programmatic dependent; unless it shares storage with an amax written before GEMM1.
-  const bool act_zero_first =
-      quant && qset->act.amax && qset->act.amax != qset->x.amax &&
-      (kernel_dtype == TE_E4M3 ||
-       (qset->act.amax != qset->kernel1.amax && qset->act.amax != qset->kernel2.amax));
-  te_status st = act_zero_first ? zero_scalar(qset->act.amax, s) : TE_OK;
-  if (st != TE_OK) return st;
-  // (1) normalization, written once in GEMM1's operand dtype
-  st = norm_into(x, dtype, M, H, gamma, beta, norm_type, zero_centered_gamma, epsilon,
-                 quant ? &qset->x : nullptr, ln, quant ? TE_E4M3 : dtype, mu, rsigma, s);
-  if (st != TE_OK) return st;
-  const void* w1 = kernel1;
-  const void* w2 = kernel2;
-  int b_kmajor = 0;
-  if (quant && kernel_dtype != TE_E4M3) {
-    st = quantize_into(kernel1, dtype, H * F1, &qset->kernel1, L.kq1, s);
-    if (st != TE_OK) return st;
-    st = quantize_into(kernel2, dtype, F * H, &qset->kernel2, L.kq2, s);
-    if (st != TE_OK) return st;
-    w1 = L.kq1;
-    w2 = L.kq2;
-  } else if (!quant && dtype == TE_F32) {
-    st = launch_transpose_f32(static_cast<const float*>(kernel1), H, F1, static_cast<float*>(L.kt1), s);
-    if (st != TE_OK) return st;
-    st = launch_transpose_f32(static_cast<const float*>(kernel2), F, H, static_cast<float*>(L.kt2), s);
-    if (st != TE_OK) return st;
-    w1 = L.kt1;
-    w2 = L.kt2;
-    b_kmajor = 1;
-  }
-  // (2)+(3) GEMM1 + bias1 -> round -> activation [-> amax, E4M3], one kernel
-  GemmArgs g1;
-  g1.A = ln;
-  g1.B = w1;
-  g1.ab_dtype = quant ? TE_E4M3 : dtype;
-  g1.a_kmajor = 1;
-  g1.b_kmajor = b_kmajor;
-  g1.M = M;
-  g1.N = F1;
-  g1.K = H;
-  g1.a_scale_inv = quant ? qset->x.scale_inv : nullptr;
-  g1.b_scale_inv = quant ? qset->kernel1.scale_inv : nullptr;
-  g1.epilogue = gated ? EPI_BIAS_GATED : EPI_BIAS_ACT;
-  g1.act = act;
-  g1.bias = bias1;
-  g1.bias_dtype = dtype;
-  g1.h_dtype = dtype;
-  g1.saved_h = saved_h;
-  const bool act_current = quant && qset->act.mode == TE_SCALING_CURRENT;
-  if (quant) {
-    if (!act_zero_first) {
-      st = zero_scalar(qset->act.amax, s);
-      if (st != TE_OK) return st;
-    }
-    g1.cast.amax_out = qset->act.amax;
-    if (act_current) {
-      g1.D = L.a2_hi;
-      g1.cast.out_dtype = TE_F32;
-    } else {
-      g1.D = a2;
-      g1.cast.out_dtype = TE_E4M3;
-      g1.cast.scale = qset->act.scale;
-      g1.cast.scale_inv_out = qset->act.scale_inv;
-    }
-  } else {
-    g1.D = a2;
-    g1.cast.out_dtype = dtype;
-  }
-  give_split(g1, L.split, workspace, ws_bytes);
-  st = launch_gemm(g1, s);
-  if (st != TE_OK) return st;
-  if (act_current) {
-    // The amax is already known from GEMM1's epilogue: one cast pass.
-    QuantizeArgs qa;
-    qa.x = L.a2_hi;
-    qa.x_dtype = TE_F32;
-    qa.n = M * F;
-    qa.out = a2;
-    qa.cast.out_dtype = TE_E4M3;
-    qa.cast.amax_in = qset->act.amax;
-    qa.cast.scale_out = qset->act.scale;
-    qa.cast.scale_inv_out = qset->act.scale_inv;
-    st = launch_quantize(qa, s);
-    if (st != TE_OK) return st;
-  }
-  // (4) GEMM2 + bias2
-  GemmArgs g2;
-  g2.A = a2;
-  g2.B = w2;
-  g2.ab_dtype = quant ? TE_E4M3 : dtype;
-  g2.a_kmajor = 1;
-  g2.b_kmajor = b_kmajor;
-  g2.M = M;
-  g2.N = H;
-  g2.K = F;
-  g2.a_scale_inv = quant ? qset->act.scale_inv : nullptr;
-  g2.b_scale_inv = quant ? qset->kernel2.scale_inv : nullptr;
-  g2.epilogue = EPI_BIAS;
-  g2.bias = bias2;
-  g2.bias_dtype = dtype;
-  g2.D = out;
-  g2.cast.out_dtype = dtype;
-  give_split(g2, L.split, workspace, ws_bytes);
-  return launch_gemm(g2, s);
+  MlpPreact h;
+  h.saved = saved_h;
+  return mlp_fwd(x, gamma, beta, kernel1, kernel2, kernel_dtype, bias1, bias2, norm_type,
+                 zero_centered_gamma, epsilon, act, qset, M, H, F, dtype, out, h, saved_act,
+                 saved_ln_out, mu, rsigma, workspace, ws_bytes, stream);
+}
+
+te_status te_layernorm_mlp_fwd_ckpt(const void* x, const void* gamma, const void* beta,
+                                    const void* kernel1, const void* kernel2, te_dtype kernel_dtype,
+                                    const void* bias1, const void* bias2, te_norm_type norm_type,
+                                    int zero_centered_gamma, float epsilon, te_act_type act,
+                                    const te_quantizer_set* qset, int64_t M, int64_t H, int64_t F,
+                                    te_dtype dtype, void* out, void* h_codes, void* h_scales,
+                                    void* saved_act,
+                                    void* saved_ln_out, float* mu, float* rsigma, void* workspace,
+                                    size_t ws_bytes, void* stream) {
+  if (M > 0 && (!h_codes || !h_scales)) return TE_ERR_INVALID_ARG;
+  MlpPreact h;
+  h.codes = h_codes;
+  h.scales = h_scales;
+  return mlp_fwd(x, gamma, beta, kernel1, kernel2, kernel_dtype, bias1, bias2, norm_type,
+                 zero_centered_gamma, epsilon, act, qset, M, H, F, dtype, out, h, saved_act,
+                 saved_ln_out, mu, rsigma, workspace, ws_bytes, stream);
 }
 
 te_status te_layernorm_mlp_bwd(const void* dy, const void* x, const void* gamma,
@@ -581,193 +844,30 @@ te_status te_layernorm_mlp_bwd(const void* dy, const void* x, const void* gamma,
                                te_dtype dtype, void* dx, float* dgamma, float* dbeta,
                                void* dkernel1, void* dkernel2, float* dbias1, float* dbias2,
                                void* saved_dh, void* workspace, size_t ws_bytes, void* stream) {
-  if (M < 0 || H <= 0 || F <= 0 || dtype != TE_BF16 || act == TE_IDENTITY || !valid_act(act) ||
-      (norm_type != TE_LAYERNORM && norm_type != TE_RMSNORM))
-    return dtype == TE_F32 ? TE_ERR_UNSUPPORTED : TE_ERR_INVALID_ARG;
-  const bool quant = qset != nullptr;
-  if (quant) {
-    if (!enabled(&qset->grad) || !quantizer_ok(&qset->grad) || !qset->x.scale_inv ||
-        !quantizer_ok(&qset->kernel1))
-      return TE_ERR_INVALID_ARG;
-    if (kernel_dtype == TE_E4M3 ? !qset->kernel1.scale_inv
-                                : (kernel_dtype != dtype || !enabled(&qset->kernel1)))
-      return TE_ERR_INVALID_ARG;
-  } else if (kernel_dtype != dtype) {
-    return TE_ERR_INVALID_ARG;
-  }
-  if (!gamma || !dgamma || (M > 0 && (!dy || !x || !kernel1 || !kernel2 || !saved_h ||
-                                      !saved_ln_out || !rsigma || !dx || !dkernel1 || !dkernel2)) ||
-      (M > 0 && norm_type == TE_LAYERNORM && !mu))
-    return TE_ERR_INVALID_ARG;
-  if (H % 16 || F % 16 || H * int64_t(esize(dtype)) > 16384) return TE_ERR_UNSUPPORTED;
-  if (!aligned16(dy) || !aligned16(x) || !aligned16(gamma) || !aligned16(kernel1) ||
-      !aligned16(kernel2) || !aligned16(saved_h) || !aligned16(saved_ln_out) || !aligned16(dx) ||
-      !aligned16(dkernel1) || !aligned16(dkernel2) || !aligned16(workspace) || !aligned4(mu) ||
-      !aligned4(rsigma) || !aligned4(dgamma) || !aligned4(dbeta) || !aligned4(dbias1) ||
-      !aligned4(dbias2) || !opt_aligned16(saved_dh))
-    return TE_ERR_UNSUPPORTED;
-  cudaStream_t s = as_stream(stream);
-  const bool gated = is_gated(act);
-  const int64_t F1 = gated ? 2 * F : F;
-  if (M == 0) {
-    // no tokens: every gradient is zero
-    const std::pair<void*, size_t> z[] = {{dgamma, size_t(H) * 4}, {dbeta, size_t(H) * 4},
-                                          {dbias1, size_t(F1) * 4}, {dbias2, size_t(H) * 4},
-                                          {dkernel1, size_t(H) * F1 * esize(dtype)},
-                                          {dkernel2, size_t(F) * H * esize(dtype)}};
-    for (const auto& e : z)
-      if (e.first && cudaMemsetAsync(e.first, 0, e.second, s) != cudaSuccess) return TE_ERR_CUDA;
-    return TE_OK;
-  }
-  BwdLayout L = bwd_layout(workspace, M, H, F, dtype, quant, kernel_dtype, act);
-  if (!workspace || ws_bytes < L.split.required) return TE_ERR_WORKSPACE;
-  float* partials = static_cast<float*>(L.partials);
-  void* dh = saved_dh ? saved_dh : L.dh;  // the dgrad / wgrad GEMMs' operand
-  te_status st;
-  // dbias2 = column sums of dy
-  if (dbias2) {
-    DactArgs d;
-    d.dy = dy;
-    d.dtype = dtype;
-    d.M = M;
-    d.N_in = H;
-    d.act = TE_IDENTITY;
-    d.dx = nullptr;
-    d.dbias = dbias2;
-    d.partials = partials;
-    st = launch_dact_dbias(d, s);
-    if (st != TE_OK) return st;
-  }
-  // recompute the activation output (what GEMM2 consumed, in dtype)
-  {
-    ActArgs aa;
-    aa.x = saved_h;
-    aa.x_dtype = dtype;
-    aa.M = M;
-    aa.N_in = F1;
-    aa.act = act;
-    aa.out = L.a;
-    aa.cast.out_dtype = dtype;
-    st = launch_act_lu(aa, s);
-    if (st != TE_OK) return st;
-  }
-  // dkernel2 = a^T dy   ([F, H], contraction over tokens)
-  {
-    GemmArgs g;
-    g.A = L.a;
-    g.B = dy;
-    g.ab_dtype = dtype;
-    g.a_kmajor = 0;
-    g.b_kmajor = 0;
-    g.M = F;
-    g.N = H;
-    g.K = M;
-    g.D = dkernel2;
-    g.cast.out_dtype = dtype;
-    give_split(g, L.split, workspace, ws_bytes);
-    st = launch_gemm(g, s);
-    if (st != TE_OK) return st;
-  }
-  // da = dy kernel2^T   ([M, F], contraction over H)
-  {
-    GemmArgs g;
-    g.A = dy;
-    g.B = kernel2;
-    g.ab_dtype = dtype;
-    g.a_kmajor = 1;
-    g.b_kmajor = 1;
-    g.M = M;
-    g.N = F;
-    g.K = H;
-    g.D = L.da;
-    g.cast.out_dtype = dtype;
-    give_split(g, L.split, workspace, ws_bytes);
-    st = launch_gemm(g, s);
-    if (st != TE_OK) return st;
-  }
-  // dH = da * act'(h), dbias1, quantized with the grad quantizer in FP8 mode
-  st = run_cast(quant ? &qset->grad : nullptr, quant ? TE_E4M3 : dtype, 0, s,
-                [&](const CastSpec& c) {
-                  DactArgs d;
-                  d.dy = L.da;
-                  d.x = saved_h;
-                  d.dtype = dtype;
-                  d.M = M;
-                  d.N_in = F1;
-                  d.act = act;
-                  d.dx = dh;
-                  const bool two_pass = quant && qset->grad.mode == TE_SCALING_CURRENT;
-                  d.dbias = (two_pass ? c.store == 0 : true) ? dbias1 : nullptr;
-                  d.partials = partials;
-                  d.cast = c;
-                  return launch_dact_dbias(d, s);
-                });
-  if (st != TE_OK) return st;
-  const void* w1 = kernel1;
-  if (quant && kernel_dtype != TE_E4M3) {
-    st = quantize_into(kernel1, dtype, H * F1, &qset->kernel1, L.kq1, s);
-    if (st != TE_OK) return st;
-    w1 = L.kq1;
-  }
-  // dln = dH kernel1^T   ([M, H], contraction over F')
-  {
-    GemmArgs g;
-    g.A = dh;
-    g.B = w1;
-    g.ab_dtype = quant ? TE_E4M3 : dtype;
-    g.a_kmajor = 1;
-    g.b_kmajor = 1;
-    g.M = M;
-    g.N = H;
-    g.K = F1;
-    g.a_scale_inv = quant ? qset->grad.scale_inv : nullptr;
-    g.b_scale_inv = quant ? qset->kernel1.scale_inv : nullptr;
-    g.D = L.dln;
-    g.cast.out_dtype = dtype;
-    give_split(g, L.split, workspace, ws_bytes);
-    st = launch_gemm(g, s);
-    if (st != TE_OK) return st;
-  }
-  // dkernel1 = ln^T dH   ([H, F'], contraction over tokens)
-  {
-    GemmArgs g;
-    g.A = saved_ln_out;
-    g.B = dh;
-    g.ab_dtype = quant ? TE_E4M3 : dtype;
-    g.a_kmajor = 0;
-    g.b_kmajor = 0;
-    g.M = H;
-    g.N = F1;
-    g.K = M;
-    g.a_scale_inv = quant ? qset->x.scale_inv : nullptr;
-    g.b_scale_inv = quant ? qset->grad.scale_inv : nullptr;
-    g.D = dkernel1;
-    g.cast.out_dtype = dtype;
-    give_split(g, L.split, workspace, ws_bytes);
-    st = launch_gemm(g, s);
-    if (st != TE_OK) return st;
-  }
-  // norm backward
-  NormBwdArgs nb;
-  nb.dz = L.dln;
-  nb.x = x;
-  nb.mu = mu;
-  nb.rsigma = rsigma;
-  nb.gamma = gamma;
-  nb.dtype = dtype;
-  nb.M = M;
-  nb.H = H;
-  nb.norm_type = norm_type;
-  nb.zero_centered_gamma = zero_centered_gamma;
-  nb.dx = dx;
-  nb.dgamma = dgamma;
-  nb.dbeta = norm_type == TE_LAYERNORM ? dbeta : nullptr;
-  nb.partials = partials;
-  // RMSNorm has no shift: the gradient of an (ignored) beta is zero
-  if (norm_type == TE_RMSNORM && dbeta &&
-      cudaMemsetAsync(dbeta, 0, size_t(H) * sizeof(float), s) != cudaSuccess)
-    return TE_ERR_CUDA;
-  return launch_norm_bwd(nb, s);
+  MlpPreact h;
+  h.saved = const_cast<void*>(saved_h);
+  return mlp_bwd(dy, x, gamma, kernel1, kernel2, kernel_dtype, h, saved_ln_out, mu, rsigma,
+                 norm_type, zero_centered_gamma, act, qset, M, H, F, dtype, dx, dgamma, dbeta,
+                 dkernel1, dkernel2, dbias1, dbias2, saved_dh, workspace, ws_bytes, stream);
+}
+
+te_status te_layernorm_mlp_bwd_ckpt(const void* dy, const void* x, const void* gamma,
+                                    const void* kernel1, const void* kernel2, te_dtype kernel_dtype,
+                                    const void* h_codes, const void* h_scales,
+                                    const void* saved_ln_out, const float* mu, const float* rsigma,
+                                    te_norm_type norm_type,
+                                    int zero_centered_gamma, te_act_type act,
+                                    const te_quantizer_set* qset, int64_t M, int64_t H, int64_t F,
+                                    te_dtype dtype, void* dx, float* dgamma, float* dbeta,
+                                    void* dkernel1, void* dkernel2, float* dbias1, float* dbias2,
+                                    void* saved_dh, void* workspace, size_t ws_bytes, void* stream) {
+  if (M > 0 && (!h_codes || !h_scales)) return TE_ERR_INVALID_ARG;
+  MlpPreact h;
+  h.codes = const_cast<void*>(h_codes);
+  h.scales = const_cast<void*>(h_scales);
+  return mlp_bwd(dy, x, gamma, kernel1, kernel2, kernel_dtype, h, saved_ln_out, mu, rsigma,
+                 norm_type, zero_centered_gamma, act, qset, M, H, F, dtype, dx, dgamma, dbeta,
+                 dkernel1, dkernel2, dbias1, dbias2, saved_dh, workspace, ws_bytes, stream);
 }
 
 te_status te_layernorm_dense_bwd(const void* dy, const void* x, const void* gamma,

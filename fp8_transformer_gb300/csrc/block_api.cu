@@ -102,7 +102,7 @@ te_status te_block_quantize(const void* x, te_dtype x_dtype, int64_t M, int64_t 
                             void* scales, void* codes_t, void* scales_t, void* stream) {
   if (M < 0 || N <= 0 || !is_act_dtype(x_dtype) || !valid_format(format) ||
       !format_quantizer_ok(format, q) || !codes != !scales || !codes_t != !scales_t ||
-      (!codes && !codes_t) || (M > 0 && !x))
+      (M > 0 && (!x || (!codes && !codes_t))))
     return TE_ERR_INVALID_ARG;
   if (N % (codes ? 32 : 16) || (codes_t && format == TE_MXFP8)) return TE_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(codes_t) ||

@@ -39,6 +39,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "block.cuh"
 #include "common.cuh"
 #include "kernels.h"
 #include "sync.cuh"
@@ -93,6 +94,9 @@ struct GemmDev {
   int bias_dtype;
   int h_dtype;
   void* saved_h;
+  uint8_t* h_codes;   // the same in MXFP8, and its scale tiles
+  uint8_t* h_scales;
+  int64_t h_groups;   // scale tiles along a row of tiles
   void* D;
   int d_dtype;
   const float* out_scale;
@@ -288,6 +292,29 @@ __device__ __forceinline__ void store_seg(void* base, int64_t off, const float (
         p[i] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
       }
   }
+}
+
+// A block of 32 pre-activations (one row, columns from `col`, a multiple of 32) as an 8-bit
+// checkpoint: a thread holds a whole block, so its scale needs no exchange.
+__device__ __forceinline__ void store_checkpoint(const GemmDev& g, int64_t row, int64_t col, const float (&v)[32]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+  const BlockScale b = block_scale<TE_MXFP8>(m, 1.0f, nullptr);
+  uint4* out = reinterpret_cast<uint4*>(g.h_codes + row * g.N + col);
+  const f32x2 s2 = f2s(b.mul);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float* x = v + 16 * q + 4 * k;
+      const f32x2 lo = mul2(f2(x[0], x[1]), s2), hi = mul2(f2(x[2], x[3]), s2);
+      w[k] = b.bad ? 0u : pack_e4m3x4(f2lo(lo), f2hi(lo), f2lo(hi), f2hi(hi));
+    }
+    out[q] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  g.h_scales[(row / 128) * g.h_groups * 512 + scale_offset(uint32_t(row % 128), uint32_t(col / 32))] = uint8_t(b.byte);
 }
 
 // The bias values of columns j and j + 1 (j even) as an fp32 pair.
@@ -667,6 +694,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           }
           if (g.epilogue == EPI_BIAS_ACT) {
             if (g.saved_h && row_ok) store_seg(g.saved_h, row * g.N + col0, v, count, g.h_dtype, 1.0f);
+            if (g.h_codes && row_ok) store_checkpoint(g, row, col0, v);
             act_chunk(g.act, v);
           }
           if (row_ok) {
@@ -706,6 +734,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           if (g.saved_h && row_ok) {
             store_seg(g.saved_h, row * g.N + col0, vg, count, g.h_dtype, 1.0f);
             store_seg(g.saved_h, row * g.N + g.F + col0, vl, count, g.h_dtype, 1.0f);
+          }
+          if (g.h_codes && row_ok) {
+            store_checkpoint(g, row, col0, vg);
+            store_checkpoint(g, row, g.F + col0, vl);
           }
           gated_chunk(gact, vg, vl);
           if (row_ok) {
@@ -946,6 +978,9 @@ te_status launch_gemm(const GemmArgs& a, cudaStream_t s) {
   g.bias_dtype = a.bias_dtype;
   g.h_dtype = a.h_dtype;
   g.saved_h = a.saved_h;
+  g.h_codes = static_cast<uint8_t*>(a.h_codes);
+  g.h_scales = static_cast<uint8_t*>(a.h_scales);
+  g.h_groups = scale_groups(TE_MXFP8, a.N);
   g.D = a.D;
   g.d_dtype = a.cast.out_dtype;
   g.out_scale = a.cast.scale;

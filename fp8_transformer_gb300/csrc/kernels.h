@@ -202,6 +202,8 @@ struct GemmArgs {
   int bias_dtype = TE_F32;
   int h_dtype = TE_F32;         // dtype the pre-activation is rounded to (act epilogues)
   void* saved_h = nullptr;      // [M, N] pre-activation, h_dtype
+  void* h_codes = nullptr;      // [M, N] pre-activation in MXFP8 (N a multiple of 32), or null
+  void* h_scales = nullptr;
   void* D = nullptr;            // [M, N] or [M, N/2] gated
   CastSpec cast;                // output stage of D (amax / E4M3 of the activation)
   // Optional scratch (256-byte aligned) for splitting the last wave's tiles along K; without it

@@ -485,6 +485,35 @@ te_status te_dact_dbias_ckpt(const void* dy, const void* codes, const void* scal
                              void* dx, te_dtype dx_dtype, void* act_out, float* dbias,
                              void* workspace, size_t ws_bytes, void* stream);
 
+/* te_layernorm_mlp_fwd_ckpt -- te_layernorm_mlp_fwd that keeps GEMM1's output plus bias1 (rounded to
+ * dtype) as an 8-bit checkpoint instead of saved_h: 1.03 bytes a value for the 2 of bf16, written by
+ * GEMM1's epilogue.
+ *   h_codes, h_scales  [M, F'] in TE_MXFP8, required.
+ * The other arguments, results and the workspace are te_layernorm_mlp_fwd's; F a multiple of 32. */
+te_status te_layernorm_mlp_fwd_ckpt(const void* x, const void* gamma, const void* beta,
+                                    const void* kernel1, const void* kernel2, te_dtype kernel_dtype,
+                                    const void* bias1, const void* bias2, te_norm_type norm_type,
+                                    int zero_centered_gamma, float epsilon, te_act_type act,
+                                    const te_quantizer_set* qset, int64_t M, int64_t H, int64_t F,
+                                    te_dtype dtype, void* out, void* h_codes, void* h_scales,
+                                    void* saved_act, void* saved_ln_out, float* mu, float* rsigma,
+                                    void* workspace, size_t ws_bytes, void* stream);
+
+/* te_layernorm_mlp_bwd_ckpt -- te_layernorm_mlp_bwd from that checkpoint.  The activation and its
+ * gradient are those of the checkpoint's values, and come from one pass over it (te_dact_dbias_ckpt)
+ * between da and dkernel2.  The other arguments, results and the workspace are
+ * te_layernorm_mlp_bwd's; F a multiple of 32. */
+te_status te_layernorm_mlp_bwd_ckpt(const void* dy, const void* x, const void* gamma,
+                                    const void* kernel1, const void* kernel2, te_dtype kernel_dtype,
+                                    const void* h_codes, const void* h_scales,
+                                    const void* saved_ln_out, const float* mu, const float* rsigma,
+                                    te_norm_type norm_type, int zero_centered_gamma,
+                                    te_act_type act, const te_quantizer_set* qset, int64_t M,
+                                    int64_t H, int64_t F, te_dtype dtype, void* dx, float* dgamma,
+                                    float* dbeta, void* dkernel1, void* dkernel2, float* dbias1,
+                                    float* dbias2, void* saved_dh, void* workspace, size_t ws_bytes,
+                                    void* stream);
+
 /* ---------------------------------------------------------------------------------------
  * te_norm_bwd -- gradients of te_norm_fwd (LayerNorm MLP page, Description: the backward pass
  * yields the gradient of every parameter; LayerNorm Dense page, Description: gradients of x,

@@ -1,0 +1,182 @@
+"""The LN-MLP block with its pre-activation kept in 8 bits: forward, then backward from the checkpoint.
+
+The forward is the plain one's in every output, and its checkpoint is the packing of the plain
+one's saved_h, byte for byte.  The backward is held, step by step, to the oracle's backward at the
+values that the checkpoint stands for (exact in bf16), by the rules of the plain backward's test.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_transformer_gb300 as te
+from oracle import block as ob
+from oracle import block_scaled as bs
+from parity import np64
+from steps import check_mlp_bwd
+from workloads import make_inputs
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+GATED = ("swiglu", "geglu", "reglu")
+
+
+def quantizers(mode):
+    if mode is None:
+        return None
+    if mode == "current":
+        return te.QuantizerSet(**{k: te.Quantizer(mode="current") for k in ("x", "kernel1", "act", "kernel2", "grad")})
+    return te.QuantizerSet(x=te.Quantizer(32.0), kernel1=te.Quantizer(2048.0), act=te.Quantizer(16.0),
+                           kernel2=te.Quantizer(2048.0), grad=te.Quantizer(64.0))
+
+
+def inputs(name, act, M, H, F):
+    inp = make_inputs(name, device=DEV, M=M, H=H, F=F)
+    if act is not None:
+        inp["act"] = act
+    if "dy" not in inp:
+        inp["dy"] = make_inputs("gpt_ln_mlp_bwd", device=DEV, M=M, H=H, F=16, seed=1)["dy"]
+    return inp
+
+
+def forward(inp, mode, ckpt):
+    M, H, F = inp["M"], inp["H"], inp["F"]
+    F1 = 2 * F if inp["act"] in GATED else F
+    dt = inp["x"].dtype
+    qs = quantizers(mode)
+    r = dict(qs=qs, out=torch.empty(M, H, dtype=dt, device=DEV),
+             ln=torch.empty(M, H, dtype=torch.uint8 if mode else dt, device=DEV),
+             mu=torch.empty(M, device=DEV), rs=torch.empty(M, device=DEV),
+             act=torch.empty(M, F, dtype=torch.uint8 if mode else dt, device=DEV))
+    kw = dict(norm_type=inp["norm"], zero_centered_gamma=inp["zero_centered_gamma"], activation_type=inp["act"],
+              quantizer_set=qs, epsilon=inp["eps"], saved_ln_out=r["ln"], mu=r["mu"], rsigma=r["rs"],
+              saved_act=r["act"])
+    args = (inp["x"], inp["gamma"], inp["beta"], inp["w1"], inp["w2"], inp.get("b1"), inp.get("b2"), r["out"])
+    if ckpt:
+        n = te.block_scale_bytes("mxfp8", M, F1)
+        codes = torch.full((M * F1 + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+        scales = torch.full((n + 256,), 0xA5, dtype=torch.uint8, device=DEV)
+        r["codes"], r["scales"] = codes[:M * F1].view(M, F1), scales[:n]
+        te.te_layernorm_mlp_fwd_ckpt(*args, r["codes"], r["scales"], **kw)
+        assert (codes[M * F1:] == 0xA5).all() and (scales[n:] == 0xA5).all()
+    else:
+        r["h"] = torch.empty(M, F1, dtype=dt, device=DEV)
+        te.te_layernorm_mlp_fwd(*args, saved_h=r["h"], **kw)
+    torch.cuda.synchronize()
+    assert te.get_device_status() == 0
+    return r
+
+
+@pytest.mark.parametrize("name,act,M,H,F", [("gpt_ln_mlp_bwd", None, 300, 512, 800),
+                                            ("gpt_ln_mlp_bwd", "relu", 1, 256, 32),
+                                            ("llama_rms_mlp", None, 256, 512, 544),
+                                            ("llama_rms_mlp", "geglu", 77, 256, 96),
+                                            ("tiny_ln_mlp", None, 64, 128, 512)])
+@pytest.mark.parametrize("mode", [None, "delayed", "current"])
+def test_forward_is_the_plain_one_with_its_preactivation_packed(name, act, M, H, F, mode):
+    inp = inputs(name, act, M, H, F)
+    if inp["x"].dtype == torch.float32:
+        inp["dy"] = None
+    a, b = forward(inp, mode, False), forward(inp, mode, True)
+    for k in ("out", "ln", "mu", "rs", "act"):
+        assert torch.equal(a[k], b[k]), k
+    c, s = bs.pack(np64(a["h"]), "mxfp8")
+    assert np.array_equal(b["codes"].cpu().numpy(), c)
+    assert np.array_equal(b["scales"].cpu().numpy(), bs.tile_scales(s))
+
+
+def backward(inp, f, **over):
+    M, H, F = inp["M"], inp["H"], inp["F"]
+    gated = inp["act"] in GATED
+    F1 = 2 * F if gated else F
+    dt = torch.bfloat16
+    g = dict(f, dx=torch.empty(M, H, dtype=dt, device=DEV), dgamma=torch.empty(H, device=DEV),
+             dbeta=torch.empty(H, device=DEV), dw1=torch.empty(H, F1, dtype=dt, device=DEV),
+             dw2=torch.empty(F, H, dtype=dt, device=DEV), db1=torch.empty(F1, device=DEV),
+             db2=torch.empty(H, device=DEV),
+             dh=torch.empty(M, F1, dtype=torch.uint8 if f["qs"] else dt, device=DEV))
+    te.te_layernorm_mlp_bwd_ckpt(inp["dy"], inp["x"], inp["gamma"], inp["w1"], inp["w2"], f["codes"], f["scales"],
+                                 f["ln"], f["mu"], f["rs"], g["dx"], g["dgamma"], g["dw1"], g["dw2"],
+                                 dbeta=g["dbeta"], dbias1=g["db1"], dbias2=g["db2"], norm_type=inp["norm"],
+                                 zero_centered_gamma=inp["zero_centered_gamma"], activation_type=inp["act"],
+                                 quantizer_set=f["qs"], saved_dh=g["dh"], **over)
+    return g
+
+
+@pytest.mark.parametrize("name,act,M,H,F", [("gpt_ln_mlp_bwd", None, 300, 512, 800),
+                                            ("gpt_ln_mlp_bwd", "silu", 33, 256, 160),
+                                            ("llama_rms_mlp", None, 256, 512, 544),
+                                            ("llama_rms_mlp", "reglu", 130, 256, 96)])
+@pytest.mark.parametrize("mode", [None, "delayed", "current"])
+def test_backward_from_the_checkpoint(name, act, M, H, F, mode):
+    inp = inputs(name, act, M, H, F)
+    f = forward(inp, mode, True)
+    g = backward(inp, f)
+    torch.cuda.synchronize()
+    assert te.get_device_status() == 0
+    # the values that the checkpoint stands for: 4 significant bits, exact in bf16
+    g["h"] = te.te_block_dequantize(f["codes"], f["scales"], "mxfp8", torch.empty_like(f["codes"], dtype=torch.bfloat16))
+    if inp["norm"] != "layernorm":
+        assert int(g["dbeta"].count_nonzero().item()) == 0
+        g["dbeta"] = None
+    check_mlp_bwd(inp, g, mode is not None)
+
+
+def test_backward_is_the_same_on_every_run_and_in_a_graph():
+    inp = inputs("llama_rms_mlp", None, 200, 256, 288)
+    f = forward(inp, None, True)
+    ref = backward(inp, f)
+    ws = torch.empty(te.workspace_size(te.binding.TE_OP_LAYERNORM_MLP_BWD, 200, 256, 288, te.binding.TE_BF16, False,
+                                       te.binding.TE_BF16, te.binding.TE_SWIGLU), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g = backward(inp, f, workspace=ws)
+    for _ in range(2):
+        ws.fill_(0xFF)
+        graph.replay()
+        for k in ("dx", "dgamma", "dw1", "dw2", "db1", "db2", "dh"):
+            assert torch.equal(g[k], ref[k]), k
+
+
+def test_no_tokens_and_refusals():
+    inp = inputs("gpt_ln_mlp_bwd", None, 16, 64, 96)
+    f = forward(inp, None, True)
+    for k in ("x", "dy"):
+        inp[k] = inp[k][:0]
+    inp["M"] = 0
+    e = {k: v[:0] if k in ("codes", "ln", "mu", "rs", "scales") else v for k, v in f.items()}
+    g = backward(inp, e)
+    torch.cuda.synchronize()
+    for k in ("dgamma", "dbeta", "dw1", "dw2", "db1", "db2"):
+        assert (g[k] == 0).all(), k
+    inp = inputs("gpt_ln_mlp_bwd", None, 16, 64, 96)
+    with pytest.raises(ValueError, match="h_codes"):
+        backward(inp, dict(f, codes=f["codes"][:8]))
+    inp = inputs("gpt_ln_mlp_bwd", None, 16, 64, 48)  # half a block
+    with pytest.raises((te.TEError, ValueError)):
+        forward(inp, None, True)
+    b = te.binding
+    P = 4096
+    call = lambda F, codes: te.lib().te_layernorm_mlp_fwd_ckpt(
+        P, P, P, P, P, b.TE_BF16, None, None, b.TE_LAYERNORM, 0, 1e-6, b.TE_GELU, None, 16, 64, F, b.TE_BF16, P, codes, P,
+        None, None, None, None, P, 1 << 30, None)
+    assert call(48, P) == b.TE_ERR_UNSUPPORTED
+    assert call(64, None) == b.TE_ERR_INVALID_ARG
+    assert call(64, P + 8) == b.TE_ERR_UNSUPPORTED
+
+
+def test_difference_to_the_uncompressed_gradients_is_the_checkpoints_rounding():
+    """The block's loss gradient against the one from saved_h: h moves by at most 2^-4 of itself (E4M3) or
+    half of E4M3's smallest step (2^-10) of its block's scale, so act(h) and act'(h) move with it."""
+    inp = inputs("gpt_ln_mlp_bwd", None, 256, 256, 512)
+    a, f = forward(inp, None, False), forward(inp, None, True)
+    h = np64(a["h"])
+    hq = bs.unpack(*bs.pack(h, "mxfp8"), "mxfp8")
+    step = np.ldexp(1.0, np.frexp(np.abs(h).reshape(256, -1, 32).max(-1) / 448.0)[1]).repeat(32, -1)
+    assert (np.abs(h - hq) <= np.maximum(np.abs(h) / 16, step * 2.0 ** -10)).all()
+    g = backward(inp, f)
+    da = np64(inp["dy"]) @ np64(inp["w2"]).T
+    lip = np.abs(ob.act_bwd(np.ones_like(h), h + 1e-3, "gelu") - ob.act_bwd(np.ones_like(h), h - 1e-3, "gelu")).max() / 2e-3
+    bound = np.abs(da) * (lip * 1.5 * np.abs(h - hq)) + 2.0 ** -7 * np.abs(da) * 1.2 + 2e-2
+    assert (np.abs(np64(g["dh"]) - ob.act_bwd(da, h, "gelu")) <= bound).all()
