@@ -881,8 +881,8 @@ bool allow_smem(Kernel kernel, size_t smem, PerDevice<bool>& set) {
 }
 
 // Codes as bytes: 128-byte rows of 256 codes, `rows` rows to a box.
-bool code_map(CUtensorMap* tm, const void* ptr, int64_t rows, int64_t K, uint32_t box_rows) {
-  return make_tmap_2d(tm, ptr, TE_E4M3, uint64_t(K / 2), uint64_t(rows), kRowBytes, box_rows, 128);
+bool code_map(CUtensorMap* tm, const void* ptr, int64_t rows, int64_t K, int64_t pitch, uint32_t box_rows) {
+  return make_tmap_2d(tm, ptr, TE_E4M3, uint64_t(K / 2), uint64_t(rows), kRowBytes, box_rows, 128, uint64_t(pitch));
 }
 
 template <int FMT>
@@ -892,7 +892,7 @@ te_status launch_batch(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStream_
   const uint64_t groups = uint64_t(scale_groups(FMT, a.K));
   g.num_m = int(ceil_div(a.M, BM * 2));
   g.num_n = int(ceil_div(a.N, BN));
-  if (!code_map(&prm.tmA, a.A, a.M, a.K, BM) || !code_map(&prm.tmB, a.B, a.N, a.K, C::kBRows) ||
+  if (!code_map(&prm.tmA, a.A, a.M, a.K, 0, BM) || !code_map(&prm.tmB, a.B, a.N, a.K, a.b_pitch, C::kBRows) ||
       !make_tmap_scales(&prm.tmSA, a.a_scales, groups, uint64_t(ceil_div(a.M, 128)), C::G, 1) ||
       !make_tmap_scales(&prm.tmSB, a.b_scales, groups, uint64_t(ceil_div(a.N, 128)), C::G, 2) ||
       !make_tmap_2d(&prm.tmD, a.D, a.d_dtype, uint64_t(a.N), uint64_t(a.M), a.d_dtype == TE_F32 ? 16 : 32, 32, kOutRow))
@@ -912,10 +912,10 @@ template <int FMT, int TOK, typename X>
 te_status launch_few(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStream_t s) {
   using C = FewCfg<FMT, TOK>;
   const uint64_t groups = uint64_t(scale_groups(FMT, a.K));
-  bool ok = code_map(&prm.tmB, a.B, a.N, a.K, BM) &&
+  bool ok = code_map(&prm.tmB, a.B, a.N, a.K, a.b_pitch, BM) &&
             make_tmap_scales(&prm.tmSB, a.b_scales, groups, uint64_t(ceil_div(a.N, 128)), C::G, 1);
   if constexpr (std::is_void_v<X>)
-    ok = ok && code_map(&prm.tmA, a.A, a.M, a.K, TOK) && make_tmap_scales(&prm.tmSA, a.a_scales, groups, 1, C::G, 1);
+    ok = ok && code_map(&prm.tmA, a.A, a.M, a.K, 0, TOK) && make_tmap_scales(&prm.tmSA, a.a_scales, groups, 1, C::G, 1);
   if (!ok) return TE_ERR_CUDA;
   const int64_t tiles = ceil_div(a.N, BM);
   if (tiles > 0x0fffffff) return TE_ERR_UNSUPPORTED;
@@ -949,7 +949,8 @@ te_status launch_fmt(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStream_t 
 bool fill(const BlockGemmArgs& a, BlockGemmParams& prm) {
   memset(static_cast<void*>(&prm), 0, sizeof(prm));
   BlockGemmDev& g = prm.g;
-  if (a.M > 0x7fffffff || a.N > 0x7fffffff || a.K > 0x7fffffff) return false;
+  constexpr int64_t kMost = int64_t(1) << 30;  // tile coordinates are 32-bit, rounded up to whole tiles
+  if (a.M > kMost || a.N > kMost || a.K > kMost) return false;
   g.M = a.M;
   g.N = a.N;
   g.K = a.K;

@@ -220,6 +220,7 @@ __global__ void __launch_bounds__(quant_threads<T, COL>()) block_quantize_kernel
     }
     __syncthreads();
     const int64_t mp = (a.M + 31) / 32 * 32;
+    const int64_t pitch_t = a.pitch_t ? a.pitch_t : mp / 2;
     const int64_t groups = scale_groups(FMT, mp);
     const int64_t g0 = r0 / kBlk / 4;
     const int n = int(min(int64_t(kScaleBytes), (groups - g0) * 512));
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(quant_threads<T, COL>()) block_quantize_kernel
     for (int u = int(threadIdx.x); u < kColTile * 4; u += THREADS) {
       const int c = u / 4, rb = u % 4;
       if (c0 + c < a.N && r0 + rb * 32 < mp)
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.codes_t) + ((c0 + c) * mp + r0) / 2 + rb * 16) =
+        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.codes_t) + (c0 + c) * pitch_t + r0 / 2 + rb * 16) =
             *reinterpret_cast<const uint4*>(stage + c * kStagePitch + rb * 16);
     }
     if (a.partials)

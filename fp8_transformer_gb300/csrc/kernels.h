@@ -144,6 +144,7 @@ struct BlockQuantArgs {
   void* codes = nullptr;    // [M, N] packed along N, or null
   void* scales = nullptr;
   void* codes_t = nullptr;  // [N, pad32(M)] packed along M, or null
+  int64_t pitch_t = 0;      // bytes from one row of codes_t to the next (0: none between them)
   void* scales_t = nullptr;
   const float* scale = nullptr;    // NVFP4: the tensor scale given (delayed scaling)
   const float* amax_in = nullptr;  // NVFP4: derive the tensor scale from this amax
@@ -223,6 +224,7 @@ struct BlockGemmArgs {
   const void* b_scales = nullptr;
   int fmt = TE_MXFP4;
   int64_t M = 0, N = 0, K = 0;     // K a multiple of 32, N of 16
+  int64_t b_pitch = 0;             // bytes from one row of B to the next, a multiple of 16 (0: K / 2)
   const float* a_scale_inv = nullptr;
   const float* b_scale_inv = nullptr;
   const void* bias = nullptr;      // [N]
@@ -302,8 +304,9 @@ class PerDevice {
 
 // 2-D TMA tensor map over a row-major [outer, inner] matrix of dtype, boxes of
 // box_inner x box_outer elements, a swizzle of 128 or 64 bytes or none (0), out-of-bounds reads zero.
+// pitch: bytes from row to row (0: none between them).
 bool make_tmap_2d(CUtensorMap* tm, const void* ptr, int dtype, uint64_t inner, uint64_t outer,
-                  uint32_t box_inner, uint32_t box_outer, int swizzle);
+                  uint32_t box_inner, uint32_t box_outer, int swizzle, uint64_t pitch = 0);
 
 // 2-D TMA tensor map over block scales: rows of tiles by 512-byte tiles, boxes of box_rows rows
 // of tiles x box_tiles tiles, out-of-bounds reads zero.

@@ -31,7 +31,7 @@ EncodeTiledFn encode_fn() {
 }  // namespace
 
 bool make_tmap_2d(CUtensorMap* tm, const void* ptr, int dtype, uint64_t inner, uint64_t outer,
-                  uint32_t box_inner, uint32_t box_outer, int swizzle) {
+                  uint32_t box_inner, uint32_t box_outer, int swizzle, uint64_t pitch) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
   CUtensorMapDataType dt = dtype == TE_BF16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
@@ -39,7 +39,7 @@ bool make_tmap_2d(CUtensorMap* tm, const void* ptr, int dtype, uint64_t inner, u
                                               : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   const int esize = dtype == TE_BF16 ? 2 : dtype == TE_E4M3 ? 1 : 4;
   cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {inner * esize};
+  cuuint64_t strides[1] = {pitch ? pitch : inner * esize};
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
   return fn(tm, dt, 2, const_cast<void*>(ptr), dims, strides, box, estr,

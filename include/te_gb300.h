@@ -428,7 +428,7 @@ te_status te_block_dequantize(const void* codes, const void* scales, te_block_fo
  *   A [M, K] and B [N, K] packed along K in one 4-bit format; products and sums in fp32.
  *   a_scale_inv, b_scale_inv  device fp32 scalars or NULL (= 1); alpha is their product.
  *   bias [N] in bias_dtype (TE_F32 / TE_BF16) or NULL; D [M, N] in d_dtype (TE_F32 / TE_BF16).
- * The result does not vary between calls.  N a multiple of 16, K of 32; M, N, K below 2^31. */
+ * The result does not vary between calls.  N a multiple of 16, K of 32; M, N, K at most 2^30. */
 te_status te_block_gemm(const void* A, const void* a_scales, const void* B, const void* b_scales,
                         te_block_format format, int64_t M, int64_t N, int64_t K,
                         const float* a_scale_inv, const float* b_scale_inv, const void* bias,
@@ -439,7 +439,7 @@ te_status te_block_gemm(const void* A, const void* a_scales, const void* B, cons
  *   x [M, K], out [M, N], bias [N] or NULL in dtype (TE_F32 / TE_BF16).
  *   kernel, kernel_scales  the kernel's transpose [N, K] packed along K (te_block_quantize's
  *       codes_t of a kernel stored [K, N]); kernel_scale_inv its NVFP4 factor or NULL.
- *   q   NVFP4: x's quantizer, scale_inv required.  MX: NULL.
+ *   q   NVFP4: x's quantizer, scale_inv required and not kernel_scale_inv.  MX: NULL.
  *   saved_xt, saved_xt_scales  NULL, or where x^T packed along the rows of x goes (codes_t,
  *       scales_t of te_block_quantize), for te_dense_fp4_bwd.
  *   workspace  te_workspace_size(TE_OP_DENSE_FP4_FWD, M, K, N, ...) bytes, 16-byte aligned; not
@@ -457,7 +457,7 @@ te_status te_dense_fp4_fwd(const void* x, te_dtype dtype, const void* kernel,
  *   dy [M, N], dx [M, K], dkernel [K, N] in dtype (TE_F32 / TE_BF16); dbias [N] fp32 or NULL.
  *   kernel, kernel_scales  the kernel [K, N] packed along N (te_block_quantize's codes).
  *   saved_xt, saved_xt_scales  from te_dense_fp4_fwd, x_scale_inv its NVFP4 factor or NULL.
- *   q   NVFP4: dy's quantizer, scale_inv required.  MX: NULL.
+ *   q   NVFP4: dy's quantizer, scale_inv required and none of the other factors.  MX: NULL.
  *   workspace  te_workspace_size(TE_OP_DENSE_FP4_BWD, M, K, N, ...) bytes, 16-byte aligned.
  * K and N multiples of 32.  M = 0 zeroes dkernel and dbias. */
 te_status te_dense_fp4_bwd(const void* dy, te_dtype dtype, const void* kernel,

@@ -78,7 +78,7 @@ def test_gemm_refusals():
                dict(bias=P, bdt=b.TE_E4M3)):
         assert f(**kw) == b.TE_ERR_INVALID_ARG, kw
     for kw in (dict(fmt=b.TE_MXFP8), dict(N=24), dict(K=48), dict(a=ODD), dict(bias=ODD), dict(ia=P + 1),
-               dict(M=1 << 31), dict(K=1 << 31)):
+               dict(M=(1 << 30) + 1), dict(N=(1 << 30) + 16), dict(K=1 << 31)):
         assert f(**kw) == b.TE_ERR_UNSUPPORTED, kw
 
 
@@ -95,6 +95,9 @@ def test_dense_refusals():
     assert fwd(M=9, ws=None) == b.TE_ERR_WORKSPACE and fwd(M=9, n=100) == b.TE_ERR_WORKSPACE
     assert fwd(xt=P, xts=P, ws=None) == b.TE_ERR_WORKSPACE
     assert fwd(M=0) == b.TE_OK
+    # the call's own factor in the place of the kernel's
+    assert te.lib().te_dense_fp4_fwd(P, b.TE_BF16, P, P, b.TE_NVFP4, quantizer(inv=P + 64), P + 64, None, 4, 64, 64, P, None,
+                                     None, P, big, None) == b.TE_ERR_INVALID_ARG
 
     def bwd(dy=P, dw=P, fmt=b.TE_MXFP4, q=None, M=4, K=64, N=64, db=None, ws=P, n=big):
         return te.lib().te_dense_fp4_bwd(dy, b.TE_BF16, P, P, P, P, fmt, q, None, None, M, K, N, P, dw, db, ws, n, None)
@@ -102,6 +105,9 @@ def test_dense_refusals():
         assert bwd(**kw) == b.TE_ERR_INVALID_ARG, kw
     for kw in (dict(fmt=b.TE_MXFP8), dict(N=80), dict(K=16), dict(dy=ODD), dict(db=P + 2)):
         assert bwd(**kw) == b.TE_ERR_UNSUPPORTED, kw
+    for fac in ((P + 64, None), (None, P + 64)):
+        assert te.lib().te_dense_fp4_bwd(P, b.TE_BF16, P, P, P, P, b.TE_NVFP4, quantizer(inv=P + 64), *fac, 4, 64, 64, P, P,
+                                         None, P, big, None) == b.TE_ERR_INVALID_ARG
     assert bwd(ws=None) == b.TE_ERR_WORKSPACE and bwd(n=100) == b.TE_ERR_WORKSPACE
 
 

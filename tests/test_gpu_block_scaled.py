@@ -246,7 +246,8 @@ def values(x, fmt, s):
 
 @pytest.mark.parametrize("fmt,mode", [("mxfp4", None), ("nvfp4", "current"), ("nvfp4", "delayed")])
 @pytest.mark.parametrize("M,K,N,dtype", [(1, 64, 96, torch.bfloat16), (50, 544, 288, torch.float32),
-                                         (333, 320, 608, torch.bfloat16), (1, 4096, 320, torch.bfloat16)])
+                                         (333, 320, 608, torch.bfloat16), (1, 4096, 320, torch.bfloat16),
+                                         (1030, 160, 288, torch.bfloat16), (1100, 96, 64, torch.float32)])
 def test_dense_forward_and_backward_together(fmt, mode, M, K, N, dtype):
     """Weights packed once along both axes, the forward keeping x^T, the backward from that."""
     x, dy = draw(M, K, dtype, 1, spread=False), draw(M, N, dtype, 2, spread=False)
