@@ -481,6 +481,78 @@ def test_on_another_stream_without_a_workspace_of_its_own():
     assert all(torch.equal(want, o) for o in outs)
 
 
+def test_two_host_threads_at_once():
+    """Calls of two threads on one stream interleave; each has a workspace of its own."""
+    import threading
+    fmt, M, K, N = "nvfp4", 40, 1024, 256
+    cb, sb, ib, _, _ = packed(N, K, fmt, 5)
+    xs = [draw(M, K, torch.bfloat16, s, spread=False) for s in (1, 2)]
+    qs = [te.Quantizer(mode="current") for _ in xs]
+    call = lambda i, o: te.te_dense_fp4_fwd(xs[i], cb, sb, o, fmt, q=qs[i], kernel_scale_inv=ib)
+    want = [call(i, torch.empty(M, N, dtype=torch.bfloat16, device=DEV)) for i in (0, 1)]
+    outs = [[torch.empty(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(100)] for _ in xs]
+
+    def work(i):
+        for o in outs[i]:
+            call(i, o)
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert all(torch.equal(o, want[i]) for o in outs[i])
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: the last rows are what they are alone."""
+    M, N = 66000, 32768 + 512
+    x = torch.empty(M, N, dtype=torch.bfloat16, device=DEV)
+    for r in range(0, M, 8000):
+        x[r:r + 8000].normal_()
+    last = slice(M - 80, M)
+    tile = slice(M // 128 * 128, M)
+    for fmt in ("mxfp8", "mxfp4"):
+        codes, scales = te.block_empty(fmt, M, N)
+        ct = st = None
+        if fmt == "mxfp4":
+            mp = (M + 31) // 32 * 32
+            ct, st = te.block_empty(fmt, N, mp)
+        te.te_block_quantize(x, fmt, codes, scales, ct, st)
+        own = x[tile].contiguous()
+        c2, s2 = te.block_empty(fmt, own.shape[0], N)
+        te.te_block_quantize(own, fmt, c2, s2)
+        assert torch.equal(codes[tile], c2)
+        assert torch.equal(scales[-s2.numel():], s2)
+        back = te.te_block_dequantize(codes, scales, fmt, torch.empty_like(x))
+        b2 = te.te_block_dequantize(c2, s2, fmt, torch.empty_like(own))
+        assert torch.equal(back[tile], b2)
+        if fmt == "mxfp8":
+            dy = back  # any values
+            dx, a = torch.empty_like(x), torch.empty_like(x)
+            te.te_dact_dbias_ckpt(dy, codes, scales, "silu", dx, act_out=a)
+            d2, a2 = torch.empty_like(own), torch.empty_like(own)
+            te.te_dact_dbias_ckpt(dy[tile].contiguous(), c2, s2, "silu", d2, act_out=a2)
+            assert torch.equal(dx[tile], d2) and torch.equal(a[tile], a2)
+            del dx, a, dy
+        else:
+            t2, u2 = te.block_empty(fmt, 128, mp)
+            te.te_block_quantize(x[:, -128:].contiguous(), fmt, codes_t=t2, scales_t=u2)
+            assert torch.equal(ct[-128:], t2)
+        del back
+    # a product with that many outputs: columns of a small one
+    K = 64
+    A, B = te.block_empty("mxfp4", M, K), te.block_empty("mxfp4", N, K)
+    te.te_block_quantize(draw(M, K, torch.bfloat16, 1, spread=False), "mxfp4", *A)
+    te.te_block_quantize(draw(N, K, torch.bfloat16, 2, spread=False), "mxfp4", *B)
+    te.te_block_gemm(*A, *B, x, "mxfp4")
+    small = torch.empty(M, 128, dtype=torch.bfloat16, device=DEV)
+    te.te_block_gemm(*A, B[0][-128:].contiguous(), B[1][-512:].contiguous(), small, "mxfp4")
+    assert torch.equal(x[:, -128:][last], small[last])
+    assert te.get_device_status() == 0
+
+
 def test_tensors_the_binding_refuses():
     x = draw(32, 64, torch.bfloat16)
     c, s = te.block_empty("mxfp4", 32, 64)
