@@ -115,6 +115,13 @@ __device__ __forceinline__ float nv_scale_from_amax(float amax) {
   return isfinite(s) ? s : 3.4028234663852886e38f;
 }
 
+// max(m, |a|, |b|), NaN if one is: the largest magnitude of two more values in one instruction.
+__device__ __forceinline__ float max_abs3(float m, float a, float b) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+  return r;
+}
+
 // 8 neighbours of T as fp32.
 template <typename T>
 struct Eight;
@@ -136,9 +143,12 @@ struct Eight<__nv_bfloat16> {
   }
   // its bits, those of a NaN above all others
   __device__ __forceinline__ uint32_t amax_bits() const {
-    constexpr uint32_t k = 0x7fff7fffu;
-    const uint32_t m = __vmaxu2(__vmaxu2(u.x & k, u.y & k), __vmaxu2(u.z & k, u.w & k));
-    return max(m << 16, m & 0xffff0000u);
+    float v[8];
+    get(v);
+    float m = max_abs3(v[0], v[1], v[2]);
+    m = max_abs3(m, v[3], v[4]);
+    m = max_abs3(m, v[5], v[6]);
+    return __float_as_uint(max_abs3(m, v[7], 0.0f));
   }
 };
 template <>
@@ -164,9 +174,12 @@ struct Eight<float> {
                  fmaxf(fmaxf(f(b.x), f(b.y)), fmaxf(f(b.z), f(b.w))));
   }
   __device__ __forceinline__ uint32_t amax_bits() const {
-    constexpr uint32_t k = 0x7fffffffu;
-    return max(max(max(a.x & k, a.y & k), max(a.z & k, a.w & k)),
-               max(max(b.x & k, b.y & k), max(b.z & k, b.w & k)));
+    float v[8];
+    get(v);
+    float m = max_abs3(v[0], v[1], v[2]);
+    m = max_abs3(m, v[3], v[4]);
+    m = max_abs3(m, v[5], v[6]);
+    return __float_as_uint(max_abs3(m, v[7], 0.0f));
   }
 };
 

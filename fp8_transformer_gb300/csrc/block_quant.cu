@@ -35,11 +35,23 @@ struct Strip<__nv_bfloat16> {
   // bits of the largest magnitudes of rows [r0, r0 + N), one a column
   template <int N>
   __device__ __forceinline__ void amax_bits(int r0, uint32_t (&m)[2]) const {
-    uint32_t t = 0;
+    // 32 rows: both columns at once in 16 bits (73 us against 77, MXFP4 8190 x 14336 both ways), 16
+    // rows: in fp32, three values an instruction (80 us against 93 for NVFP4)
+    if constexpr (N == 32) {
+      uint32_t t = 0;
 #pragma unroll
-    for (int r = 0; r < N; ++r) t = __vmaxu2(t, w[r0 + r] & 0x7fff7fffu);
-    m[0] = t << 16;
-    m[1] = t & 0xffff0000u;
+      for (int r = 0; r < N; ++r) t = __vmaxu2(t, w[r0 + r] & 0x7fff7fffu);
+      m[0] = t << 16;
+      m[1] = t & 0xffff0000u;
+    } else {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float t = 0.0f;
+#pragma unroll
+        for (int r = 0; r < N; r += 2) t = max_abs3(t, at(k, r0 + r), at(k, r0 + r + 1));
+        m[k] = __float_as_uint(t);
+      }
+    }
   }
 };
 template <>
@@ -53,9 +65,10 @@ struct Strip<float> {
   __device__ __forceinline__ float at(int, int r) const { return v[r]; }
   template <int N>
   __device__ __forceinline__ void amax_bits(int r0, uint32_t (&m)[1]) const {
-    m[0] = 0;
+    float t = 0.0f;
 #pragma unroll
-    for (int r = 0; r < N; ++r) m[0] = max(m[0], __float_as_uint(v[r0 + r]) & 0x7fffffffu);
+    for (int r = 0; r < N; r += 2) t = max_abs3(t, v[r0 + r], v[r0 + r + 1]);
+    m[0] = __float_as_uint(t);
   }
 };
 
@@ -115,6 +128,7 @@ __global__ void __launch_bounds__(quant_threads<T, COL>()) block_quantize_kernel
   const int64_t pitch = a.N / codes_per_byte(FMT);
   uint8_t* codes = static_cast<uint8_t*>(a.codes) + r0 * pitch + (c0 + cl) / codes_per_byte(FMT);
   uint32_t amax = 0;
+  const int rows = col_ok ? int(min(int64_t(SUB), a.M - r0)) : 0;  // of this lane's column
 #pragma unroll 1
   for (int p0 = 0; p0 < kPasses; p0 += kBatch) {
     Eight<T> e[kBatch][kPer];
@@ -123,7 +137,7 @@ __global__ void __launch_bounds__(quant_threads<T, COL>()) block_quantize_kernel
       const int r = (p0 + j) * kRowsPass + rl;
 #pragma unroll
       for (int k = 0; k < kPer; ++k) {
-        if (col_ok && r0 + r < a.M) e[j][k].load(x + int64_t(r) * a.N + 8 * k);
+        if (r < rows) e[j][k].load(x + int64_t(r) * a.N + 8 * k);
         else e[j][k].zero();
       }
     }
@@ -141,7 +155,7 @@ __global__ void __launch_bounds__(quant_threads<T, COL>()) block_quantize_kernel
       for (int o = 1; o * 8 * kPer < kBlk; o *= 2) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
       if (a.amax_out) amax = max(amax, m <= kInfBits ? m : 0u);  // blocks with a NaN left out
       if (!COL || a.codes) {
-        const bool in = col_ok && r0 + r < a.M;
+        const bool in = r < rows;
         const BlockScale b = block_scale<FMT>(m, s, factors);
         if (in) {
           uint2 c[kPer];
