@@ -116,7 +116,10 @@ __global__ void __launch_bounds__(quant_threads<T, COL>()) block_quantize_kernel
     __syncthreads();
   }
   const int64_t tiles_c = (a.N + TC - 1) / TC;
-  const int64_t st = blockIdx.x / tiles_c, ct = blockIdx.x % tiles_c;
+  // after a pass for the amax the last tiles first: those of them that it left in L2 are read there
+  // (8190 x 14336 bf16 with that pass 91 -> 82 us, both ways 128 -> 123)
+  const int64_t tile_id = FMT == TE_NVFP4 && a.amax_in ? int64_t(gridDim.x) - 1 - blockIdx.x : int64_t(blockIdx.x);
+  const int64_t st = tile_id / tiles_c, ct = tile_id % tiles_c;
   const int64_t rt = st / (kTileRows / SUB);
   const int sub = int(st % (kTileRows / SUB));
   const int64_t r0 = st * SUB, c0 = ct * TC;
@@ -291,7 +294,7 @@ te_status launch_quant_t(const BlockQuantArgs& a, cudaStream_t s) {
 // max |x| of `vectors` vectors of 8, NaN ignored, by one integer atomic a CTA.  Four vectors a thread
 // are in flight; all of a wave's threads stride together.
 constexpr int kAmaxBatch = 4;
-constexpr int kAmaxCtas = 4;  // CTAs of an SM
+constexpr int kAmaxCtas = 8;  // CTAs of an SM
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) amax_kernel(const void* x, int64_t vectors, float* amax_out) {
