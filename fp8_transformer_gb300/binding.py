@@ -204,10 +204,10 @@ def _dt(t) -> int:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream):
+def _stream(stream, dev=None):
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(torch.cuda.current_device() if dev is None else dev)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream
 
@@ -601,7 +601,8 @@ def _workspace(op, M, H, N, like, workspace, stream):
     if workspace is None:
         n = max(_sized(op, M, H, N), 1)
         if n <= _SMALL_WORKSPACE and stream is None and not torch.cuda.is_current_stream_capturing():
-            key = (like.get_device(), _stream(None))
+            dev = like.get_device()
+            key = (dev, _stream(None, dev))
             kept = _small.__dict__.setdefault("kept", {})
             workspace = kept.get(key)
             if workspace is None:
@@ -639,7 +640,7 @@ def te_block_quantize(x, fmt, codes=None, scales=None, codes_t=None, scales_t=No
     if codes_t is not None:
         pct, pst = _packed("codes_t", codes_t, scales_t, f, N, (M + 31) // 32 * 32, dev)
     st = lib().te_block_quantize(px, _dt(x), M, N, f, _tensor_scale(f, q, dev), pc, ps, pct, pst,
-                                 _stream(stream))
+                                 _stream(stream, dev))
     _check("te_block_quantize", st)
 
 
@@ -650,7 +651,7 @@ def te_block_dequantize(codes, scales, fmt, out, scale_inv=None, stream=None):
     po = _arg("out", out, (M, N), _ACT_DTYPES, dev)
     pc, ps = _packed("codes", codes, scales, f, M, N, dev)
     st = lib().te_block_dequantize(pc, ps, f, _scalar("scale_inv", scale_inv, dev), M, N, po, _dt(out),
-                                   _stream(stream))
+                                   _stream(stream, dev))
     _check("te_block_dequantize", st)
     return out
 
@@ -667,7 +668,7 @@ def te_block_gemm(a, a_scales, b, b_scales, out, fmt, a_scale_inv=None, b_scale_
     pz = None if bias is None else _arg("bias", bias, (N,), _ACT_DTYPES, dev)
     st = lib().te_block_gemm(pa, psa, pb, psb, f, M, N, K, _scalar("a_scale_inv", a_scale_inv, dev),
                              _scalar("b_scale_inv", b_scale_inv, dev), pz,
-                             TE_F32 if bias is None else _dt(bias), po, _dt(out), _stream(stream))
+                             TE_F32 if bias is None else _dt(bias), po, _dt(out), _stream(stream, dev))
     _check("te_block_gemm", st)
     return out
 
@@ -692,7 +693,7 @@ def te_dense_fp4_fwd(x, kernel, kernel_scales, out, fmt, bias=None, q=None, kern
     if M > 8 or saved_xt is not None or workspace is not None:
         workspace, pw, nw = _workspace(TE_OP_DENSE_FP4_FWD, M, K, N, x, workspace, stream)
     st = lib().te_dense_fp4_fwd(px, _dt(x), pk, psk, f, cq, _scalar("kernel_scale_inv", kernel_scale_inv, dev),
-                                pz, M, K, N, po, pt, pst, pw, nw, _stream(stream))
+                                pz, M, K, N, po, pt, pst, pw, nw, _stream(stream, dev))
     _check("te_dense_fp4_fwd", st)
     return out
 
@@ -716,7 +717,7 @@ def te_dense_fp4_bwd(dy, kernel, kernel_scales, saved_xt, saved_xt_scales, dx, d
     st = lib().te_dense_fp4_bwd(py, _dt(dy), pk, psk, pt, pst, f, cq,
                                 _scalar("kernel_scale_inv", kernel_scale_inv, dev),
                                 _scalar("x_scale_inv", x_scale_inv, dev), M, K, N, px, pw, pz, pws, nws,
-                                _stream(stream))
+                                _stream(stream, dev))
     _check("te_dense_fp4_bwd", st)
     return dx
 
@@ -738,7 +739,7 @@ def te_dact_dbias_ckpt(dy, codes, scales, act, dx, dbias=None, act_out=None, q=N
         pb = _arg("dbias", dbias, (N_in,), _F32, dev)
         workspace, pws, nws = _workspace(TE_OP_DACT_DBIAS, M, 0, N_in, dy, workspace, stream)
     st = lib().te_dact_dbias_ckpt(py, pc, ps, _dt(dy), M, N_in, a, _qp(q), px, _dt(dx), pa, pb, pws, nws,
-                                  _stream(stream))
+                                  _stream(stream, dev))
     _check("te_dact_dbias_ckpt", st)
     return dx
 
@@ -764,7 +765,7 @@ def te_layernorm_mlp_fwd_ckpt(x, gamma, beta, kernel1, kernel2, bias1, bias2, ou
                                          int(bool(zero_centered_gamma)), float(epsilon), act,
                                          ctypes.byref(qs) if qs is not None else None, M, H, F, dt, _ptr(out),
                                          pc, ps, _ptr(saved_act), _ptr(saved_ln_out), _ptr(mu), _ptr(rsigma),
-                                         _ptr(workspace), workspace.numel(), _stream(stream))
+                                         _ptr(workspace), workspace.numel(), _stream(stream, dev))
     _check("te_layernorm_mlp_fwd_ckpt", st)
     return out
 
@@ -790,6 +791,6 @@ def te_layernorm_mlp_bwd_ckpt(dy, x, gamma, kernel1, kernel2, h_codes, h_scales,
                                          ctypes.byref(qs) if qs is not None else None, M, H, F, dt, _ptr(dx),
                                          _ptr(dgamma), _ptr(dbeta), _ptr(dkernel1), _ptr(dkernel2), _ptr(dbias1),
                                          _ptr(dbias2), _ptr(saved_dh), _ptr(workspace), workspace.numel(),
-                                         _stream(stream))
+                                         _stream(stream, dev))
     _check("te_layernorm_mlp_bwd_ckpt", st)
     return dx
