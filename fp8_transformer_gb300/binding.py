@@ -585,8 +585,29 @@ def _tensor_scale(f, q, dev):
         raise ValueError("q: the quantizer of nvfp4's tensor scale (None for the other formats)")
     if q is None:
         return None
-    return ctypes.byref(_Quantizer(_scalar("q.scale", q.scale, dev), _scalar("q.scale_inv", q.scale_inv, dev),
-                                   _scalar("q.amax", q.amax, dev), q.mode))
+    return ctypes.byref(_quantizer("q", q, dev))
+
+
+def _quantizer(name, q, dev):
+    """The C quantizer, its scalars on the current device (None without one)."""
+    if q is None:
+        return None
+    return _Quantizer(_scalar(name + ".scale", q.scale, dev), _scalar(name + ".scale_inv", q.scale_inv, dev),
+                      _scalar(name + ".amax", q.amax, dev), q.mode)
+
+
+def _quantizer_set(qs, dev):
+    """The same of a set, by reference."""
+    if qs is None:
+        return None
+    z = _Quantizer(None, None, None, 0)
+    return ctypes.byref(_QuantizerSet(*(_quantizer(k, getattr(qs, k), dev) or z
+                                        for k in ("x", "kernel1", "act", "kernel2", "grad"))))
+
+
+def _sized_arg(name, t, n, dtypes, dev):
+    """Address of a tensor of n values in any shape, or None without it."""
+    return None if t is None else _arg(name, t.reshape(-1) if t.is_contiguous() else t, (n,), dtypes, dev)
 
 
 _sized = functools.lru_cache(maxsize=1024)(workspace_size)
@@ -738,7 +759,8 @@ def te_dact_dbias_ckpt(dy, codes, scales, act, dx, dbias=None, act_out=None, q=N
     if dbias is not None:
         pb = _arg("dbias", dbias, (N_in,), _F32, dev)
         workspace, pws, nws = _workspace(TE_OP_DACT_DBIAS, M, 0, N_in, dy, workspace, stream)
-    st = lib().te_dact_dbias_ckpt(py, pc, ps, _dt(dy), M, N_in, a, _qp(q), px, _dt(dx), pa, pb, pws, nws,
+    cq = None if q is None else ctypes.byref(_quantizer("q", q, dev))
+    st = lib().te_dact_dbias_ckpt(py, pc, ps, _dt(dy), M, N_in, a, cq, px, _dt(dx), pa, pb, pws, nws,
                                   _stream(stream, dev))
     _check("te_dact_dbias_ckpt", st)
     return dx
@@ -753,19 +775,30 @@ def te_layernorm_mlp_fwd_ckpt(x, gamma, beta, kernel1, kernel2, bias1, bias2, ou
     M, H = x.shape
     F = kernel2.shape[0]
     act, dt, kd, dev = _act_id(activation_type), _dt(x), _dt(kernel1), torch.cuda.current_device()
-    pc, ps = _packed("h_codes", h_codes, h_scales, TE_MXFP8, M, 2 * F if act >= TE_SWIGLU else F, dev)
+    F1 = 2 * F if act >= TE_SWIGLU else F
+    pc, ps = _packed("h_codes", h_codes, h_scales, TE_MXFP8, M, F1, dev)
+    d = (x.dtype,)
+    e = _E4M3_BYTES if quantizer_set is not None else d
+    k = _E4M3_BYTES if kd == TE_E4M3 else (kernel1.dtype,)
+    px = _arg("x", x, (M, H), _ACT_DTYPES, dev)
+    pg, pbe = _sized_arg("gamma", gamma, H, d, dev), _sized_arg("beta", beta, H, d, dev)
+    p1, p2 = _sized_arg("kernel1", kernel1, H * F1, k, dev), _sized_arg("kernel2", kernel2, F * H, k, dev)
+    pb1, pb2 = _sized_arg("bias1", bias1, F1, d, dev), _sized_arg("bias2", bias2, H, d, dev)
+    po = _arg("out", out, (M, H), d, dev)
+    pa, pl = _sized_arg("saved_act", saved_act, M * F, e, dev), _sized_arg("saved_ln_out", saved_ln_out, M * H, e, dev)
+    pm, pr = _sized_arg("mu", mu, M, _F32, dev), _sized_arg("rsigma", rsigma, M, _F32, dev)
+    qs = _quantizer_set(quantizer_set, dev)
     if workspace is None:
         workspace = _ws(workspace_size(TE_OP_LAYERNORM_MLP_FWD, M, H, F, dt, quantizer_set is not None, kd, act),
                         x.device)
         if stream is not None:
             workspace.record_stream(stream)
-    qs = quantizer_set.c() if quantizer_set is not None else None
-    st = lib().te_layernorm_mlp_fwd_ckpt(_ptr(x), _ptr(gamma), _ptr(beta), _ptr(kernel1), _ptr(kernel2), kd,
-                                         _ptr(bias1), _ptr(bias2), _norm_id(norm_type),
-                                         int(bool(zero_centered_gamma)), float(epsilon), act,
-                                         ctypes.byref(qs) if qs is not None else None, M, H, F, dt, _ptr(out),
-                                         pc, ps, _ptr(saved_act), _ptr(saved_ln_out), _ptr(mu), _ptr(rsigma),
-                                         _ptr(workspace), workspace.numel(), _stream(stream, dev))
+    elif workspace.get_device() != dev:
+        raise ValueError("workspace: on the device of the other tensors")
+    st = lib().te_layernorm_mlp_fwd_ckpt(px, pg, pbe, p1, p2, kd, pb1, pb2, _norm_id(norm_type),
+                                         int(bool(zero_centered_gamma)), float(epsilon), act, qs, M, H, F, dt, po,
+                                         pc, ps, pa, pl, pm, pr, _ptr(workspace), workspace.numel(),
+                                         _stream(stream, dev))
     _check("te_layernorm_mlp_fwd_ckpt", st)
     return out
 
@@ -778,19 +811,32 @@ def te_layernorm_mlp_bwd_ckpt(dy, x, gamma, kernel1, kernel2, h_codes, h_scales,
     M, H = x.shape
     F = kernel2.shape[0]
     act, dt, kd, dev = _act_id(activation_type), _dt(x), _dt(kernel1), torch.cuda.current_device()
-    pc, ps = _packed("h_codes", h_codes, h_scales, TE_MXFP8, M, 2 * F if act >= TE_SWIGLU else F, dev)
+    F1 = 2 * F if act >= TE_SWIGLU else F
+    pc, ps = _packed("h_codes", h_codes, h_scales, TE_MXFP8, M, F1, dev)
+    d = (x.dtype,)
+    e = _E4M3_BYTES if quantizer_set is not None else d
+    k = _E4M3_BYTES if kd == TE_E4M3 else (kernel1.dtype,)
+    py, px = _arg("dy", dy, (M, H), d, dev), _arg("x", x, (M, H), _ACT_DTYPES, dev)
+    pg = _sized_arg("gamma", gamma, H, d, dev)
+    p1, p2 = _sized_arg("kernel1", kernel1, H * F1, k, dev), _sized_arg("kernel2", kernel2, F * H, d, dev)
+    pl = _sized_arg("saved_ln_out", saved_ln_out, M * H, e, dev)
+    pm, pr = _sized_arg("mu", mu, M, _F32, dev), _sized_arg("rsigma", rsigma, M, _F32, dev)
+    pdx = _arg("dx", dx, (M, H), d, dev)
+    pdg, pdb = _sized_arg("dgamma", dgamma, H, _F32, dev), _sized_arg("dbeta", dbeta, H, _F32, dev)
+    pd1, pd2 = _sized_arg("dkernel1", dkernel1, H * F1, d, dev), _sized_arg("dkernel2", dkernel2, F * H, d, dev)
+    pb1, pb2 = _sized_arg("dbias1", dbias1, F1, _F32, dev), _sized_arg("dbias2", dbias2, H, _F32, dev)
+    pdh = _sized_arg("saved_dh", saved_dh, M * F1, e, dev)
+    qs = _quantizer_set(quantizer_set, dev)
     if workspace is None:
         workspace = _ws(workspace_size(TE_OP_LAYERNORM_MLP_BWD, M, H, F, dt, quantizer_set is not None, kd, act),
                         x.device)
         if stream is not None:
             workspace.record_stream(stream)
-    qs = quantizer_set.c() if quantizer_set is not None else None
-    st = lib().te_layernorm_mlp_bwd_ckpt(_ptr(dy), _ptr(x), _ptr(gamma), _ptr(kernel1), _ptr(kernel2), kd, pc, ps,
-                                         _ptr(saved_ln_out), _ptr(mu), _ptr(rsigma), _norm_id(norm_type),
-                                         int(bool(zero_centered_gamma)), act,
-                                         ctypes.byref(qs) if qs is not None else None, M, H, F, dt, _ptr(dx),
-                                         _ptr(dgamma), _ptr(dbeta), _ptr(dkernel1), _ptr(dkernel2), _ptr(dbias1),
-                                         _ptr(dbias2), _ptr(saved_dh), _ptr(workspace), workspace.numel(),
+    elif workspace.get_device() != dev:
+        raise ValueError("workspace: on the device of the other tensors")
+    st = lib().te_layernorm_mlp_bwd_ckpt(py, px, pg, p1, p2, kd, pc, ps, pl, pm, pr, _norm_id(norm_type),
+                                         int(bool(zero_centered_gamma)), act, qs, M, H, F, dt, pdx, pdg, pdb, pd1,
+                                         pd2, pb1, pb2, pdh, _ptr(workspace), workspace.numel(),
                                          _stream(stream, dev))
     _check("te_layernorm_mlp_bwd_ckpt", st)
     return dx

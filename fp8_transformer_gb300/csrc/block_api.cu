@@ -20,9 +20,13 @@ bool format_quantizer_ok(int f, const te_quantizer* q) {
   return f == TE_NVFP4 ? enabled(q) && quantizer_ok(q) : q == nullptr;
 }
 
-// A product's quantizer writes its factor, which cannot be the one of an operand packed before.
+// A product's quantizer writes its factor and its amax, with current scaling its scale too: none of
+// them can be the factor of an operand packed before.
 bool factor_ok(const te_quantizer* q, const float* other) {
-  return !q || (q->scale_inv && q->scale_inv != other);
+  if (!q) return true;
+  if (!q->scale_inv) return false;
+  return !other || (q->scale_inv != other && q->amax != other &&
+                    (q->mode != TE_SCALING_CURRENT || q->scale != other));
 }
 
 // Gives a its tensor scale's places; NVFP4 finds this call's amax first when the scale is to come

@@ -439,7 +439,8 @@ te_status te_block_gemm(const void* A, const void* a_scales, const void* B, cons
  *   x [M, K], out [M, N], bias [N] or NULL in dtype (TE_F32 / TE_BF16).
  *   kernel, kernel_scales  the kernel's transpose [N, K] packed along K (te_block_quantize's
  *       codes_t of a kernel stored [K, N]); kernel_scale_inv its NVFP4 factor or NULL.
- *   q   NVFP4: x's quantizer, scale_inv required and not kernel_scale_inv.  MX: NULL.
+ *   q   NVFP4: x's quantizer, scale_inv required; what the call writes (scale_inv, amax, with
+ *       current scaling scale) is not kernel_scale_inv.  MX: NULL.
  *   saved_xt, saved_xt_scales  NULL, or where x^T packed along the rows of x goes (codes_t,
  *       scales_t of te_block_quantize), for te_dense_fp4_bwd.
  *   workspace  te_workspace_size(TE_OP_DENSE_FP4_FWD, M, K, N, ...) bytes, 16-byte aligned; not

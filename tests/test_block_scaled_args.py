@@ -128,3 +128,16 @@ def test_the_bindings_scale_size_is_the_librarys():
         for rows in (0, 1, 127, 128, 129, 1000):
             for cols in (32, 64, 96, 128, 160, 4096):
                 assert b._scale_size(f, rows, cols) == te.lib().te_block_scale_bytes(f, rows, cols)
+
+
+@pytest.mark.parametrize("q,ok", [(dict(), False), (dict(inv=P + 64), False), (dict(inv=P + 64, amax=P + 128), True),
+                                  (dict(inv=P + 64, amax=P + 128, mode=b.TE_SCALING_CURRENT), False)])
+def test_a_factor_that_the_call_would_write(q, ok):
+    """The kernel's factor at P in a quantizer's own places (scale at P by default): refused where the call writes
+    there; a delayed scale is only read.  Valid calls are stopped by their missing workspace."""
+    want = b.TE_ERR_WORKSPACE if ok else b.TE_ERR_INVALID_ARG
+    for k, x in ((P, None), (None, P)):
+        assert te.lib().te_dense_fp4_bwd(P, b.TE_BF16, P, P, P, P, b.TE_NVFP4, quantizer(**q), k, x, 4, 64, 64, P, P,
+                                         None, None, 0, None) == want
+    assert te.lib().te_dense_fp4_fwd(P, b.TE_BF16, P, P, b.TE_NVFP4, quantizer(**q), P, None, 16, 64, 64, P, None,
+                                     None, None, 0, None) == want

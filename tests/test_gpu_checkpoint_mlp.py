@@ -180,3 +180,32 @@ def test_difference_to_the_uncompressed_gradients_is_the_checkpoints_rounding():
     lip = np.abs(ob.act_bwd(np.ones_like(h), h + 1e-3, "gelu") - ob.act_bwd(np.ones_like(h), h - 1e-3, "gelu")).max() / 2e-3
     bound = np.abs(da) * (lip * 1.5 * np.abs(h - hq)) + 2.0 ** -7 * np.abs(da) * 1.2 + 2e-2
     assert (np.abs(np64(g["dh"]) - ob.act_bwd(da, h, "gelu")) <= bound).all()
+
+
+def test_tensors_the_binding_refuses():
+    """Another device, type or size of any argument is an error on the host."""
+    inp = inputs("gpt_ln_mlp_bwd", None, 16, 64, 96)
+    for mode in (None, "delayed"):
+        f = forward(inp, mode, True)
+        for k in ("x", "gamma", "beta", "w1", "w2"):
+            for bad in (inp[k].cpu(), inp[k].double(), torch.cat([inp[k], inp[k]])):
+                if k == "x" and bad.shape != inp[k].shape:
+                    continue  # another number of rows is another call
+                with pytest.raises((ValueError, KeyError)):
+                    forward(dict(inp, **{k: bad}), mode, True)
+        for k in ("ln", "mu", "rs", "codes", "scales"):
+            for bad in (f[k].cpu(), f[k].double(), f[k][:8].contiguous()):
+                with pytest.raises(ValueError):
+                    backward(inp, dict(f, **{k: bad}))
+        with pytest.raises(ValueError):
+            backward(dict(inp, dy=inp["dy"][:8].contiguous()), f)
+        with pytest.raises(ValueError):
+            backward(inp, f, workspace=torch.empty(1 << 24, dtype=torch.uint8))
+    host = te.Quantizer(2.0, device="cpu")
+    with pytest.raises(ValueError, match="grad.scale"):
+        backward(inp, dict(f, qs=te.QuantizerSet(**dict(vars(f["qs"]), grad=host))))
+    F = inp["F"]
+    c = te.block_empty("mxfp8", 16, F)
+    dy = torch.zeros(16, F, dtype=torch.bfloat16, device=DEV)
+    with pytest.raises(ValueError, match="q.scale"):
+        te.te_dact_dbias_ckpt(dy, *c, "gelu", torch.empty(16, F, dtype=torch.uint8, device=DEV), q=host)
