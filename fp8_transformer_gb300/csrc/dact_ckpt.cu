@@ -58,12 +58,26 @@ __device__ __forceinline__ void decode8(const uint2& c, float f, f32x2 (&h)[4]) 
 // negative argument is exactly zero (and e * s with it) and no product with it can overflow.
 constexpr float kExp2Top = 126.5f;
 
-// act(h) and act'(h) from one exponential and one reciprocal.
+// max and min that hand a NaN on, where fmaxf and fminf drop it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// act(h) and act'(h) from one exponential and one reciprocal.  Both are NaN where h is: the format keeps
+// an infinity as a NaN block, and 32 zero gradients in its place would hide it.  (Here ReLU does so too,
+// unlike the kernels that read h itself, where a NaN counts as not positive.)
 template <int ACT>
 __device__ __forceinline__ void act_both(f32x2 h, f32x2& y, f32x2& d) {
   if constexpr (ACT == TE_RELU) {
-    y = relu2(h);
-    d = drelu2(h);
+    y = f2(max_nan(f2lo(h), 0.0f), max_nan(f2hi(h), 0.0f));
+    d = f2(f2lo(h) > 0.0f ? 1.0f : f2lo(y), f2hi(h) > 0.0f ? 1.0f : f2hi(y));  // y: 0 or NaN there
   } else if constexpr (ACT == TE_SILU) {
     const f32x2 e = ex2_2(min2s(mul2(h, f2s(-kLog2e)), kExp2Top));
     const f32x2 s = rcp2(add2(e, f2s(1.0f)));
@@ -71,7 +85,7 @@ __device__ __forceinline__ void act_both(f32x2 h, f32x2& y, f32x2& d) {
     d = mul2(s, fma2(h, mul2(e, s), f2s(1.0f)));
   } else {
     // beyond +-100 the logistic is 0 or 1 in fp32; the cube must not overflow
-    const f32x2 c = f2(fminf(fmaxf(f2lo(h), -100.0f), 100.0f), fminf(fmaxf(f2hi(h), -100.0f), 100.0f));
+    const f32x2 c = f2(min_nan(max_nan(f2lo(h), -100.0f), 100.0f), min_nan(max_nan(f2hi(h), -100.0f), 100.0f));
     const f32x2 cc = mul2(c, c);
     const f32x2 e = ex2_2(min2s(mul2(c, fma2(cc, f2s(kGeluA2), f2s(kGeluA1))), kExp2Top));
     const f32x2 s = rcp2(add2(e, f2s(1.0f)));

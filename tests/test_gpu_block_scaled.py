@@ -426,6 +426,44 @@ def test_gradient_from_checkpoint_far_from_zero(act):
     assert (np.abs(f64(a) - wa)[fin] <= 1e-5 * np.abs(wa)[fin] + 1e-30).all()
 
 
+@pytest.mark.parametrize("kind", ["f32", "bf16", "e4m3"])
+@pytest.mark.parametrize("act", ACTS)
+def test_gradient_from_a_bad_block_is_nan(act, kind):
+    """A NaN or an infinity makes its block NaN: activation, gradient and column sums say so, and no other
+    block does."""
+    M, F = 130, 96
+    gated = act in ("swiglu", "geglu", "reglu")
+    n_in = 2 * F if gated else F
+    dtype = torch.float32 if kind == "f32" else torch.bfloat16
+    h, dy = draw(M, n_in, dtype, 1, spread=False), draw(M, F, dtype, 2, spread=False)
+    dy[dy == 0] = 1.0
+    h[3, 40] = float("nan")    # block 1 of row 3
+    h[129, 95] = float("inf")  # block 2 of row 129
+    h[70, 0] = float("-inf")   # block 0 of row 70
+    bad = torch.zeros(M, n_in, dtype=torch.bool, device=DEV)  # of h
+    for r, c in ((3, 32), (129, 64), (70, 0)):
+        bad[r, c:c + 32] = True
+    if gated:
+        h[5, F + 33] = float("nan")  # the linear half alone
+        bad[5, F + 32:F + 64] = True
+    codes, scales = te.block_empty("mxfp8", M, n_in)
+    te.te_block_quantize(h, "mxfp8", codes, scales)
+    dx = torch.empty(M, n_in, dtype=torch.uint8 if kind == "e4m3" else dtype, device=DEV)
+    a, db = torch.empty(M, F, dtype=dtype, device=DEV), torch.empty(n_in, device=DEV)
+    q = te.Quantizer(scale=16.0) if kind == "e4m3" else None
+    te.te_dact_dbias_ckpt(dy, codes, scales, act, dx, dbias=db, act_out=a, q=q)
+    dx = dx.view(torch.float8_e4m3fn).float() if kind == "e4m3" else dx.float()
+    # act(gate) * lin and both gradients but the linear half's, dy * act(gate), depend on the linear half
+    of_act = bad[:, :F] | bad[:, F:] if gated else bad
+    of_dx = torch.cat([of_act, bad[:, :F]], 1) if gated else bad
+    assert torch.equal(torch.isnan(a), of_act)
+    assert torch.equal(torch.isnan(dx), of_dx)
+    assert torch.equal(torch.isnan(db), of_dx.any(0))
+    assert torch.isfinite(dx[~of_dx]).all() and torch.isfinite(a[~of_act]).all()
+    if q is not None:
+        assert np.isfinite(q.amax.item()) and q.amax.item() > 0
+
+
 def test_gradient_from_checkpoint_by_differences():
     """dx is the slope of sum(dy * act(h)) at the checkpointed h (central differences, float64)."""
     for act in ("gelu", "silu", "swiglu", "geglu"):

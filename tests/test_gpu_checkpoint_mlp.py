@@ -122,6 +122,28 @@ def test_backward_from_the_checkpoint(name, act, M, H, F, mode):
     check_mlp_bwd(inp, g, mode is not None)
 
 
+@pytest.mark.parametrize("act", ["gelu", "relu", "geglu", "swiglu"])
+@pytest.mark.parametrize("mode", [None, "delayed"])
+def test_an_overflow_before_the_activation_is_not_hidden(act, mode):
+    """An infinite bias of one column: the gradients of its block's 32 columns are NaN, the others finite."""
+    M, H, F = 70, 128, 96
+    inp = inputs("gpt_ln_mlp_bwd" if act in ("gelu", "relu") else "llama_rms_mlp", act, M, H, F)
+    F1 = 2 * F if act in GATED else F
+    b1 = torch.zeros(F1, dtype=torch.bfloat16, device=DEV)
+    b1[37] = float("inf")
+    inp["b1"] = b1
+    f = forward(inp, mode, True)
+    g = backward(inp, f)
+    torch.cuda.synchronize()
+    of_act = torch.zeros(F, dtype=torch.bool, device=DEV)
+    of_act[32:64] = True
+    of_h = torch.cat([of_act, of_act]) if act in GATED else of_act
+    assert torch.equal(torch.isnan(g["db1"]), of_h)
+    assert torch.isnan(g["dw1"][:, of_h]).all() and torch.isnan(g["dw2"][of_act]).all()
+    assert torch.isfinite(g["dw1"][:, ~of_h]).all() and torch.isfinite(g["dw2"][~of_act]).all()
+    assert torch.isfinite(g["db1"][~of_h]).all()
+
+
 def test_backward_is_the_same_on_every_run_and_in_a_graph():
     inp = inputs("llama_rms_mlp", None, 200, 256, 288)
     f = forward(inp, None, True)
