@@ -17,6 +17,7 @@ namespace te {
 
 // Bits of |v| order like the values, infinities above every finite number and NaN above those.
 constexpr uint32_t kInfBits = 0x7f800000u;
+constexpr float kF32Max = 3.4028234663852886e38f;
 
 // The byte of one scale within its row of tiles: tiles of 128 rows x 4 blocks, 512 bytes, in
 // which the rows r, r + 32, r + 64, r + 96 are neighbours.  This is the order in which
@@ -78,11 +79,15 @@ __device__ __forceinline__ float sixth(float t) {
 }
 
 // NVFP4's factors fp32(s / scale) by the scale's byte, made once by the threads of a CTA (a division
-// a block costs as much as the rest of its packing).  Entry 0 is 0: such a block holds zeros.
+// a block costs as much as the rest of its packing).  Entry 0 is 0: such a block holds zeros.  A quotient
+// past the largest float becomes that float: with an infinite factor a zero of the block would turn
+// into NaN, and its code into the largest.
 constexpr int kNvFactors = 128;
 __device__ __forceinline__ void nv_factors(float* table, float s, int thread, int threads) {
-  for (int i = thread; i < kNvFactors; i += threads)
-    table[i] = i == 0 || i == 0x7f ? 0.0f : __fdiv_rn(s, unpack_e4m3x2(uint16_t(i)).x);
+  for (int i = thread; i < kNvFactors; i += threads) {
+    const float f = i == 0 || i == 0x7f ? 0.0f : __fdiv_rn(s, unpack_e4m3x2(uint16_t(i)).x);
+    table[i] = f > kF32Max ? kF32Max : f;
+  }
 }
 
 // factors: nv_factors' table of s (NVFP4 only).
@@ -112,7 +117,7 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float s, c
 __device__ __forceinline__ float nv_scale_from_amax(float amax) {
   if (!(amax > 0.0f) || !isfinite(amax)) return 1.0f;
   const float s = __fdiv_rn(6.0f * kE4M3Max, amax);
-  return isfinite(s) ? s : 3.4028234663852886e38f;
+  return isfinite(s) ? s : kF32Max;
 }
 
 // max(m, |a|, |b|), NaN if one is: the largest magnitude of two more values in one instruction.

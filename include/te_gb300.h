@@ -395,7 +395,8 @@ te_status te_layernorm_dense_bwd(const void* dy, const void* x, const void* gamm
  * Scales and codes of a block with largest magnitude a:
  *   MX     scale = the smallest power of two with a / scale <= 6 (MXFP8: 448), at least 2^-127;
  *          code = round-to-nearest-even of x / scale, which then never saturates.
- *   NVFP4  scale = E4M3(fp32(fp32(a * s) / 6)); code = E2M1(fp32(x * fp32(s / scale))), saturating;
+ *   NVFP4  scale = E4M3(fp32(fp32(a * s) / 6)); code = E2M1(fp32(x * fp32(s / scale))), saturating,
+ *          with FLT_MAX for s / scale where that overflows (s of 2^119 and more);
  *          all zeros where the scale rounds to zero.  The value of a code is
  *          fp32(code * scale * (1 / s)).
  *   A block with an infinity or a NaN gets a NaN scale and zero codes: it reads as NaN.

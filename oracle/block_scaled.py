@@ -62,6 +62,7 @@ def pack(x, fmt, s=None):
         sf = nx.e4m3_decode(sb).astype(np.float32)
         with np.errstate(divide="ignore", over="ignore"):
             e = np.where(sf > 0, s32 / np.where(sf > 0, sf, np.float32(1)), np.float32(0))
+        e = np.where(np.isposinf(e), np.finfo(np.float32).max, e)  # so that a zero stays a zero
         with np.errstate(over="ignore", invalid="ignore"):
             v = (b.astype(np.float32) * e[..., None].astype(np.float32)).astype(np.float64)
         scales = np.where(bad, 0x7F, sb)

@@ -130,6 +130,32 @@ def test_nvfp4_packing_is_exact_with_either_scaling(both, dtype):
     quantize_checked(z, "nvfp4", both, te.Quantizer(mode="current"), 1.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_nvfp4_zeros_beside_tiny_values(dtype):
+    """A tensor so small that s is the largest float and s / scale overflows in its blocks below 1.8e-38:
+    their zeros stay zeros, packed along rows, along columns and inside the product."""
+    x = torch.zeros(40, 96, device=DEV)
+    x[::3, ::5] = 1e-38
+    x[1::4, 3::7] = -1.2e-38
+    x[7, 3] = 2e-36
+    x = x.to(dtype)
+    s = bs.nv_scale(np.abs(f64(x)).max())
+    assert s == np.finfo(np.float32).max
+    quantize_checked(x, "nvfp4", True, te.Quantizer(mode="current"), s)
+    quantize_checked(x, "nvfp4", False, te.Quantizer(mode="current"), s)
+    w = draw(64, 96, torch.float32, 3, spread=False) * 1e30  # brings the products back into range
+    wc, ws = te.block_empty("nvfp4", 64, 96)
+    qw, qx = te.Quantizer(mode="current"), te.Quantizer(mode="current")
+    te.te_block_quantize(w, "nvfp4", wc, ws, q=qw)
+    for rows in (8, 40):  # packed inside the product, and before it
+        out = torch.empty(rows, 64, dtype=dtype, device=DEV)
+        te.te_dense_fp4_fwd(x[:rows].contiguous(), wc, ws, out, "nvfp4", q=qx, kernel_scale_inv=qw.scale_inv)
+        a, b = values(f64(x[:rows]), "nvfp4", s), values(f64(w), "nvfp4", np.float32(qw.scale.item()))
+        alpha = float(np.float32(1) / s) * float(np.float32(1) / np.float32(qw.scale.item()))
+        want = alpha * (a @ b.T)
+        assert (np.abs(f64(out) - want) <= product_bound(a, b, alpha, want, 96, dtype)).all()
+
+
 def test_transposed_alone():
     x = draw(100, 96, torch.bfloat16)
     ct, st = te.block_empty("mxfp4", 96, 128)

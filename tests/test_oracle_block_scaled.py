@@ -79,3 +79,14 @@ def test_mxfp8_codes_are_torchs_cast_of_the_scaled_values():
     f = torch.from_numpy(bs.e8m0_decode(s)).float().repeat_interleave(32, 1)
     assert np.array_equal(c, (x / f).to(torch.float8_e4m3fn).view(torch.uint8).numpy())
     assert nx.e4m3_decode(c).max() <= 448
+
+
+def test_a_zero_stays_zero_where_the_factor_overflows():
+    """s / scale past the largest float: that float in its place, so that 0 times it is 0."""
+    x = np.zeros((1, 48))
+    x[0, 1], x[0, 17], x[0, 40] = 2e-36, -1e-38, 1.2e-38
+    s = bs.nv_scale(2e-36)
+    assert s == np.finfo(np.float32).max
+    c, sc = bs.pack(x, "nvfp4", s)
+    assert (sc > 0).all() and np.array_equal(np.flatnonzero(c), [1, 17, 40])
+    assert c[0, 17] == 8 + 5 and c[0, 40] == 6  # -1e-38 * 3.4e38 = -3.4 -> -3, 4.08 -> 4
