@@ -19,11 +19,16 @@ namespace te {
 constexpr uint32_t kInfBits = 0x7f800000u;
 constexpr float kF32Max = 3.4028234663852886e38f;
 
-// The byte of one scale within its row of tiles: tiles of 128 rows x 4 blocks, 512 bytes, in
-// which the rows r, r + 32, r + 64, r + 96 are neighbours.  This is the order in which
+// The byte of one scale within its row of tiles, for blocks counted within a CTA's own tiles: tiles
+// of 128 rows x 4 blocks, 512 bytes, in which the rows r, r + 32, r + 64, r + 96 are neighbours.  This is the order in which
 // tcgen05.cp.32x128b hands a tile to tensor memory.
 __device__ __forceinline__ uint32_t scale_offset(uint32_t row_in_tile, uint32_t block) {
   return (block >> 2) * 512 + (row_in_tile & 31) * 16 + (row_in_tile >> 5) * 4 + (block & 3);
+}
+
+// The same of any block of a row of tiles: 4 bytes a column, so past 32 bits from 2^30 columns on.
+__device__ __forceinline__ int64_t scale_offset_wide(uint32_t row_in_tile, int64_t block) {
+  return (block >> 2) * 512 + scale_offset(row_in_tile, uint32_t(block) & 3);
 }
 
 // Two fp32 -> two E2M1 codes in a byte (lo in the low half): nearest even, saturating to +-6.

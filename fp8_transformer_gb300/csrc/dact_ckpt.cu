@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) dact_ckpt_kernel(DactCkptArgs 
     for (int i = threadIdx.x; i < kRows * kSb; i += kWarps * 32) {
       const int64_t b = (h * n_out + c0) / 32 + i % kSb;
       const bool in = c0 + i % kSb * 32 < n_out;  // n_out is a multiple of 32
-      sc[h][i / kSb][i % kSb] = in ? e8m0_value(__ldg(scales + scale_offset(i / kSb, uint32_t(b)))) : 0.0f;
+      sc[h][i / kSb][i % kSb] = in ? e8m0_value(__ldg(scales + scale_offset_wide(i / kSb, b))) : 0.0f;
     }
   __syncthreads();
   f32x2 acc[kGated ? 2 : 1][4];

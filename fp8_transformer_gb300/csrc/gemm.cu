@@ -314,7 +314,7 @@ __device__ __forceinline__ void store_checkpoint(const GemmDev& g, int64_t row, 
     }
     out[q] = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  g.h_scales[(row / 128) * g.h_groups * 512 + scale_offset(uint32_t(row % 128), uint32_t(col / 32))] = uint8_t(b.byte);
+  g.h_scales[(row / 128) * g.h_groups * 512 + scale_offset_wide(uint32_t(row % 128), col / 32)] = uint8_t(b.byte);
 }
 
 // The bias values of columns j and j + 1 (j even) as an fp32 pair.

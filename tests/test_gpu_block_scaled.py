@@ -617,6 +617,19 @@ def test_offsets_past_32_bits():
     assert te.get_device_status() == 0
 
 
+def test_a_checkpoint_of_more_than_2_to_the_30_columns():
+    """Its scales take 4 bytes a column: offsets past 32 bits within one row of tiles."""
+    N = (1 << 30) + 256
+    x = torch.zeros(1, N, dtype=torch.bfloat16, device=DEV)
+    x[0, :256], x[0, -256:], x[0, N // 2:N // 2 + 256] = 1.0, 8.0, 2.0 ** 20
+    codes, scales = te.block_empty("mxfp8", 1, N)
+    te.te_block_quantize(x, "mxfp8", codes, scales)
+    dx, a = torch.empty_like(x), torch.empty_like(x)
+    te.te_dact_dbias_ckpt(x, codes, scales, "relu", dx, act_out=a)
+    assert torch.equal(a, x) and torch.equal(dx, x)
+    assert te.get_device_status() == 0
+
+
 def test_tensors_the_binding_refuses():
     x = draw(32, 64, torch.bfloat16)
     c, s = te.block_empty("mxfp4", 32, 64)
