@@ -610,6 +610,13 @@ def _sized_arg(name, t, n, dtypes, dev):
     return None if t is None else _arg(name, t.reshape(-1) if t.is_contiguous() else t, (n,), dtypes, dev)
 
 
+def _given_workspace(workspace, dev):
+    """(address, bytes) of a caller's workspace: dense, of any type, on the device `dev` of the other tensors."""
+    if workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: dense, on the device of the other tensors")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 _sized = functools.lru_cache(maxsize=1024)(workspace_size)
 _SMALL_WORKSPACE = 1 << 20
 _small = threading.local()
@@ -632,9 +639,7 @@ def _workspace(op, M, H, N, like, workspace, stream):
         workspace = torch.empty(n, dtype=torch.uint8, device=like.device)
         if stream is not None:  # freed on return: kept from reuse until that stream has passed it
             workspace.record_stream(stream)
-    elif workspace.get_device() != like.get_device() or not workspace.is_contiguous():
-        raise ValueError("workspace: dense, on the device of the other tensors")
-    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return (workspace, *_given_workspace(workspace, like.get_device()))
 
 
 def block_scale_bytes(fmt, rows, cols) -> int:
@@ -793,11 +798,10 @@ def te_layernorm_mlp_fwd_ckpt(x, gamma, beta, kernel1, kernel2, bias1, bias2, ou
                         x.device)
         if stream is not None:
             workspace.record_stream(stream)
-    elif workspace.get_device() != dev:
-        raise ValueError("workspace: on the device of the other tensors")
+    pw, nw = _given_workspace(workspace, dev)
     st = lib().te_layernorm_mlp_fwd_ckpt(px, pg, pbe, p1, p2, kd, pb1, pb2, _norm_id(norm_type),
                                          int(bool(zero_centered_gamma)), float(epsilon), act, qs, M, H, F, dt, po,
-                                         pc, ps, pa, pl, pm, pr, _ptr(workspace), workspace.numel(),
+                                         pc, ps, pa, pl, pm, pr, pw, nw,
                                          _stream(stream, dev))
     _check("te_layernorm_mlp_fwd_ckpt", st)
     return out
@@ -832,11 +836,10 @@ def te_layernorm_mlp_bwd_ckpt(dy, x, gamma, kernel1, kernel2, h_codes, h_scales,
                         x.device)
         if stream is not None:
             workspace.record_stream(stream)
-    elif workspace.get_device() != dev:
-        raise ValueError("workspace: on the device of the other tensors")
+    pw, nw = _given_workspace(workspace, dev)
     st = lib().te_layernorm_mlp_bwd_ckpt(py, px, pg, p1, p2, kd, pc, ps, pl, pm, pr, _norm_id(norm_type),
                                          int(bool(zero_centered_gamma)), act, qs, M, H, F, dt, pdx, pdg, pdb, pd1,
-                                         pd2, pb1, pb2, pdh, _ptr(workspace), workspace.numel(),
+                                         pd2, pb1, pb2, pdh, pw, nw,
                                          _stream(stream, dev))
     _check("te_layernorm_mlp_bwd_ckpt", st)
     return dx

@@ -4,6 +4,7 @@ stand-in addresses that nothing reads), and size their buffers (CPU only)."""
 import ctypes
 
 import pytest
+import torch
 
 import fp8_transformer_gb300 as te
 
@@ -141,3 +142,12 @@ def test_a_factor_that_the_call_would_write(q, ok):
                                          None, None, 0, None) == want
     assert te.lib().te_dense_fp4_fwd(P, b.TE_BF16, P, P, b.TE_NVFP4, quantizer(**q), P, None, 16, 64, 64, P, None,
                                      None, None, 0, None) == want
+
+
+def test_a_callers_workspace_is_counted_in_bytes_and_is_dense():
+    w = torch.empty(100, dtype=torch.float32)
+    assert b._given_workspace(w, -1) == (w.data_ptr(), 400)
+    assert b._given_workspace(w[10:20], -1) == (w.data_ptr() + 40, 40)
+    for bad, dev in ((w[::2], -1), (w[:1].expand(1 << 20), -1), (w, 0)):
+        with pytest.raises(ValueError, match="workspace"):
+            b._given_workspace(bad, dev)

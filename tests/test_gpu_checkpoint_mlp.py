@@ -231,3 +231,27 @@ def test_tensors_the_binding_refuses():
     dy = torch.zeros(16, F, dtype=torch.bfloat16, device=DEV)
     with pytest.raises(ValueError, match="q.scale"):
         te.te_dact_dbias_ckpt(dy, *c, "gelu", torch.empty(16, F, dtype=torch.uint8, device=DEV), q=host)
+
+
+def test_workspaces_of_any_type_that_are_dense():
+    """A workspace counts by its bytes whatever its type; one without that many behind it is refused."""
+    inp = inputs("gpt_ln_mlp_bwd", None, 48, 128, 96)
+    f = forward(inp, None, True)
+    ref = backward(inp, f)
+    b = te.binding
+    kw = dict(norm_type=inp["norm"], activation_type=inp["act"], epsilon=inp["eps"])
+    args = (inp["x"], inp["gamma"], inp["beta"], inp["w1"], inp["w2"], inp["b1"], inp["b2"])
+    size = lambda op: te.workspace_size(op, 48, 128, 96, b.TE_BF16, False, b.TE_BF16, b.TE_GELU)
+    bad = torch.empty(1, dtype=torch.uint8, device=DEV).expand(size(b.TE_OP_LAYERNORM_MLP_BWD) + (1 << 20))
+    for dt in (torch.uint8, torch.float32, torch.int64):
+        new = lambda op: torch.empty((size(op) + 7) // 8 * 8 // torch.empty(0, dtype=dt).element_size(), dtype=dt, device=DEV)
+        out, c = torch.empty_like(f["out"]), te.block_empty("mxfp8", 48, 96)
+        te.te_layernorm_mlp_fwd_ckpt(*args, out, *c, workspace=new(b.TE_OP_LAYERNORM_MLP_FWD), **kw)
+        assert torch.equal(out, f["out"]) and torch.equal(c[0], f["codes"])
+        g = backward(inp, f, workspace=new(b.TE_OP_LAYERNORM_MLP_BWD))
+        for k in ("dx", "dgamma", "dw1", "dw2", "db1", "db2"):
+            assert torch.equal(g[k], ref[k]), (dt, k)
+    with pytest.raises(ValueError, match="workspace"):
+        te.te_layernorm_mlp_fwd_ckpt(*args, out, *c, workspace=bad, **kw)
+    with pytest.raises(ValueError, match="workspace"):
+        backward(inp, f, workspace=bad)
