@@ -617,6 +617,20 @@ def _given_workspace(workspace, dev):
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
+# (id, device index, device type) of a device's current stream.
+_stream_data = torch._C._cuda_getCurrentStream if hasattr(torch._C, "_cuda_getCurrentStream") else None
+
+
+def _lasting_stream(dev, handle):
+    """Whether the current stream of `dev`, of this raw handle, is the default one or of torch's pools:
+    these are few and live as long as the process.  A stream made elsewhere has its handle for an id; once
+    it is destroyed the handle may come back as another stream's."""
+    if handle == 0:
+        return True
+    sid = torch.cuda.current_stream(dev).stream_id if _stream_data is None else _stream_data(dev)[0]
+    return sid != handle
+
+
 _sized = functools.lru_cache(maxsize=1024)(workspace_size)
 _SMALL_WORKSPACE = 1 << 20
 _small = threading.local()
@@ -624,8 +638,8 @@ _small = threading.local()
 
 def _workspace(op, M, H, N, like, workspace, stream):
     """(tensor, address, bytes) of the given workspace, or of a new one.  Small ones of eager calls
-    are kept, one for each host thread and stream, whose calls run one after another: an allocation
-    costs a short call 5 to 7 us of host time, as much as its launches."""
+    are kept, one for each host thread and stream of torch's own, whose calls run one after another: an
+    allocation costs a short call 5 to 7 us of host time, as much as its launches."""
     if workspace is None:
         n = max(_sized(op, M, H, N), 1)
         if n <= _SMALL_WORKSPACE and stream is None and not torch.cuda.is_current_stream_capturing():
@@ -633,9 +647,10 @@ def _workspace(op, M, H, N, like, workspace, stream):
             key = (dev, _stream(None, dev))
             kept = _small.__dict__.setdefault("kept", {})
             workspace = kept.get(key)
-            if workspace is None:
+            if workspace is None and _lasting_stream(*key):
                 workspace = kept[key] = torch.empty(_SMALL_WORKSPACE, dtype=torch.uint8, device=like.device)
-            return workspace, workspace.data_ptr(), _SMALL_WORKSPACE
+            if workspace is not None:
+                return workspace, workspace.data_ptr(), _SMALL_WORKSPACE
         workspace = torch.empty(n, dtype=torch.uint8, device=like.device)
         if stream is not None:  # freed on return: kept from reuse until that stream has passed it
             workspace.record_stream(stream)

@@ -2,6 +2,7 @@
 stand-in addresses that nothing reads), and size their buffers (CPU only)."""
 
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -151,3 +152,24 @@ def test_a_callers_workspace_is_counted_in_bytes_and_is_dense():
     for bad, dev in ((w[::2], -1), (w[:1].expand(1 << 20), -1), (w, 0)):
         with pytest.raises(ValueError, match="workspace"):
             b._given_workspace(bad, dev)
+
+
+def test_workspaces_are_kept_for_torchs_own_streams_alone(monkeypatch):
+    """A stream made elsewhere may be destroyed and its handle come back: its calls get a buffer each."""
+    now = {}
+    monkeypatch.setattr(b, "_raw_stream", lambda dev: now["handle"])
+    monkeypatch.setattr(b, "_stream_data", lambda dev: (now["id"], 0, 1))
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: now.get("capturing", False))
+    monkeypatch.setattr(b, "_small", threading.local())
+    like = torch.empty(1)
+
+    def take(sid, handle, **kw):
+        now.update(id=sid, handle=handle, **kw)
+        return b._workspace(b.TE_OP_DENSE_FP4_FWD, 9, 64, 64, like, None, None)
+    default, pooled = take(0, 0), take(35, 0x5000)
+    assert take(0, 0)[1] == default[1] and take(35, 0x5000)[1] == pooled[1] != default[1]
+    assert default[2] == pooled[2] == 1 << 20
+    first, second = take(0x7000, 0x7000), take(0x7000, 0x7000)
+    assert first[1] != second[1] and first[2] == te.workspace_size(b.TE_OP_DENSE_FP4_FWD, 9, 64, 64)
+    assert take(35, 0x5000, capturing=True)[1] != pooled[1]
+    assert sorted(b._small.kept) == [(-1, 0), (-1, 0x5000)]

@@ -545,6 +545,22 @@ def test_on_another_stream_without_a_workspace_of_its_own():
     assert all(torch.equal(want, o) for o in outs)
 
 
+def test_nothing_is_kept_for_a_stream_made_elsewhere():
+    M, K, N, fmt = 20, 512, 256, "mxfp4"
+    x = draw(M, K, torch.bfloat16, 1)
+    cb, sb, _, _, _ = packed(N, K, fmt, 2)
+    want = te.te_dense_fp4_fwd(x, cb, sb, torch.empty(M, N, dtype=torch.bfloat16, device=DEV), fmt)
+    pooled = torch.cuda.Stream()
+    kept = lambda: {h for _, h in te.binding._small.kept}
+    for stream, lasts in ((torch.cuda.ExternalStream(pooled.cuda_stream), False), (pooled, True)):
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            outs = [te.te_dense_fp4_fwd(x, cb, sb, torch.empty(M, N, dtype=torch.bfloat16, device=DEV), fmt) for _ in range(20)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(want, o) for o in outs)
+        assert (pooled.cuda_stream in kept()) == lasts
+
+
 def test_two_host_threads_at_once():
     """Calls of two threads on one stream interleave; each has a workspace of its own."""
     import threading
