@@ -168,9 +168,10 @@ __device__ __forceinline__ bool wait_or_abort(uint32_t bar, uint32_t parity, vol
 }
 
 // Arrives at a barrier of the pair without ordering this thread's memory accesses: what these
-// signals hand over is tensor memory, whose accesses tcgen05.wait and the tcgen05 fences order.  A
-// release at cluster scope waits for the thread's global stores as well; it made an epilogue or scale
-// warp's turn about 0.7 us longer.
+// signals hand over is tensor memory, whose accesses tcgen05.wait and the tcgen05 fences order: the
+// arriving warp waits for its tcgen05.ld or st and fences before it, and the MMA warp, the only one to act
+// on these phases, fences after its wait.  A release at cluster scope waits for the thread's global
+// stores as well; it made an epilogue or scale warp's turn about 0.7 us longer.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -188,9 +189,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   int ok = 1;
   if ((threadIdx.x & 31) == 0) ok = wait_or_abort(bar, parity, abort_flag, status) ? 1 : 0;
   if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
-  // The phase that one lane saw complete stays so until this warp signals: each lane sees it itself.
+  // The phase that one lane saw complete stays so until this warp signals: each lane sees it itself, on
+  // its first tries (in line: through the bounded wait's call, products took 1% more).  A lane that did
+  // not raises the flag and records the timeout as that wait does.
   bool seen = false;
   for (int i = 0; i < 1024 && !seen; ++i) seen = mbar_try_wait(bar, parity);
+  if (!seen) {
+    if (status) atomicCAS(status, 0, int(TE_ERR_TIMEOUT));
+    *abort_flag = 1;
+  }
   return __all_sync(0xffffffffu, seen);
 }
 
@@ -377,9 +384,12 @@ __global__ void __launch_bounds__(kBatchThreads, 1)
       uint32_t phase = 0, acc_phase = 0;
       bool ok = true;
       for (int t = cluster_id; t < num_tiles && ok; t += num_clusters, acc_phase ^= 1) {
+        // the accumulator has been read by both CTAs: their relaxed arrivals and this fence order that
         if (!warp_wait(smem_u32(tempty), acc_phase ^ 1, abort_flag, g.status)) break;
         tc_fence_after();
         for (int kb = 0; kb < g.num_kb; ++kb) {
+          // codes have landed (TMA's own signal) and the scale warps' stores are done (relaxed arrivals,
+          // ordered by this fence)
           if (!warp_wait(smem_u32(&full[stage]), phase, abort_flag, g.status)) {
             ok = false;
             break;
