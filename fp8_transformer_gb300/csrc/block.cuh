@@ -132,13 +132,15 @@ __device__ __forceinline__ float max_abs3(float m, float a, float b) {
   return r;
 }
 
-// 8 neighbours of T as fp32.
+// 8 neighbours of T as fp32.  load: memory that nothing writes while the kernel runs; load_fresh: what the
+// kernel before a programmatic dependent may still have been writing when this one began.
 template <typename T>
 struct Eight;
 template <>
 struct Eight<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const void* p) { u = __ldg(static_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void load_fresh(const void* p) { u = *static_cast<const uint4*>(p); }
   __device__ __forceinline__ void zero() { u = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void to_smem(void* p) const { *static_cast<uint4*>(p) = u; }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -167,6 +169,10 @@ struct Eight<float> {
   __device__ __forceinline__ void load(const void* p) {
     a = __ldg(static_cast<const uint4*>(p));
     b = __ldg(static_cast<const uint4*>(p) + 1);
+  }
+  __device__ __forceinline__ void load_fresh(const void* p) {
+    a = static_cast<const uint4*>(p)[0];
+    b = static_cast<const uint4*>(p)[1];
   }
   __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void to_smem(void* p) const {

@@ -146,9 +146,10 @@ __device__ __forceinline__ float alpha_of(const BlockGemmDev& g) {
   return alpha;
 }
 
+// By ordinary loads: the bias may come from the kernel before.
 __device__ __forceinline__ float load_bias(const void* bias, int dtype, int64_t j) {
-  return dtype == TE_BF16 ? __bfloat162float(__ldg(static_cast<const __nv_bfloat16*>(bias) + j))
-                          : __ldg(static_cast<const float*>(bias) + j);
+  return dtype == TE_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(bias)[j])
+                          : static_cast<const float*>(bias)[j];
 }
 
 // r (32 consecutive columns) times alpha plus their bias, of which lane i of the warp holds column i's.
@@ -772,7 +773,7 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         Eight<X> e[kFewPacked];
 #pragma unroll
         for (int r = 0; r < int(kFewPacked); ++r) {
-          if (col < g.K && r < tokens) e[r].load(x + r * g.K);
+          if (col < g.K && r < tokens) e[r].load_fresh(x + r * g.K);
           else e[r].zero();
         }
         ok = warp_wait(smem_u32(&empty[stage]), ((i / STAGES) & 1) ^ 1, abort_flag, g.status);

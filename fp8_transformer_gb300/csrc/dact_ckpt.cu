@@ -24,13 +24,15 @@ constexpr int kRows = 128;  // rows of a CTA = of a scale tile = of a dbias part
 constexpr int kCols = 256;
 constexpr int kSb = kCols / 32;
 
+// Inputs are read by ordinary loads, not through the read-only path: this grid may be running while the
+// kernel before it still writes them.
 template <typename T>
 struct Dy8;
 template <>
 struct Dy8<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    u = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i));
+    u = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
   }
   __device__ __forceinline__ void get(f32x2 (&v)[4]) const { Pairs<__nv_bfloat16>::cvt(u, v); }
 };
@@ -38,8 +40,8 @@ template <>
 struct Dy8<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const void* p, int64_t i) {
-    a = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i));
-    b = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i) + 1);
+    a = *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+    b = *(reinterpret_cast<const float4*>(static_cast<const float*>(p) + i) + 1);
   }
   __device__ __forceinline__ void get(f32x2 (&v)[4]) const {
     v[0] = f2(a.x, a.y); v[1] = f2(a.z, a.w); v[2] = f2(b.x, b.y); v[3] = f2(b.z, b.w);
@@ -138,8 +140,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) dact_ckpt_kernel(DactCkptArgs 
     for (int j = 0; j < U; ++j) {
       const int64_t r = r0 + min(warp + j * kWarps, rows - 1);
       next.dy[j].load(a.dy, r * n_out + col);
-      next.g[j] = __ldg(reinterpret_cast<const uint2*>(codes + r * a.N_in + col));
-      if constexpr (kGated) next.l[j] = __ldg(reinterpret_cast<const uint2*>(codes + r * a.N_in + n_out + col));
+      next.g[j] = *reinterpret_cast<const uint2*>(codes + r * a.N_in + col);
+      if constexpr (kGated) next.l[j] = *reinterpret_cast<const uint2*>(codes + r * a.N_in + n_out + col);
     }
   }
 #pragma unroll
@@ -147,7 +149,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) dact_ckpt_kernel(DactCkptArgs 
     for (int i = threadIdx.x; i < kRows * kSb; i += kWarps * 32) {
       const int64_t b = (h * n_out + c0) / 32 + i % kSb;
       const bool in = c0 + i % kSb * 32 < n_out;  // n_out is a multiple of 32
-      sc[h][i / kSb][i % kSb] = in ? e8m0_value(__ldg(scales + scale_offset_wide(i / kSb, b))) : 0.0f;
+      sc[h][i / kSb][i % kSb] = in ? e8m0_value(scales[scale_offset_wide(i / kSb, b)]) : 0.0f;
     }
   __syncthreads();
   f32x2 acc[kGated ? 2 : 1][4];
@@ -167,8 +169,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) dact_ckpt_kernel(DactCkptArgs 
         for (int j = 0; j < U; ++j) {
           const int64_t r = r0 + min(rb + j * kWarps, rows - 1);
           b.dy[j].load(a.dy, r * n_out + col);
-          b.g[j] = __ldg(reinterpret_cast<const uint2*>(codes + r * a.N_in + col));
-          if constexpr (kGated) b.l[j] = __ldg(reinterpret_cast<const uint2*>(codes + r * a.N_in + n_out + col));
+          b.g[j] = *reinterpret_cast<const uint2*>(codes + r * a.N_in + col);
+          if constexpr (kGated) b.l[j] = *reinterpret_cast<const uint2*>(codes + r * a.N_in + n_out + col);
         }
       };
 #pragma unroll 1

@@ -272,7 +272,8 @@ constexpr int kColsumWarps = 16;
 __global__ void __launch_bounds__(kColsumWarps * 32)
     colsum_partials_kernel(const float* partials, int chunks, int64_t n, float* out) {
   __shared__ float4 sums[kColsumWarps][32];
-  // launched as a programmatic dependent of the dact kernel: wait for that grid's partials
+  // launched as a programmatic dependent of the kernel that writes the partials: wait for that grid, and
+  // read them by ordinary loads (they are not read-only for this grid's lifetime)
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t j = int64_t(blockIdx.x) * 128 + lane * 4;
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kColsumWarps * 32)
   if (j < n) {
 #pragma unroll 4
     for (int c = w; c < chunks; c += kColsumWarps) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(partials + int64_t(c) * n + j));
+      const float4 v = *reinterpret_cast<const float4*>(partials + int64_t(c) * n + j);
       acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
     }
   }

@@ -561,6 +561,43 @@ def test_nothing_is_kept_for_a_stream_made_elsewhere():
         assert (pooled.cuda_stream in kept()) == lasts
 
 
+def test_chains_through_the_same_buffers_without_waits():
+    """Each kernel may start before the one whose output it reads has ended: with buffers that take other
+    values every time, nothing of the time before is read."""
+    M, F, act = 300, 544, "swiglu"
+    hs = [draw(M, 2 * F, torch.bfloat16, s, spread=False) for s in (1, 2, 3)]
+    dy = draw(M, F, torch.bfloat16, 4, spread=False)
+    codes, scales = te.block_empty("mxfp8", M, 2 * F)
+
+    def gradient(i):
+        dx, a = torch.empty(M, 2 * F, dtype=torch.uint8, device=DEV), torch.empty(M, F, dtype=torch.bfloat16, device=DEV)
+        db, q = torch.empty(2 * F, device=DEV), te.Quantizer(scale=16.0)
+        te.te_block_quantize(hs[i], "mxfp8", codes, scales)
+        te.te_dact_dbias_ckpt(dy, codes, scales, act, dx, dbias=db, act_out=a, q=q)
+        return dx, a, db, q.amax
+
+    T, K, N, fmt = 4, 1024, 768, "mxfp4"  # two layers of four tokens, each packing its input itself
+    xs = [draw(T, K, torch.bfloat16, s, spread=False) for s in (5, 6, 7)]
+    c1, s1, _, _, _ = packed(N, K, fmt, 8)
+    c2, s2, _, _, _ = packed(K, N, fmt, 9)
+    mid, bias = torch.empty(T, N, dtype=torch.bfloat16, device=DEV), draw(1, K, torch.bfloat16, 10, spread=False)[0]
+
+    def layers(i):
+        out = torch.empty(T, K, dtype=torch.bfloat16, device=DEV)
+        te.te_dense_fp4_fwd(xs[i], c1, s1, mid, fmt)
+        return (te.te_dense_fp4_fwd(mid, c2, s2, out, fmt, bias=bias),)
+
+    for f in (gradient, layers):
+        want = []
+        for i in range(3):
+            want.append(f(i))
+            torch.cuda.synchronize()
+        got = [f(i % 3) for i in range(60)]
+        torch.cuda.synchronize()
+        for i, g in enumerate(got):
+            assert all(torch.equal(u, v) for u, v in zip(g, want[i % 3])), (f.__name__, i)
+
+
 def test_two_host_threads_at_once():
     """Calls of two threads on one stream interleave; each has a workspace of its own."""
     import threading
