@@ -678,8 +678,12 @@ def te_block_quantize(x, fmt, codes=None, scales=None, codes_t=None, scales_t=No
     pc = ps = pct = pst = None
     if codes is not None:
         pc, ps = _packed("codes", codes, scales, f, M, N, dev)
+    elif scales is not None:
+        raise ValueError("scales: given without their codes")
     if codes_t is not None:
         pct, pst = _packed("codes_t", codes_t, scales_t, f, N, (M + 31) // 32 * 32, dev)
+    elif scales_t is not None:
+        raise ValueError("scales_t: given without their codes")
     st = lib().te_block_quantize(px, _dt(x), M, N, f, _tensor_scale(f, q, dev), pc, ps, pct, pst,
                                  _stream(stream, dev))
     _check("te_block_quantize", st)
@@ -729,6 +733,8 @@ def te_dense_fp4_fwd(x, kernel, kernel_scales, out, fmt, bias=None, q=None, kern
     pt = pst = None
     if saved_xt is not None:
         pt, pst = _packed("saved_xt", saved_xt, saved_xt_scales, f, K, (M + 31) // 32 * 32, dev)
+    elif saved_xt_scales is not None:
+        raise ValueError("saved_xt_scales: given without their codes")
     cq = _tensor_scale(f, q, dev)
     pw, nw = None, 0
     if M > 8 or saved_xt is not None or workspace is not None:

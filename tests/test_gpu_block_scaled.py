@@ -703,3 +703,15 @@ def test_tensors_the_binding_refuses():
     with pytest.raises(te.TEError):  # 8-bit codes do not go into the 4-bit product
         e, f = te.block_empty("mxfp8", 32, 64)
         te.te_block_gemm(e, f, e, f, torch.empty(32, 32, device=DEV), "mxfp8")
+
+
+def test_scales_without_their_codes_are_refused():
+    """They would be left as they were."""
+    x, (c, s) = draw(32, 64, torch.bfloat16), te.block_empty("mxfp4", 32, 64)
+    ct, st = te.block_empty("mxfp4", 64, 32)
+    with pytest.raises(ValueError, match="scales_t: given without"):
+        te.te_block_quantize(x, "mxfp4", c, s, scales_t=st)
+    with pytest.raises(ValueError, match="scales: given without"):
+        te.te_block_quantize(x, "mxfp4", scales=s, codes_t=ct, scales_t=st)
+    with pytest.raises(ValueError, match="saved_xt_scales: given without"):
+        te.te_dense_fp4_fwd(x, c, s, torch.empty(32, 32, dtype=torch.bfloat16, device=DEV), "mxfp4", saved_xt_scales=st)
