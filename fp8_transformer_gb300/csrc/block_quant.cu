@@ -268,13 +268,23 @@ te_status launch_quant_t(const BlockQuantArgs& a, cudaStream_t s) {
   const int64_t tiles = ceil_div(a.M, kTileRows) * ceil_div(a.N, tc);
   if (tiles > 0x1fffffff) return TE_ERR_UNSUPPORTED;
   if (!col) {
-    // Whole tiles once they give every SM three CTAs.  32-row CTAs against whole tiles, bf16 in L2, MXFP4
-    // and MXFP8: 16 tiles 1.6 us against 2.6, 1.7 against 2.7; 320 tiles 4.6 against 5.4, 4.2 against 5.5;
-    // 512 tiles 6.7 against 6.5, 6.1 against 6.9; 1024 tiles 12.4 against 10.4, 13.1 against 14.2.
-    if (tiles < 3 * num_sms())
-      block_quantize_kernel<T, FMT, 256, false, 32><<<unsigned(tiles * 4), kThreads, 0, s>>>(a);
-    else
-      block_quantize_kernel<T, FMT, 256, false, kTileRows><<<unsigned(tiles), kThreads, 0, s>>>(a);
+    // 32-row CTAs throughout for fp32 and for MXFP8, whole tiles for bf16 to 4 bits once there are enough
+    // of them for every SM.  32-row CTAs against whole tiles, us:
+    //   tiles          64         160        320        448        512        1024       4096
+    //   bf16 MXFP4   2.0  3.1   3.0  4.1   4.7  5.3   5.9  5.5   6.5  6.4  12.2 10.3  53.8 50.1
+    //   bf16 NVFP4   2.6  3.5   3.6  4.4   5.4  5.4   6.7  5.6   7.5  6.5  14.3 10.7  58.3 51.4
+    //   bf16 MXFP8   2.1  3.4   3.0  4.3   4.3  5.4   5.3  5.4   5.9  6.7  12.7 13.9  57.7 58.4
+    //   fp32 MXFP4   2.7  5.1   3.9  6.1   5.5  7.7   6.8  7.8   7.8  9.5  23.6 25.1  84.9 86.1
+    //   fp32 NVFP4   3.1  5.7   4.5  6.8   6.4  8.3   8.2  8.3   9.1 10.0  24.5 27.1  86.4 92.1
+    //   fp32 MXFP8   2.8  5.0   4.0  6.1   5.6  7.7   7.0  7.8   8.2  9.7  25.6 26.9  93.7 94.6
+    // (MXFP4 crosses at 288, back at 320, and for good after 480; NVFP4 at 240.)
+    if constexpr (sizeof(T) == 2 && FMT != TE_MXFP8) {
+      if (2 * tiles >= (FMT == TE_NVFP4 ? 3 : 6) * num_sms()) {
+        block_quantize_kernel<T, FMT, 256, false, kTileRows><<<unsigned(tiles), kThreads, 0, s>>>(a);
+        return cudaGetLastError() == cudaSuccess ? TE_OK : TE_ERR_CUDA;
+      }
+    }
+    block_quantize_kernel<T, FMT, 256, false, 32><<<unsigned(tiles * 4), kThreads, 0, s>>>(a);
   } else if constexpr (FMT == TE_MXFP8) {
     return TE_ERR_UNSUPPORTED;  // checkpoints are read along their rows only
   } else {

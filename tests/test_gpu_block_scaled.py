@@ -156,6 +156,28 @@ def test_nvfp4_zeros_beside_tiny_values(dtype):
         assert (np.abs(f64(out) - want) <= product_bound(a, b, alpha, want, 96, dtype)).all()
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "mxfp8"])
+def test_large_tensors_are_packed_like_their_parts(fmt, dtype):
+    """Whichever form packs it, a tensor's rows come out as those of a few of them alone (which are held to
+    the oracle above)."""
+    for M, N in ((4230, 4256), (1800, 4256)):
+        x = draw(M, N, dtype, 1, spread=fmt != "nvfp4")
+        new = lambda: te.Quantizer(scale=500.0) if fmt == "nvfp4" else None
+        codes, scales = te.block_empty(fmt, M, N)
+        q = new()
+        te.te_block_quantize(x, fmt, codes, scales, q=q)
+        per = scales.numel() // ((M + 127) // 128)
+        for r in (0, 128 * 7, M // 128 * 128):
+            part = x[r:r + 256].contiguous()
+            c, s = te.block_empty(fmt, part.shape[0], N)
+            te.te_block_quantize(part, fmt, c, s, q=new())
+            assert torch.equal(codes[r:r + 256], c)
+            assert torch.equal(scales[r // 128 * per:][:s.numel()], s)
+        if q is not None:
+            assert q.amax.item() == x.abs().max().item()
+
+
 def test_transposed_alone():
     x = draw(100, 96, torch.bfloat16)
     ct, st = te.block_empty("mxfp4", 96, 128)
