@@ -157,6 +157,26 @@ def test_nvfp4_zeros_beside_tiny_values(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+@pytest.mark.parametrize("M,N", [(1, 16), (45, 48), (300, 112), (129, 272)])
+def test_transposed_alone_with_half_a_block_in_a_row(M, N, fmt, dtype):
+    """x^T alone takes rows of x of any multiple of 16, the last block of 32 of them half there."""
+    x = draw(M, N, dtype, M, spread=fmt == "mxfp4")
+    x[M // 2, N - 1] = -3.0
+    mp = (M + 31) // 32 * 32
+    gc, ct = guarded(N * mp // 2)
+    gs, st = guarded(te.block_scale_bytes(fmt, N, mp))
+    q = te.Quantizer(scale=100.0) if fmt == "nvfp4" else None
+    te.te_block_quantize(x, fmt, codes_t=ct.view(N, mp // 2), scales_t=st, q=q)
+    torch.cuda.synchronize()
+    c, s = bs.pack(bs.pad_t(f64(x)), fmt, 100.0)
+    assert np.array_equal(u8(ct).reshape(N, -1), bs.to_bytes(c, fmt)) and np.array_equal(u8(st), bs.tile_scales(s))
+    assert (gc[ct.numel():] == GUARD).all() and (gs[st.numel():] == GUARD).all()
+    if q is not None:
+        assert q.amax.item() == x.abs().max().item()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4", "mxfp8"])
 def test_large_tensors_are_packed_like_their_parts(fmt, dtype):
     """Whichever form packs it, a tensor's rows come out as those of a few of them alone (which are held to
@@ -581,6 +601,63 @@ def test_nothing_is_kept_for_a_stream_made_elsewhere():
         torch.cuda.synchronize()
         assert all(torch.equal(want, o) for o in outs)
         assert (pooled.cuda_stream in kept()) == lasts
+
+
+def dense_backward_inputs(fmt, M, K, N, seeds):
+    """(calls, packed weights and x^T) of te_dense_fp4_bwd; calls(i, **kw) on dy number i -> dx, dw, db."""
+    dys = [draw(M, N, torch.bfloat16, s, spread=False) for s in seeds]
+    kc, ks, ik, _, _ = packed(K, N, fmt, 21)
+    xt, xts, ix, _, _ = packed(K, (M + 31) // 32 * 32, fmt, 22)
+
+    def call(dy, q, out=None, **kw):
+        dx, dw, db = out or (torch.empty(M, K, dtype=torch.bfloat16, device=DEV),
+                             torch.empty(K, N, dtype=torch.bfloat16, device=DEV), torch.empty(N, device=DEV))
+        te.te_dense_fp4_bwd(dy, kc, ks, xt, xts, dx, dw, fmt, dbias=db, q=q, kernel_scale_inv=ik, x_scale_inv=ix, **kw)
+        return dx, dw, db
+    return dys, call
+
+
+@pytest.mark.parametrize("fmt,mode", [("mxfp4", None), ("nvfp4", "current"), ("nvfp4", "delayed")])
+@pytest.mark.parametrize("M", [20, 300])
+def test_dense_backward_captured_and_replayed_on_other_inputs(fmt, mode, M):
+    """With a workspace of the caller's and with the graph's own."""
+    K, N = 288, 416
+    dys, call = dense_backward_inputs(fmt, M, K, N, (1, 2))
+    new = lambda: None if mode is None else te.Quantizer(scale=300.0, mode=mode)
+    want = [call(dy, new()) for dy in dys]
+    ws = torch.empty(te.workspace_size(te.binding.TE_OP_DENSE_FP4_BWD, M, K, N), dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for kw in (dict(workspace=ws), dict()):
+        dy, q = dys[0].clone(), new()
+        out = tuple(torch.empty_like(t) for t in want[0])
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call(dy, q, out, **kw)
+        for k in (0, 1, 0):
+            dy.copy_(dys[k])
+            g.replay()
+            assert all(torch.equal(a, b) for a, b in zip(out, want[k])), (kw.keys(), k)
+    assert te.get_device_status() == 0
+
+
+def test_dense_backward_on_another_stream():
+    """On the current stream and on one that is passed, whose workspace lasts until that stream is past it."""
+    M, K, N, fmt = 260, 544, 512, "mxfp4"
+    dys, call = dense_backward_inputs(fmt, M, K, N, (1, 2))
+    want = [call(dy, None) for dy in dys]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    outs = [[tuple(torch.empty_like(t) for t in want[0]) for _ in range(8)] for _ in range(2)]
+    for i, o in enumerate(outs[0]):
+        call(dys[i % 2], None, o, stream=s)
+        torch.empty(M * N, dtype=torch.uint8, device=DEV).fill_(255)  # would land in a workspace freed too early
+    with torch.cuda.stream(s):
+        for i, o in enumerate(outs[1]):
+            call(dys[i % 2], None, o)
+    torch.cuda.synchronize()
+    for o in outs:
+        for i, got in enumerate(o):
+            assert all(torch.equal(a, b) for a, b in zip(got, want[i % 2])), i
 
 
 def test_chains_through_the_same_buffers_without_waits():
