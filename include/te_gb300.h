@@ -481,7 +481,7 @@ te_status te_dense_fp4_bwd(const void* dy, te_dtype dtype, const void* kernel,
  *   act_out     [M, N_out] act(h) in dtype, or NULL.
  *   dbias       [N_in] fp32 column sums of the fp32 dx, in a fixed order, or NULL.
  *   workspace   te_workspace_size(TE_OP_DACT_DBIAS, M, 0, N_in, ...) bytes, needed for dbias.
- * N_out must be a multiple of 32.
+ * N_out must be a multiple of 32.  No output overlaps an input or another output.
  * A block that reads as NaN gives NaN in dx, dbias and act_out, with every activation (ReLU among
  * them; of a gated pair's linear half: in the gate's gradient and act_out, as its own does not depend
  * on it).  q's amax leaves NaN out. */

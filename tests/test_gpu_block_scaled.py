@@ -697,6 +697,32 @@ def test_chains_through_the_same_buffers_without_waits():
             assert all(torch.equal(u, v) for u, v in zip(g, want[i % 3])), (f.__name__, i)
 
 
+def test_checkpoint_gradients_on_two_streams_at_once():
+    """Each stream's calls sum their columns in a workspace of that stream's."""
+    M, F, act = 1000, 1024, "geglu"
+    hs = [draw(M, 2 * F, torch.bfloat16, s, spread=False) for s in (1, 2)]
+    dy = draw(M, F, torch.bfloat16, 3, spread=False)
+    packs = [te.block_empty("mxfp8", M, 2 * F) for _ in hs]
+    for h, p in zip(hs, packs):
+        te.te_block_quantize(h, "mxfp8", *p)
+
+    def call(i):
+        dx, db = torch.empty(M, 2 * F, dtype=torch.bfloat16, device=DEV), torch.empty(2 * F, device=DEV)
+        te.te_dact_dbias_ckpt(dy, *packs[i], act, dx, dbias=db)
+        return dx, db
+    want = [call(i) for i in (0, 1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in hs]
+    got = []
+    for n in range(40):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append((i, call(i)))
+    torch.cuda.synchronize()
+    for i, g in got:
+        assert all(torch.equal(u, v) for u, v in zip(g, want[i]))
+
+
 def test_two_host_threads_at_once():
     """Calls of two threads on one stream interleave; each has a workspace of its own."""
     import threading

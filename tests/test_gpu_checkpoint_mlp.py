@@ -255,3 +255,35 @@ def test_workspaces_of_any_type_that_are_dense():
         te.te_layernorm_mlp_fwd_ckpt(*args, out, *c, workspace=bad, **kw)
     with pytest.raises(ValueError, match="workspace"):
         backward(inp, f, workspace=bad)
+
+
+def test_on_streams_of_their_own():
+    """Forward and backward on a passed stream and on a current one, without a workspace of the caller's."""
+    inp = inputs("llama_rms_mlp", None, 200, 256, 288)
+    ref = forward(inp, None, True)
+    want = backward(inp, ref)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    args = (inp["x"], inp["gamma"], inp["beta"], inp["w1"], inp["w2"], None, None)
+    kw = dict(norm_type=inp["norm"], zero_centered_gamma=inp["zero_centered_gamma"], activation_type=inp["act"],
+              epsilon=inp["eps"])
+    got = []
+    for passed in (True, False, True, False):
+        f = dict(ref, out=torch.empty_like(ref["out"]), ln=torch.empty_like(ref["ln"]), mu=torch.empty_like(ref["mu"]),
+                 rs=torch.empty_like(ref["rs"]))
+        f["codes"], f["scales"] = te.block_empty("mxfp8", 200, 576)
+        call = lambda **st: (te.te_layernorm_mlp_fwd_ckpt(*args, f["out"], f["codes"], f["scales"], saved_ln_out=f["ln"],
+                                                          mu=f["mu"], rsigma=f["rs"], **kw, **st), backward(inp, f, **st))[1]
+        s.wait_stream(torch.cuda.current_stream())
+        if passed:
+            got.append(call(stream=s))
+            torch.empty(1 << 21, dtype=torch.uint8, device=DEV).fill_(255)  # would land in a workspace freed too early
+        else:
+            with torch.cuda.stream(s):
+                got.append(call())
+    torch.cuda.synchronize()
+    assert te.get_device_status() == 0
+    for g in got:
+        for k in ("out", "codes", "scales", "dx", "dgamma", "dw1", "dw2", "db1", "db2", "dh"):
+            assert torch.equal(g[k], want[k]), k
