@@ -10,9 +10,10 @@
 //     walks 32 rows of its column(s), lanes on neighbouring columns (no bank conflicts), and the
 //     codes go out through a second small stage, 64 bytes of a transposed row at a time.
 // Both outputs cost one read of x.  Rows alone are bound by memory: 8190 x 14336 bf16 takes 47 us to
-// MXFP4 (93% of the copy rate), 49 to NVFP4, 54 to MXFP8; 4096 x 28672 fp32 80 us to MXFP4 (98%).  Both
-// ways are bound by instructions, about 8 an element for each way: 71 us (75%), NVFP4 81 (67%), fp32 116
-// (75%).  Reading back is bound by its writes: 50 us (87%), NVFP4 52 (85%), MXFP8 58 (91%).
+// MXFP4 (94% of the copy rate), 50 to NVFP4 (89%), 53 to MXFP8 (99%); 4096 x 28672 fp32 77 us to MXFP4
+// (101%), 80 to NVFP4 (99%), 84 to MXFP8 (103%).  Both ways are bound by instructions, about 8 an element
+// for each way: 70 us (76%), NVFP4 84 (64%), fp32 115 (76%) and 132 (67%).  Reading back is bound by its
+// writes: 49 us (89%), NVFP4 51 (86%), MXFP8 57 (92%).
 #include "block.cuh"
 #include "cast.cuh"
 

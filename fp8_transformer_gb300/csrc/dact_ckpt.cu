@@ -8,7 +8,13 @@
 // Decoding is exact in fp32 (4 significant bits times a power of two).
 //
 // Bound by memory: with bf16 dy, dx and a, 2 + 1.03 + 2 + 2 bytes an element; 16384 x 16384 gelu takes
-// 301 us (92% of the copy rate), 8192 x 14336 swiglu 193 us (90%), with E4M3 dx 165 (85%).  A CTA owns a strip
+// 301 us (92% of the copy rate), relu 290 (96%), 8192 x 14336 swiglu 191 us (91%), geglu 192, with E4M3 dx
+// 163 (86%).  Current scaling takes two passes, the first for the amax, each reading dy and codes and
+// computing the derivative: 258 us.  In fp32 8192 x 16384 silu takes 293 us (88%), gelu 295, but 8192 x
+// 14336 swiglu 457 (69%) and geglu 449: three CTAs an SM leave 80 registers, and the fp32 gated forms
+// spill 940 to 1020 bytes a thread, the bf16 gated ones 310 to 440, gelu in bf16 16, fp32 plain 16 to 230
+// (bf16 relu and silu none).  Two CTAs an SM spill nothing: fp32 swiglu 378 us, but bf16 198 and with E4M3
+// dx 177.  A CTA owns a strip
 // of 256 columns (8 a lane: 16 bytes of dy, 8 of codes) and 128 rows, the rows of one row of
 // scale tiles; the strip's scales are decoded to fp32 in shared memory once.  The column sums go
 // the way of dact_dbias_kernel: registers, warps in order, one partial row a CTA, and an ordered
