@@ -593,6 +593,8 @@ def test_nothing_is_kept_for_a_stream_made_elsewhere():
     cb, sb, _, _, _ = packed(N, K, fmt, 2)
     want = te.te_dense_fp4_fwd(x, cb, sb, torch.empty(M, N, dtype=torch.bfloat16, device=DEV), fmt)
     pooled = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    te.binding._small.kept.clear()  # the pool may have handed this stream out before
     kept = lambda: {h for _, h in te.binding._small.kept}
     for stream, lasts in ((torch.cuda.ExternalStream(pooled.cuda_stream), False), (pooled, True)):
         stream.wait_stream(torch.cuda.current_stream())
