@@ -15,7 +15,9 @@ from .binding import (ACT_TUPLES, ACT_TYPES, BLOCK_FORMATS, EXPORTED, KERNEL_KIN
                       te_dact_dbias_quantize, te_dact_dbias_quantize_noalloc, te_gemm,
                       te_layernorm_dense_bwd, te_layernorm_dense_fwd, te_layernorm_mlp_bwd,
                       te_layernorm_mlp_fwd, te_layernorm_mlp_fwd_host, te_norm_bwd, te_norm_fwd,
-                      te_quantize, version, workspace_size)
+                      te_quantize, version, workspace_size, GradList, te_clip_grad_norm,
+                      te_dense_residual_bwd, te_dense_residual_fwd, te_grad_norm,
+                      te_residual_norm_bwd, te_residual_norm_fwd)
 from .binding import *  # noqa: F401,F403  (enum constants)
 
 __all__ = ["Quantizer", "QuantizerSet", "TEError", "te_norm_fwd", "te_act_lu",
@@ -28,4 +30,6 @@ __all__ = ["Quantizer", "QuantizerSet", "TEError", "te_norm_fwd", "te_act_lu",
            "selftest_wait_timeout", "te_layernorm_mlp_fwd_host", "stream_probe",
            "BLOCK_FORMATS", "block_empty", "block_scale_bytes", "te_block_quantize",
            "te_block_dequantize", "te_block_gemm", "te_dense_fp4_fwd", "te_dense_fp4_bwd",
-           "te_dact_dbias_ckpt", "te_layernorm_mlp_fwd_ckpt", "te_layernorm_mlp_bwd_ckpt"]
+           "te_dact_dbias_ckpt", "te_layernorm_mlp_fwd_ckpt", "te_layernorm_mlp_bwd_ckpt",
+           "te_residual_norm_fwd", "te_residual_norm_bwd", "te_dense_residual_fwd",
+           "te_dense_residual_bwd", "GradList", "te_grad_norm", "te_clip_grad_norm"]

@@ -50,7 +50,11 @@ EXPORTED = ["te_status_string", "te_version", "te_get_device_status", "te_worksp
             "te_layernorm_mlp_fwd_host", "te_update_scales", "te_stream_probe",
             "te_block_scale_bytes", "te_block_quantize", "te_block_dequantize", "te_block_gemm",
             "te_dense_fp4_fwd", "te_dense_fp4_bwd", "te_dact_dbias_ckpt",
-            "te_layernorm_mlp_fwd_ckpt", "te_layernorm_mlp_bwd_ckpt"]
+            "te_layernorm_mlp_fwd_ckpt", "te_layernorm_mlp_bwd_ckpt",
+            "te_residual_norm_fwd", "te_residual_norm_bwd", "te_residual_norm_bwd_workspace",
+            "te_dense_residual_fwd", "te_dense_residual_fwd_workspace", "te_dense_residual_bwd",
+            "te_dense_residual_bwd_workspace", "te_grad_norm", "te_clip_grad_norm",
+            "te_grad_norm_workspace"]
 KERNEL_KINDS = ["norm_fwd", "quantize", "act_lu", "dact_dbias", "gemm", "gemm_act", "norm_bwd",
                 "transpose"]
 
@@ -69,6 +73,11 @@ class _Quantizer(ctypes.Structure):
 class _QuantizerSet(ctypes.Structure):
     _fields_ = [("x", _Quantizer), ("kernel1", _Quantizer), ("act", _Quantizer),
                 ("kernel2", _Quantizer), ("grad", _Quantizer)]
+
+
+class _Grad(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("out", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
 
 
 _lib = None
@@ -139,6 +148,23 @@ _SIGS = {
     "te_dact_dbias_ckpt": (ctypes.c_int, [_vp, _vp, _vp, ctypes.c_int, _i64, _i64, ctypes.c_int,
                                           _QP, _vp, ctypes.c_int, _vp, _vp, _vp, _sz, _vp]),
 }
+_int, _GP = ctypes.c_int, ctypes.POINTER(_Grad)
+_SIGS.update({
+    "te_residual_norm_fwd": (_int, [_vp, _int, _vp, _int, _i64, _i64] + [_vp] * 5 + [_i64, _f, _int, _int, _f, _QP,
+                                    _vp, _vp, _int] + [_vp] * 5),
+    "te_residual_norm_bwd_workspace": (_sz, [_i64] * 3),
+    "te_residual_norm_bwd": (_int, [_vp] * 4 + [_int, _int, _i64, _i64] + [_vp] * 8 + [_i64, _f, _int, _int]
+                             + [_vp] * 8 + [_sz, _vp]),
+    "te_dense_residual_fwd_workspace": (_sz, [_i64] * 3 + [_int]),
+    "te_dense_residual_fwd": (_int, [_vp, _vp, _int, _vp, _vp, _vp, _int, _vp, _i64, _vp, _int, _f, _i64, _i64, _i64,
+                                     _vp, _vp, _vp, _sz, _vp]),
+    "te_dense_residual_bwd_workspace": (_sz, [_i64] * 4 + [_int]),
+    "te_dense_residual_bwd": (_int, [_vp, _int, _vp, _vp, _int, _vp, _int, _vp, _i64, _f, _QP, _vp, _vp, _i64, _i64,
+                                     _i64] + [_vp] * 6 + [_sz, _vp]),
+    "te_grad_norm_workspace": (_sz, [_i64]),
+    "te_grad_norm": (_int, [_GP, _i64, _vp, _vp, _sz, _vp]),
+    "te_clip_grad_norm": (_int, [_GP, _i64, ctypes.c_double, ctypes.c_double, _vp, _vp, _sz, _vp]),
+})
 # the checkpoint forms have two pointers (codes, scales) in the place of saved_h
 for _name, _at in (("te_layernorm_mlp_fwd", 17), ("te_layernorm_mlp_bwd", 6)):
     _res, _args = _SIGS[_name]
@@ -640,8 +666,13 @@ def _workspace(op, M, H, N, like, workspace, stream):
     """(tensor, address, bytes) of the given workspace, or of a new one.  Small ones of eager calls
     are kept, one for each host thread and stream of torch's own, whose calls run one after another: an
     allocation costs a short call 5 to 7 us of host time, as much as its launches."""
+    return _workspace_of(_sized(op, M, H, N) if workspace is None else 0, like, workspace, stream)
+
+
+def _workspace_of(n, like, workspace, stream):
+    """The same for a size in bytes."""
     if workspace is None:
-        n = max(_sized(op, M, H, N), 1)
+        n = max(n, 1)
         if n <= _SMALL_WORKSPACE and stream is None and not torch.cuda.is_current_stream_capturing():
             dev = like.get_device()
             key = (dev, _stream(None, dev))
@@ -864,3 +895,204 @@ def te_layernorm_mlp_bwd_ckpt(dy, x, gamma, kernel1, kernel2, h_codes, h_scales,
                                          _stream(stream, dev))
     _check("te_layernorm_mlp_bwd_ckpt", st)
     return dx
+
+
+# ------------------------------------------------------------- around the residual stream ---
+
+
+@functools.lru_cache(maxsize=1024)
+def _sized_by(name, *dims):
+    return int(getattr(lib(), name)(*dims))
+
+
+def _gate(gate, M, H, dtypes, dev):
+    """(address, rows) of a gate [H] or [G, H] whose rows divide M."""
+    if gate is None:
+        return None, 1
+    g = gate.shape[0] if gate.dim() == 2 else 1
+    if gate.dim() == 2:
+        p = _arg("gate", gate, (g, H), dtypes, dev)
+    else:
+        p = _arg("gate", gate, (H,), dtypes, dev)
+    if g < 1 or M % g:
+        raise ValueError(f"gate: its {g} rows do not divide {M}")
+    return p, g
+
+
+def _opt(name, t, shape, dtypes, dev):
+    return None if t is None else _arg(name, t, shape, dtypes, dev)
+
+
+def te_residual_norm_fwd(y, residual, gamma, beta, x_out, out, norm_type="layernorm", zero_centered_gamma=False,
+                         epsilon=1e-6, post_gamma=None, post_beta=None, gate=None, residual_scale=1.0, q=None,
+                         mu=None, rsigma=None, post_mu=None, post_rsigma=None, stream=None):
+    """x_out = residual_scale * residual + gate * p, p = norm(y; post_gamma, post_beta) or y without post_gamma,
+    and out = norm(x_out; gamma, beta), in one pass.  gate: [H], or [G, H] with a row for M / G neighbouring
+    rows.  x_out may be residual."""
+    M, H = y.shape
+    dev = torch.cuda.current_device()
+    d, r = (y.dtype,), (residual.dtype,)
+    py, pr = _arg("y", y, (M, H), _ACT_DTYPES, dev), _arg("residual", residual, (M, H), _ACT_DTYPES, dev)
+    pg, pb = _arg("gamma", gamma, (H,), d, dev), _opt("beta", beta, (H,), d, dev)
+    ppg, ppb = _opt("post_gamma", post_gamma, (H,), d, dev), _opt("post_beta", post_beta, (H,), d, dev)
+    pgt, ng = _gate(gate, M, H, d, dev)
+    px = _arg("x_out", x_out, (M, H), r, dev)
+    po = _arg("out", out, (M, H), _ACT_DTYPES + _E4M3_BYTES, dev)
+    stats = [_opt(n, t, (M,), _F32, dev) for n, t in (("mu", mu), ("rsigma", rsigma), ("post_mu", post_mu),
+                                                      ("post_rsigma", post_rsigma))]
+    cq = None if q is None else ctypes.byref(_quantizer("q", q, dev))
+    st = lib().te_residual_norm_fwd(py, _dt(y), pr, _dt(residual), M, H, pg, pb, ppg, ppb, pgt, ng,
+                                    float(residual_scale), _norm_id(norm_type), int(bool(zero_centered_gamma)),
+                                    float(epsilon), cq, px, po, _dt(out), *stats, _stream(stream, dev))
+    _check("te_residual_norm_fwd", st)
+    return out
+
+
+def te_residual_norm_bwd(dout, dx_out, x_out, mu, rsigma, gamma, dresidual, dy, dgamma, dbeta=None, y=None,
+                         post_mu=None, post_rsigma=None, post_gamma=None, post_beta=None, gate=None,
+                         residual_scale=1.0, dpost_gamma=None, dpost_beta=None, dgate=None, norm_type="layernorm",
+                         zero_centered_gamma=False, workspace=None, stream=None):
+    """Gradients of te_residual_norm_fwd from dout (of out) and dx_out (what reaches x_out otherwise, or None).
+    dresidual (may be dx_out) and dy may be None; y is needed with a post norm or a gate."""
+    M, H = dout.shape
+    dev = torch.cuda.current_device()
+    d, r = (dout.dtype,), (x_out.dtype,)
+    pd, pxo = _arg("dout", dout, (M, H), _ACT_DTYPES, dev), _opt("dx_out", dx_out, (M, H), r, dev)
+    px = _arg("x_out", x_out, (M, H), _ACT_DTYPES, dev)
+    py = _opt("y", y, (M, H), d, dev)
+    stats = [_opt(n, t, (M,), _F32, dev) for n, t in (("mu", mu), ("rsigma", rsigma), ("post_mu", post_mu),
+                                                      ("post_rsigma", post_rsigma))]
+    vecs = [_opt(n, t, (H,), d, dev) for n, t in (("gamma", gamma), ("post_gamma", post_gamma),
+                                                  ("post_beta", post_beta))]
+    pgt, ng = _gate(gate, M, H, d, dev)
+    pdr, pdy = _opt("dresidual", dresidual, (M, H), r, dev), _opt("dy", dy, (M, H), d, dev)
+    grads = [_opt(n, t, (H,), _F32, dev) for n, t in (("dgamma", dgamma), ("dbeta", dbeta),
+                                                      ("dpost_gamma", dpost_gamma), ("dpost_beta", dpost_beta))]
+    pdg = None if dgate is None else _arg("dgate", dgate, (H,) if gate is not None and gate.dim() == 1 else (ng, H),
+                                          _F32, dev)
+    n = _sized_by("te_residual_norm_bwd_workspace", M, H, ng) if workspace is None else 0
+    workspace, pw, nw = _workspace_of(n, dout, workspace, stream)
+    st = lib().te_residual_norm_bwd(pd, pxo, px, py, _dt(dout), _dt(x_out), M, H, *stats, *vecs, pgt, ng,
+                                    float(residual_scale), _norm_id(norm_type), int(bool(zero_centered_gamma)), pdr,
+                                    pdy, *grads, pdg, pw, nw, _stream(stream, dev))
+    _check("te_residual_norm_bwd", st)
+
+
+def te_dense_residual_fwd(x, kernel, residual, out, bias=None, activation="identity", gate=None, residual_scale=1.0,
+                          saved_z=None, x_scale_inv=None, kernel_scale_inv=None, workspace=None, stream=None):
+    """out = residual_scale * residual + gate * act(x @ kernel + bias); x [M, K] and kernel [K, N] bfloat16 or
+    E4M3, bias and gate ([N] or [G, N]) bfloat16.  out may be residual; saved_z [M, N] bfloat16 receives
+    x @ kernel + bias."""
+    M, K = x.shape
+    N = kernel.shape[1]
+    dev = torch.cuda.current_device()
+    bf = (torch.bfloat16,)
+    e4m3 = x.dtype in _E4M3_BYTES
+    px = _arg("x", x, (M, K), bf + _E4M3_BYTES, dev)
+    pk = _arg("kernel", kernel, (K, N), _E4M3_BYTES if e4m3 else bf, dev)
+    pr = _arg("residual", residual, (M, N), _ACT_DTYPES, dev)
+    po = _arg("out", out, (M, N), (residual.dtype,), dev)
+    pb, pz = _opt("bias", bias, (N,), bf, dev), _opt("saved_z", saved_z, (M, N), bf, dev)
+    pgt, ng = _gate(gate, M, N, bf, dev)
+    n = _sized_by("te_dense_residual_fwd_workspace", M, K, N, _dt(x)) if workspace is None else 0
+    pw, nw = None, 0
+    if n or workspace is not None:
+        workspace, pw, nw = _workspace_of(n, x, workspace, stream)
+    st = lib().te_dense_residual_fwd(px, pk, _dt(x), _scalar("x_scale_inv", x_scale_inv, dev),
+                                     _scalar("kernel_scale_inv", kernel_scale_inv, dev), pb, _act_id(activation), pgt,
+                                     ng, pr, _dt(residual), float(residual_scale), M, K, N, po, pz, pw, nw,
+                                     _stream(stream, dev))
+    _check("te_dense_residual_fwd", st)
+    return out
+
+
+def te_dense_residual_bwd(dout, x, kernel, dx, dkernel, dresidual=None, saved_z=None, activation="identity", gate=None,
+                          residual_scale=1.0, dbias=None, dgate=None, q=None, x_scale_inv=None, kernel_scale_inv=None,
+                          workspace=None, stream=None):
+    """Gradients of te_dense_residual_fwd from dout [M, N]; q: the quantizer of dz with E4M3 operands."""
+    M, K = x.shape
+    N = kernel.shape[1]
+    dev = torch.cuda.current_device()
+    bf = (torch.bfloat16,)
+    e4m3 = x.dtype in _E4M3_BYTES
+    px = _arg("x", x, (M, K), bf + _E4M3_BYTES, dev)
+    pk = _arg("kernel", kernel, (K, N), _E4M3_BYTES if e4m3 else bf, dev)
+    pd = _arg("dout", dout, (M, N), _ACT_DTYPES, dev)
+    pz = _opt("saved_z", saved_z, (M, N), bf, dev)
+    pgt, ng = _gate(gate, M, N, bf, dev)
+    pdx, pdk = _arg("dx", dx, (M, K), bf, dev), _arg("dkernel", dkernel, (K, N), bf, dev)
+    pdr = _opt("dresidual", dresidual, (M, N), (dout.dtype,), dev)
+    pdb = _opt("dbias", dbias, (N,), _F32, dev)
+    pdg = None if dgate is None else _arg("dgate", dgate, (N,) if gate is not None and gate.dim() == 1 else (ng, N),
+                                          _F32, dev)
+    cq = None if q is None else ctypes.byref(_quantizer("q", q, dev))
+    n = _sized_by("te_dense_residual_bwd_workspace", M, K, N, ng, _dt(x)) if workspace is None else 0
+    workspace, pw, nw = _workspace_of(n, x, workspace, stream)
+    st = lib().te_dense_residual_bwd(pd, _dt(dout), px, pk, _dt(x), pz, _act_id(activation), pgt, ng,
+                                     float(residual_scale), cq, _scalar("x_scale_inv", x_scale_inv, dev),
+                                     _scalar("kernel_scale_inv", kernel_scale_inv, dev), M, K, N, pdx, pdk, pdr, pdb,
+                                     pdg, pw, nw, _stream(stream, dev))
+    _check("te_dense_residual_bwd", st)
+    return dx
+
+
+class GradList:
+    """Gradients for te_grad_norm and te_clip_grad_norm, checked and laid out once: dense float32 / bfloat16
+    tensors on one device, and outs, where their clipped values go (None: in place).  It keeps the tensors;
+    one that has moved since (a new .data) is checked and laid out again at the next call."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = None if outs is None else list(outs)
+        if self.outs is not None and len(self.outs) != len(self.grads):
+            raise ValueError("outs: one for each gradient")
+        self._at = None
+        self._table()
+
+    def _where(self):
+        at = list(map(torch.Tensor.data_ptr, self.grads))
+        return at if self.outs is None else at + list(map(torch.Tensor.data_ptr, self.outs))
+
+    def _table(self):
+        """The C table, its device and the first gradient (None of an empty list)."""
+        at = self._where()
+        if at == self._at:
+            return
+        self._c = (_Grad * max(len(self.grads), 1))()
+        self.device = self.grads[0].get_device() if self.grads else None
+        for i, g in enumerate(self.grads):
+            p = _arg("grads", g, g.shape, _ACT_DTYPES, self.device)
+            o = None if self.outs is None else _arg("outs", self.outs[i], g.shape, (g.dtype,), self.device)
+            self._c[i] = _Grad(p, o, g.numel(), _dt(g))
+        self._at = at
+
+
+def _grad_args(grads, norm, outs, workspace, stream):
+    if not isinstance(grads, GradList):
+        grads = GradList(grads, outs)
+    elif outs is not None:
+        raise ValueError("outs: given with the GradList")
+    grads._table()
+    dev = torch.cuda.current_device()
+    if grads.device is not None and grads.device != dev:
+        raise ValueError(f"grads: tensors must live on the current device (cuda:{dev})")
+    pn = _arg("norm", norm.reshape(-1), (1,), _F32, dev)
+    n = len(grads.grads)
+    size = _sized_by("te_grad_norm_workspace", n) if workspace is None else 0
+    workspace, pw, nw = _workspace_of(size, norm, workspace, stream)
+    return grads, n, pn, workspace, pw, nw, _stream(stream, dev)
+
+
+def te_grad_norm(grads, norm, workspace=None, stream=None):
+    """norm (one float32) = the root of the sum of the squares of all values of the tensors `grads` (a list, or
+    a GradList)."""
+    grads, n, pn, workspace, pw, nw, s = _grad_args(grads, norm, None, workspace, stream)
+    _check("te_grad_norm", lib().te_grad_norm(grads._c, n, pn, pw, nw, s))
+    return norm
+
+
+def te_clip_grad_norm(grads, max_norm, norm, outs=None, epsilon=1e-6, workspace=None, stream=None):
+    """te_grad_norm, and every value times min(1, max_norm / (norm + epsilon)): in place, or into outs."""
+    grads, n, pn, workspace, pw, nw, s = _grad_args(grads, norm, outs, workspace, stream)
+    _check("te_clip_grad_norm", lib().te_clip_grad_norm(grads._c, n, float(max_norm), float(epsilon), pn, pw, nw, s))
+    return norm

@@ -18,7 +18,7 @@
 //              scale by the FP8 dequantization factor, add the bias, round the pre-activation,
 //              apply the activation (a gated pair's gate and linear halves sit in the two
 //              column halves of one accumulator tile), track amax, and store fp32 / bf16 /
-//              E4M3.
+//              E4M3; the RES kernels end in a residual stream (D = a residual + gate * act).
 // The epilogue of tile i overlaps the MMAs of tile i + 1.  Tiles go in raster groups of m-tiles
 // that keep their A rows in L2; a B of at most 64 MB is instead kept in L2 for the whole GEMM
 // (n fastest, with L2 eviction hints on the loads) while A streams through once.
@@ -97,6 +97,11 @@ struct GemmDev {
   uint8_t* h_codes;   // the same in MXFP8, and its scale tiles
   uint8_t* h_scales;
   int64_t h_groups;   // scale tiles along a row of tiles
+  // RES kernels: D = residual_scale * residual + gate * act(h), residual in D's dtype
+  const void* residual;
+  float residual_scale;
+  const void* gate;    // [M / gate_rows, N] bf16, or null
+  uint32_t gate_rows;
   void* D;
   int d_dtype;
   const float* out_scale;
@@ -397,7 +402,56 @@ __device__ __forceinline__ f32x2 round_bf16_2(f32x2 v) {
 
 // ------------------------------------------------------------------ the kernel ------------
 
-template <int KIND, bool A_KMAJOR, bool B_KMAJOR, int CG>
+// 32 values (`count` of them there) of one row of an fp32 or bf16 tensor, as raw words.
+__device__ __forceinline__ void load_seg(const void* base, int64_t off, int count, int dtype, uint4 (&w)[8]) {
+  const int n = dtype == TE_BF16 ? count / 8 : count / 4;
+  const uint4* p = dtype == TE_BF16 ? reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + off)
+                                    : reinterpret_cast<const uint4*>(static_cast<const float*>(base) + off);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = i < n ? p[i] : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// v = residual_scale * residual + gate * v for a chunk of 32 values of one row.
+__device__ __forceinline__ void residual_chunk(const GemmDev& g, int64_t row, int64_t col0, int count,
+                                               const uint4 (&r)[8], float (&v)[32]) {
+  if (g.gate) {
+    const uint16_t* gt = static_cast<const uint16_t*>(g.gate) + int64_t(uint32_t(row) / g.gate_rows) * g.N + col0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (8 * i < count) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4*>(gt) + i);
+        const f32x2 q[4] = {bf16x2_f2(w.x), bf16x2_f2(w.y), bf16x2_f2(w.z), bf16x2_f2(w.w)};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          v[8 * i + 2 * k] *= q[k].x;
+          v[8 * i + 2 * k + 1] *= q[k].y;
+        }
+      }
+    }
+  }
+  const float s = g.residual_scale;
+  if (g.d_dtype == TE_BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {r[i].x, r[i].y, r[i].z, r[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        v[8 * i + 2 * k] = fmaf(s, bf16_lo(w[k]), v[8 * i + 2 * k]);
+        v[8 * i + 2 * k + 1] = fmaf(s, bf16_hi(w[k]), v[8 * i + 2 * k + 1]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[4 * i] = fmaf(s, __uint_as_float(r[i].x), v[4 * i]);
+      v[4 * i + 1] = fmaf(s, __uint_as_float(r[i].y), v[4 * i + 1]);
+      v[4 * i + 2] = fmaf(s, __uint_as_float(r[i].z), v[4 * i + 2]);
+      v[4 * i + 3] = fmaf(s, __uint_as_float(r[i].w), v[4 * i + 3]);
+    }
+  }
+}
+
+template <int KIND, bool A_KMAJOR, bool B_KMAJOR, int CG, bool RES>
 __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant__ GemmParams p) {
   using C = Cfg<CG>;
   constexpr int STAGES = C::kStages;
@@ -683,6 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           tmem_ld32(taddr + c * 32, r);
           f32x2 bz[16];  // the chunk's bias, loaded while the accumulator columns arrive
           load_bias_chunk(g.bias, g.bias_dtype, col0, count, bz);
+          uint4 res[8];  // and its residual
+          if constexpr (RES) load_seg(g.residual, row * g.N + col0, row_ok ? count : 0, g.d_dtype, res);
           tmem_ld_wait();
           float v[32];
 #pragma unroll
@@ -696,6 +752,11 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
             if (g.saved_h && row_ok) store_seg(g.saved_h, row * g.N + col0, v, count, g.h_dtype, 1.0f);
             if (g.h_codes && row_ok) store_checkpoint(g, row, col0, v);
             act_chunk(g.act, v);
+          }
+          if constexpr (RES) {
+            if (g.saved_h && row_ok) store_seg(g.saved_h, row * g.N + col0, v, count, TE_BF16, 1.0f);
+            act_chunk(g.act, v);
+            if (row_ok) residual_chunk(g, row, col0, count, res, v);
           }
           if (row_ok) {
             if (g.amax_out) amax = chunk_amax(amax, v, count);
@@ -766,13 +827,13 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
 
 // ------------------------------------------------------------------ host side -------------
 
-template <int KIND, bool AK, bool BK, int CG>
+template <int KIND, bool AK, bool BK, int CG, bool RES = false>
 te_status launch_t(GemmParams& prm, int grid, cudaStream_t s) {
   constexpr size_t smem = Cfg<CG>::kSmem;
   static PerDevice<bool> attr_set;
   bool ok = false;
   if (!attr_set.get(&ok, [](bool* v) {
-        *v = cudaFuncSetAttribute(gemm_kernel<KIND, AK, BK, CG>,
+        *v = cudaFuncSetAttribute(gemm_kernel<KIND, AK, BK, CG, RES>,
                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   int(smem)) == cudaSuccess;
         return *v;
@@ -794,7 +855,7 @@ te_status launch_t(GemmParams& prm, int grid, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = CG == 1 ? 1 : 2;
-  if (cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, AK, BK, CG>, prm) != cudaSuccess) return TE_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, gemm_kernel<KIND, AK, BK, CG, RES>, prm) != cudaSuccess) return TE_ERR_CUDA;
   return cudaGetLastError() == cudaSuccess ? TE_OK : TE_ERR_CUDA;
 }
 
@@ -981,6 +1042,10 @@ te_status launch_gemm(const GemmArgs& a, cudaStream_t s) {
   g.h_codes = static_cast<uint8_t*>(a.h_codes);
   g.h_scales = static_cast<uint8_t*>(a.h_scales);
   g.h_groups = scale_groups(TE_MXFP8, a.N);
+  g.residual = a.residual;
+  g.residual_scale = a.residual_scale;
+  g.gate = a.gate;
+  g.gate_rows = uint32_t(a.gate_rows);
   g.D = a.D;
   g.d_dtype = a.cast.out_dtype;
   g.out_scale = a.cast.scale;
@@ -1003,6 +1068,12 @@ te_status launch_gemm(const GemmArgs& a, cudaStream_t s) {
   const int64_t items = sp.full_tiles + (tiles - sp.full_tiles) * sp.split;
   const int grid = int(items < slots ? items : slots) * cg;
   ProfileScope prof(a.epilogue == EPI_BIAS ? TE_KERNEL_GEMM : TE_KERNEL_GEMM_ACT, s);
+  if (a.epilogue == EPI_RESIDUAL) {  // bf16 or E4M3, the weights stored [K, N]
+    if (kind == 2 || !a.a_kmajor || a.b_kmajor) return TE_ERR_UNSUPPORTED;
+    if (kind == 0)
+      return cg == 1 ? launch_t<0, true, false, 1, true>(prm, grid, s) : launch_t<0, true, false, 2, true>(prm, grid, s);
+    return cg == 1 ? launch_t<1, true, false, 1, true>(prm, grid, s) : launch_t<1, true, false, 2, true>(prm, grid, s);
+  }
   if (cg == 1) {
     if (kind == 0) return launch_kind<0, 1>(prm, grid, a.a_kmajor, a.b_kmajor, s);
     if (kind == 1) return launch_kind<1, 1>(prm, grid, a.a_kmajor, a.b_kmajor, s);

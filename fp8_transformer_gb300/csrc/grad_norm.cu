@@ -1,0 +1,345 @@
+// The global norm of many gradients and their clipping: n = sqrt(sum of g^2), out = g min(1, max / (n + eps)).
+//
+// The tensors go in a kernel's parameters, up to 512 of them a launch, so that a call needs no table
+// in device memory and can be captured.  They are cut into chunks of 1024 vectors of 16 bytes; a CTA
+// takes every grid-th chunk.  The squares pass is bound by reading; the scaling pass reads again (the
+// last chunks first, which the squares pass left in L2) and writes.
+//
+// Sums: a thread adds the squares of its 32 (bf16) or 16 (fp32) values of a chunk in fp32, and the
+// chunks' sums as an unevaluated pair of fp32, which loses nothing a double would keep; fp64
+// instructions are two orders slower here and would bound the pass.  Where a chunk's fp32 sum leaves
+// [2^-80, 2^100] (a square overflowed, or small ones vanished), the thread takes that chunk's squares
+// again in fp64, so that the norm is right wherever it is a finite fp32.
+#include "cast.cuh"
+#include "common.cuh"
+#include "kernels.h"
+
+namespace te {
+
+namespace {
+
+constexpr int kThreads = 512;
+constexpr int kVecs = 1024;              // vectors of 16 bytes in a chunk
+constexpr int kPer = kVecs / kThreads;   // of a thread
+constexpr int kCtasPerSm = 4;
+constexpr int kSmall = 32, kLarge = 512;  // tensors of one launch
+
+template <int CAP>
+struct Table {
+  const void* src[CAP];
+  void* dst[CAP];
+  int64_t n[CAP];
+  uint32_t first[CAP + 1];  // the tensor's first chunk
+  uint8_t bf16[CAP];
+  int count;
+};
+
+// A tensor cut at 16-byte boundaries of its source.
+struct Cut {
+  int64_t vecs;  // whole vectors
+  int head;      // elements before them
+  int tail;      // and behind
+};
+
+__host__ __device__ __forceinline__ Cut cut_of(const void* p, int64_t n, int es) {
+  Cut c;
+  const int64_t lead = int64_t((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / es;
+  c.head = int(lead < n ? lead : n);
+  c.vecs = (n - c.head) / (16 / es);
+  c.tail = int((n - c.head) % (16 / es));
+  return c;
+}
+
+template <int CAP>
+__device__ __forceinline__ int tensor_of(const Table<CAP>& t, uint32_t chunk) {
+  int lo = 0, hi = t.count - 1;  // the last tensor whose first chunk is at or before it
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= chunk) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float element(const void* p, int64_t i, bool bf16) {
+  return bf16 ? __uint_as_float(uint32_t(static_cast<const uint16_t*>(p)[i]) << 16) : static_cast<const float*>(p)[i];
+}
+
+__device__ __forceinline__ void store_element(void* p, int64_t i, bool bf16, float v) {
+  if (bf16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
+  else static_cast<float*>(p)[i] = v;
+}
+
+__device__ __forceinline__ double square64(const uint4& w, bool bf16) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  double s = 0.0;
+  for (int i = 0; i < 4; ++i) {
+    if (bf16) {
+      const double lo = bf16_lo(u[i]), hi = bf16_hi(u[i]);
+      s += lo * lo + hi * hi;
+    } else {
+      const double v = __uint_as_float(u[i]);
+      s += v * v;
+    }
+  }
+  return s;
+}
+
+__device__ __noinline__ double chunk64(const uint4 (&w)[kPer], bool bf16) {
+  double s = 0.0;
+  for (int k = 0; k < kPer; ++k) s += square64(w[k], bf16);
+  return s;
+}
+
+__device__ __forceinline__ double warp_sum64(double v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 2048 / kThreads) grad_squares_kernel(const __grid_constant__ Table<CAP> t,
+                                                                                uint32_t chunks, double* slots) {
+  __shared__ double red[kThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x;
+  float hi = 0.0f, lo = 0.0f;  // their exact sum is the squares so far
+  double rest = 0.0;           // squares taken in fp64
+  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    const int i = tensor_of(t, c);
+    const bool bf16 = t.bf16[i];
+    const void* p = t.src[i];
+    const Cut cut = cut_of(p, t.n[i], bf16 ? 2 : 4);
+    const uint32_t at = c - t.first[i];
+    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + int64_t(cut.head) * (bf16 ? 2 : 4));
+    uint4 w[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int64_t n = int64_t(at) * kVecs + tid + k * kThreads;
+      w[k] = n < cut.vecs ? v[n] : make_uint4(0u, 0u, 0u, 0u);
+    }
+    f32x2 s0 = f2s(0.0f), s1 = f2s(0.0f);
+    uint32_t any = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      any |= (w[k].x | w[k].y | w[k].z | w[k].w) & 0x7fff7fffu;
+      if (bf16) {
+        f32x2 q[4];
+        Pairs<__nv_bfloat16>::cvt(w[k], q);
+        s0 = fma2(q[0], q[0], s0);
+        s1 = fma2(q[1], q[1], s1);
+        s0 = fma2(q[2], q[2], s0);
+        s1 = fma2(q[3], q[3], s1);
+      } else {
+        any |= (w[k].x | w[k].y | w[k].z | w[k].w) & 0x7fffffffu;
+        f32x2 q[2];
+        Pairs<float>::cvt(w[k], q);
+        s0 = fma2(q[0], q[0], s0);
+        s1 = fma2(q[1], q[1], s1);
+      }
+    }
+    s0 = add2(s0, s1);
+    const float s = f2lo(s0) + f2hi(s0);
+    if (s >= 0x1p-80f && s <= 0x1p100f) {
+      const float sum = hi + s, b = sum - hi;  // the sum's rounding error, exactly
+      lo += (hi - (sum - b)) + (s - b);
+      hi = sum;
+    } else if (any) {
+      rest += chunk64(w, bf16);
+    }
+    if (at == 0) {  // the ends that no vector covers
+      const int64_t n = t.n[i];
+      if (tid < cut.head) {
+        const double x = element(p, tid, bf16);
+        rest += x * x;
+      } else if (tid >= 32 && tid < 32 + cut.tail) {
+        const double x = element(p, n - cut.tail + (tid - 32), bf16);
+        rest += x * x;
+      }
+    }
+  }
+  const double total = warp_sum64(double(hi) + (double(lo) + rest));
+  if ((tid & 31) == 0) red[tid >> 5] = total;
+  __syncthreads();
+  if (tid == 0) {
+    double sum = 0.0;
+    for (int w = 0; w < kThreads / 32; ++w) sum += red[w];
+    slots[blockIdx.x] = sum;
+  }
+}
+
+// The norm from the slots, by one warp, in a fixed order: the same bits in every CTA.
+__device__ __forceinline__ double norm_of(const double* slots, int used, int lane) {
+  double s = 0.0;
+#pragma unroll 4
+  for (int i = lane; i < used; i += 32) s += __ldcg(slots + i);
+  return sqrt(warp_sum64(s));
+}
+
+__global__ void grad_norm_kernel(const double* slots, int used, float* norm) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const double n = norm_of(slots, used, threadIdx.x);
+  if (threadIdx.x == 0) *norm = float(n);
+}
+
+template <int CAP>
+__global__ void __launch_bounds__(kThreads, 2048 / kThreads) grad_clip_kernel(const __grid_constant__ Table<CAP> t,
+                                                                             uint32_t chunks, const double* slots,
+                                                                             int used, double max_norm, double eps,
+                                                                             float* norm) {
+  __shared__ float factor;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int tid = threadIdx.x;
+  if (tid < 32) {
+    const double n = norm_of(slots, used, tid);
+    if (tid == 0) {
+      const double c = n + eps == 0.0 ? 1.0 : max_norm / (n + eps);
+      factor = c > 1.0 ? 1.0f : float(c);  // a NaN stays one
+      if (blockIdx.x == 0 && norm) *norm = float(n);
+    }
+  }
+  __syncthreads();
+  const float f = factor;
+  const f32x2 f2v = f2s(f);
+  // the last chunks first: they are what the squares pass has left in L2
+  for (int64_t back = int64_t(chunks) - 1 - blockIdx.x; back >= 0; back -= gridDim.x) {
+    const uint32_t c = uint32_t(back);
+    const int i = tensor_of(t, c);
+    const bool bf16 = t.bf16[i];
+    const void* p = t.src[i];
+    void* d = t.dst[i];
+    if (f == 1.0f && p == d) continue;  // nothing changes
+    const int es = bf16 ? 2 : 4;
+    const Cut cut = cut_of(p, t.n[i], es);
+    const uint32_t at = c - t.first[i];
+    const int64_t n = t.n[i];
+    const int64_t v0 = int64_t(at) * kVecs;
+    if (((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(d)) & 15) == 0) {
+      const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + int64_t(cut.head) * es);
+      uint4* o = reinterpret_cast<uint4*>(static_cast<char*>(d) + int64_t(cut.head) * es);
+      uint4 w[kPer];
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int64_t m = v0 + tid + k * kThreads;
+        if (m < cut.vecs) w[k] = v[m];
+      }
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) {
+        const int64_t m = v0 + tid + k * kThreads;
+        if (m >= cut.vecs) break;
+        uint4 r;
+        if (bf16) {
+          f32x2 q[4];
+          Pairs<__nv_bfloat16>::cvt(w[k], q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[e] = mul2(q[e], f2v);
+          r = make_uint4(pack_bf16x2(q[0].x, q[0].y), pack_bf16x2(q[1].x, q[1].y), pack_bf16x2(q[2].x, q[2].y),
+                         pack_bf16x2(q[3].x, q[3].y));
+        } else {
+          f32x2 q[2];
+          Pairs<float>::cvt(w[k], q);
+          q[0] = mul2(q[0], f2v);
+          q[1] = mul2(q[1], f2v);
+          r = make_uint4(__float_as_uint(q[0].x), __float_as_uint(q[0].y), __float_as_uint(q[1].x),
+                         __float_as_uint(q[1].y));
+        }
+        __stcs(o + m, r);
+      }
+    } else {  // ends of another alignment: one element at a time
+      const int64_t e0 = cut.head + v0 * (16 / es);
+      const int64_t last = v0 + kVecs < cut.vecs ? v0 + kVecs : cut.vecs;
+      const int64_t e1 = cut.head + last * (16 / es);
+      for (int64_t e = e0 + tid; e < e1; e += kThreads) store_element(d, e, bf16, element(p, e, bf16) * f);
+    }
+    if (at == 0) {
+      if (tid < cut.head) store_element(d, tid, bf16, element(p, tid, bf16) * f);
+      else if (tid >= 32 && tid < 32 + cut.tail) {
+        const int64_t e = n - cut.tail + (tid - 32);
+        store_element(d, e, bf16, element(p, e, bf16) * f);
+      }
+    }
+  }
+}
+
+int max_grid() { return num_sms() * kCtasPerSm; }
+
+uint32_t chunks_of(const GradTensor& g) {
+  const Cut c = cut_of(g.data, g.numel, g.dtype == TE_BF16 ? 2 : 4);
+  const int64_t n = ceil_div(c.vecs, int64_t(kVecs));
+  return uint32_t(n > 0 ? n : 1);
+}
+
+// Runs launch(table, chunks, grid) over the tensors, in batches of up to CAP.
+template <int CAP, class Launch>
+te_status batches(const GradTensor* g, int64_t count, Launch&& launch) {
+  Table<CAP> t;
+  for (int64_t i = 0; i < count;) {
+    t.count = 0;
+    uint64_t chunks = 0;
+    for (; i < count && t.count < CAP; ++i) {
+      if (g[i].numel == 0) continue;
+      const uint64_t more = chunks_of(g[i]);
+      if (chunks + more > 0x7fffffffull) {
+        if (t.count == 0) return TE_ERR_UNSUPPORTED;
+        break;
+      }
+      t.src[t.count] = g[i].data;
+      t.dst[t.count] = g[i].out;
+      t.n[t.count] = g[i].numel;
+      t.bf16[t.count] = g[i].dtype == TE_BF16;
+      t.first[t.count++] = uint32_t(chunks);
+      chunks += more;
+    }
+    if (t.count == 0) break;
+    t.first[t.count] = uint32_t(chunks);
+    const int grid = int(chunks < uint64_t(max_grid()) ? chunks : uint64_t(max_grid()));
+    const te_status st = launch(t, uint32_t(chunks), grid);
+    if (st != TE_OK) return st;
+  }
+  return TE_OK;
+}
+
+template <int CAP>
+te_status squares(const GradTensor* g, int64_t count, double* slots, int* used, cudaStream_t s) {
+  return batches<CAP>(g, count, [&](const Table<CAP>& t, uint32_t chunks, int grid) {
+    grad_squares_kernel<CAP><<<grid, kThreads, 0, s>>>(t, chunks, slots + *used);
+    *used += grid;
+    return cudaGetLastError() == cudaSuccess ? TE_OK : TE_ERR_CUDA;
+  });
+}
+
+template <int CAP>
+te_status clip(const GradTensor* g, int64_t count, const double* slots, int used, double max_norm, double eps,
+               float* norm, cudaStream_t s) {
+  return batches<CAP>(g, count, [&](const Table<CAP>& t, uint32_t chunks, int grid) {
+    const te_status st = launch_dependent(grad_clip_kernel<CAP>, dim3(unsigned(grid)), dim3(kThreads), s, t, chunks,
+                                          slots, used, max_norm, eps, norm);
+    norm = nullptr;  // the first launch writes it
+    return st;
+  });
+}
+
+}  // namespace
+
+size_t grad_norm_workspace(int64_t count) {
+  if (count <= 0) return 0;
+  return size_t(ceil_div(count, int64_t(kLarge)) + 1) * size_t(max_grid()) * sizeof(double);
+}
+
+te_status launch_grad_squares(const GradTensor* t, int64_t count, double* slots, int* used, cudaStream_t s) {
+  ProfileScope prof(TE_KERNEL_QUANTIZE, s);
+  *used = 0;
+  return count <= kSmall ? squares<kSmall>(t, count, slots, used, s) : squares<kLarge>(t, count, slots, used, s);
+}
+
+te_status launch_grad_norm(const double* slots, int used, float* norm, cudaStream_t s) {
+  return launch_dependent(grad_norm_kernel, dim3(1), dim3(32), s, slots, used, norm);
+}
+
+te_status launch_grad_clip(const GradTensor* t, int64_t count, const double* slots, int used, double max_norm,
+                           double eps, float* norm, cudaStream_t s) {
+  return count <= kSmall ? clip<kSmall>(t, count, slots, used, max_norm, eps, norm, s)
+                         : clip<kLarge>(t, count, slots, used, max_norm, eps, norm, s);
+}
+
+}  // namespace te

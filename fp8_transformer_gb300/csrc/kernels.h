@@ -67,6 +67,65 @@ struct NormBwdArgs {
 };
 te_status launch_norm_bwd(const NormBwdArgs& a, cudaStream_t s);
 
+// p = norm(y) or y, x_out = residual_scale * residual + gate * p, out = norm(x_out).
+struct ResidualNormArgs {
+  const void* y = nullptr;         // [M, H] y_dtype
+  const void* residual = nullptr;  // [M, H] residual_dtype
+  int y_dtype = TE_BF16, residual_dtype = TE_BF16;
+  int64_t M = 0, H = 0;
+  const void* gamma = nullptr;       // [H] y_dtype, like the vectors below
+  const void* beta = nullptr;
+  const void* post_gamma = nullptr;  // null: no norm of y
+  const void* post_beta = nullptr;
+  const void* gate = nullptr;        // [M / gate_rows, H] or null
+  int64_t gate_rows = 1;             // rows that share a gate row
+  float residual_scale = 1.0f;
+  int norm_type = TE_LAYERNORM;
+  int zero_centered_gamma = 0;
+  float eps = 1e-6f;
+  void* x_out = nullptr;  // [M, H] residual_dtype; may be residual
+  void* out = nullptr;
+  float* mu = nullptr;
+  float* rsigma = nullptr;
+  float* post_mu = nullptr;
+  float* post_rsigma = nullptr;
+  CastSpec cast;
+};
+te_status launch_residual_norm_fwd(const ResidualNormArgs& a, cudaStream_t s);
+
+struct ResidualNormBwdArgs {
+  const void* dout = nullptr;    // [M, H] dtype
+  const void* dx_out = nullptr;  // [M, H] residual_dtype, or null
+  const void* x_out = nullptr;   // [M, H] residual_dtype
+  const void* y = nullptr;       // [M, H] dtype; read with a post norm or a gate
+  int dtype = TE_BF16, residual_dtype = TE_BF16;
+  int64_t M = 0, H = 0;
+  const float* mu = nullptr;
+  const float* rsigma = nullptr;
+  const float* post_mu = nullptr;
+  const float* post_rsigma = nullptr;
+  const void* gamma = nullptr;
+  const void* post_gamma = nullptr;
+  const void* post_beta = nullptr;
+  const void* gate = nullptr;
+  int64_t gate_rows = 1;
+  float residual_scale = 1.0f;
+  int norm_type = TE_LAYERNORM;
+  int zero_centered_gamma = 0;
+  void* dresidual = nullptr;  // [M, H] residual_dtype or null; may be dx_out
+  void* dy = nullptr;         // [M, H] dtype or null
+  float* dgamma = nullptr;
+  float* dbeta = nullptr;
+  float* dpost_gamma = nullptr;
+  float* dpost_beta = nullptr;
+  float* dgate = nullptr;          // [M / gate_rows, H]
+  float* partials = nullptr;       // workspace
+  float* gate_partials = nullptr;  // set at launch, like rows_per_cta
+  int64_t rows_per_cta = 1;
+};
+te_status launch_residual_norm_bwd(const ResidualNormBwdArgs& a, cudaStream_t s);
+size_t residual_norm_bwd_workspace(int64_t M, int64_t H, int64_t gates);
+
 // Workspace of te_layernorm_mlp_fwd_host: device staging of x and out plus one forward's.
 size_t host_fwd_workspace(int64_t M, int64_t H, int64_t F, int dtype, int act);
 size_t norm_bwd_workspace(int64_t M, int64_t H);
@@ -186,7 +245,9 @@ struct ScaleUpdateArgs {
 te_status launch_update_scales(const ScaleUpdateArgs& a, cudaStream_t s);
 
 // Tensor-core GEMM D[M, N] = epilogue(alpha * op(A) op(B)).
-enum Epilogue { EPI_BIAS = 0, EPI_BIAS_ACT = 1, EPI_BIAS_GATED = 2 };
+// EPI_RESIDUAL: D = residual_scale * residual + gate * act(alpha op(A) op(B) + bias); A K-major, B
+// stored [K, N], bf16 or E4M3.
+enum Epilogue { EPI_BIAS = 0, EPI_BIAS_ACT = 1, EPI_BIAS_GATED = 2, EPI_RESIDUAL = 3 };
 
 struct GemmArgs {
   const void* A = nullptr;
@@ -205,6 +266,10 @@ struct GemmArgs {
   void* saved_h = nullptr;      // [M, N] pre-activation, h_dtype
   void* h_codes = nullptr;      // [M, N] pre-activation in MXFP8 (N a multiple of 32), or null
   void* h_scales = nullptr;
+  const void* residual = nullptr;  // EPI_RESIDUAL: [M, N] in D's dtype; may be D
+  float residual_scale = 1.0f;
+  const void* gate = nullptr;      // [M / gate_rows, N] bf16, or null
+  int64_t gate_rows = 1;
   void* D = nullptr;            // [M, N] or [M, N/2] gated
   CastSpec cast;                // output stage of D (amax / E4M3 of the activation)
   // Optional scratch (256-byte aligned) for splitting the last wave's tiles along K; without it
@@ -241,6 +306,37 @@ te_status launch_block_gemm(const BlockGemmArgs& a, cudaStream_t s);
 // kFewPacked only (TE_ERR_UNSUPPORTED beyond).
 constexpr int64_t kFewPacked = 8;
 te_status launch_block_gemm_packing(const BlockGemmArgs& g, const BlockQuantArgs& q, cudaStream_t s);
+
+// The gradient of that epilogue: dz = gate * dout * act'(z), with its column sums (dbias), those of
+// dout * act(z) over each gate's rows (dgate), and residual_scale * dout.
+struct DenseResidualGradArgs {
+  const void* dout = nullptr;  // [M, N] dtype
+  const void* z = nullptr;     // [M, N] bf16; read with an activation or for dgate
+  int dtype = TE_BF16;
+  int64_t M = 0, N = 0;
+  int act = TE_IDENTITY;
+  const void* gate = nullptr;  // [M / gate_rows, N] bf16, or null
+  int64_t gate_rows = 1;
+  float residual_scale = 1.0f;
+  void* dz = nullptr;          // [M, N] bf16 or E4M3, or null
+  void* dresidual = nullptr;   // [M, N] dtype, or null
+  float* dbias = nullptr;
+  float* dgate = nullptr;      // [M / gate_rows, N]
+  float* partials = nullptr;   // workspace
+  CastSpec cast;
+};
+te_status launch_dense_residual_grad(const DenseResidualGradArgs& a, cudaStream_t s);
+size_t dense_residual_grad_workspace(int64_t M, int64_t N, int64_t gates);
+
+// Sum of the squares of many tensors, and the tensors scaled by min(1, max_norm / (norm + eps)).
+using GradTensor = te_grad;  // `out` set
+// The squares, into `slots` doubles of workspace (the number used is returned in *used).
+te_status launch_grad_squares(const GradTensor* t, int64_t count, double* slots, int* used, cudaStream_t s);
+// norm = the square root of the slots' sum.
+te_status launch_grad_norm(const double* slots, int used, float* norm, cudaStream_t s);
+te_status launch_grad_clip(const GradTensor* t, int64_t count, const double* slots, int used, double max_norm,
+                           double eps, float* norm, cudaStream_t s);
+size_t grad_norm_workspace(int64_t count);
 
 // Device status word (TE_OK or the first failure a kernel recorded).
 int* device_status_ptr();

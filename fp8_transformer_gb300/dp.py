@@ -24,7 +24,7 @@ from __future__ import annotations
 import torch
 import torch.distributed as dist
 
-from .binding import Quantizer, QuantizerSet, te_layernorm_mlp_bwd, te_update_scales
+from .binding import GradList, Quantizer, QuantizerSet, te_clip_grad_norm, te_layernorm_mlp_bwd, te_update_scales
 
 NAMES = ("x", "kernel1", "act", "kernel2", "grad")
 
@@ -83,6 +83,13 @@ class GradBuckets:
         """Sum every gradient over the ranks (one collective per buffer)."""
         dist.all_reduce(self.weights, op=dist.ReduceOp.SUM, group=group)
         dist.all_reduce(self.vectors, op=dist.ReduceOp.SUM, group=group)
+
+    def clip(self, max_norm, norm, epsilon=1e-6, stream=None):
+        """Scale every gradient by min(1, max_norm / (norm + epsilon)) in place, on the device; norm (one
+        float32) receives their global norm.  After allreduce each rank computes the same factor from
+        the same sums."""
+        return te_clip_grad_norm(GradList([self.weights, self.vectors]), max_norm, norm, epsilon=epsilon,
+                                 stream=stream)
 
 
 def layernorm_mlp_bwd_dp(dy, x, gamma, kernel1, kernel2, saved_h, saved_ln_out, mu, rsigma, dx,

@@ -520,6 +520,122 @@ te_status te_layernorm_mlp_bwd_ckpt(const void* dy, const void* x, const void* g
                                     void* stream);
 
 /* ---------------------------------------------------------------------------------------
+ * Around the residual stream (no counterpart on the pages; an addition of this library): the norms
+ * before and after a block, the dense layer that ends in the stream, and the gradients' norm.
+ * Types: a block's tensors are in dtype, the stream in residual_dtype.  A gate is a factor for each
+ * channel of what joins the stream: [gates, H], where row m of the tensors takes the gate's row
+ * m / (M / gates), so that `gates` divides M (1: one gate for every row; one for each sequence of a
+ * batch; NULL: none, `gates` is not read).  What a call writes overlaps nothing else that it reads or
+ * writes, the workspace among it (TE_ERR_INVALID_ARG), but where a tensor may be updated in place.
+ * Rows at most 2^30.  The results do not vary between calls. */
+
+/* te_residual_norm_fwd -- the end of a block and the beginning of the next in one pass:
+ *     p = norm(y; post_gamma, post_beta), or y without post_gamma
+ *     x_out = residual_scale * residual + gate * p
+ *     out = norm(x_out; gamma, beta)
+ *   y [M, H], gamma, beta, post_gamma, post_beta [H], gate in dtype (TE_BF16, or TE_F32 with an fp32
+ *       stream); residual, x_out [M, H] in residual_dtype; x_out may be residual.
+ *   norm_type, zero_centered_gamma, epsilon  of both norms, as in te_norm_fwd (betas: NULL is zero,
+ *       ignored by rmsnorm).  Everything is computed in fp32 from the tensors' values; the second
+ *       norm takes the fp32 sum, before x_out is rounded.
+ *   out [M, H] in out_dtype (TE_F32, TE_BF16, or TE_E4M3 with q); q as in te_norm_fwd.
+ *   mu, rsigma, post_mu, post_rsigma  [M] fp32 statistics of the two norms, or NULL.
+ * H a multiple of 8, at most 8192. */
+te_status te_residual_norm_fwd(const void* y, te_dtype dtype, const void* residual,
+                               te_dtype residual_dtype, int64_t M, int64_t H, const void* gamma,
+                               const void* beta, const void* post_gamma, const void* post_beta,
+                               const void* gate, int64_t gates, float residual_scale,
+                               te_norm_type norm_type, int zero_centered_gamma, float epsilon,
+                               const te_quantizer* q, void* x_out, void* out, te_dtype out_dtype,
+                               float* mu, float* rsigma, float* post_mu, float* post_rsigma,
+                               void* stream);
+
+/* te_residual_norm_bwd -- its gradients.  With dx the gradient of x_out (dx_out plus what comes
+ * through the second norm) and phat the normalized y:
+ *     dresidual = residual_scale * dx,   dgate = sum over the gate's rows of dx * p
+ *     dy = the post norm's gradient from gate * dx, or gate * dx without it
+ *   dout [M, H] in dtype: gradient of out.  dx_out [M, H] in residual_dtype: what reaches x_out from
+ *       elsewhere, or NULL.  x_out and the statistics from the forward (the means not for rmsnorm).
+ *   y, post_mu, post_rsigma  as in the forward; y is not read without a post norm and a gate.
+ *   dresidual [M, H] in residual_dtype (may be dx_out) and dy [M, H] in dtype, either or both NULL.
+ *   dgamma [H]; dbeta, dpost_gamma, dpost_beta [H], dgate [gates, H] fp32, each or NULL (rmsnorm:
+ *       the betas' with zeros).  M = 0 zeroes all of these.
+ *   workspace  te_residual_norm_bwd_workspace(M, H, gates) bytes, 16-byte aligned. */
+size_t te_residual_norm_bwd_workspace(int64_t M, int64_t H, int64_t gates);
+te_status te_residual_norm_bwd(const void* dout, const void* dx_out, const void* x_out,
+                               const void* y, te_dtype dtype, te_dtype residual_dtype, int64_t M,
+                               int64_t H, const float* mu, const float* rsigma,
+                               const float* post_mu, const float* post_rsigma, const void* gamma,
+                               const void* post_gamma, const void* post_beta, const void* gate,
+                               int64_t gates, float residual_scale, te_norm_type norm_type,
+                               int zero_centered_gamma, void* dresidual, void* dy, float* dgamma,
+                               float* dbeta, float* dpost_gamma, float* dpost_beta, float* dgate,
+                               void* workspace, size_t ws_bytes, void* stream);
+
+/* te_dense_residual_fwd -- out = residual_scale * residual + gate * act(x @ kernel + bias) in one
+ * product.
+ *   x [M, K], kernel [K, N] in dtype: TE_BF16, or TE_E4M3 with the factors x_scale_inv and
+ *       kernel_scale_inv (device fp32 scalars, NULL = 1).
+ *   bias [N] and gate in bf16, each or NULL; act TE_IDENTITY, TE_RELU, TE_GELU or TE_SILU.
+ *   residual, out [M, N] in residual_dtype (TE_BF16 / TE_F32); out may be residual.
+ *   saved_z [M, N] bf16 or NULL: x @ kernel + bias, for te_dense_residual_bwd (the activation here
+ *       takes the fp32 value).
+ *   workspace  NULL, or te_dense_residual_fwd_workspace(M, K, N, dtype) bytes, 16-byte aligned: scratch
+ *       for splitting the product along K, as in te_gemm.
+ * K and N multiples of 16, at most 2^30. */
+size_t te_dense_residual_fwd_workspace(int64_t M, int64_t K, int64_t N, te_dtype dtype);
+te_status te_dense_residual_fwd(const void* x, const void* kernel, te_dtype dtype,
+                                const float* x_scale_inv, const float* kernel_scale_inv,
+                                const void* bias, te_act_type act, const void* gate, int64_t gates,
+                                const void* residual, te_dtype residual_dtype,
+                                float residual_scale, int64_t M, int64_t K, int64_t N, void* out,
+                                void* saved_z, void* workspace, size_t ws_bytes, void* stream);
+
+/* te_dense_residual_bwd -- its gradients: with dz = gate * dout * act'(z) in the operands' type,
+ *     dx = dz @ kernel^T,  dkernel = x^T @ dz,  dresidual = residual_scale * dout,
+ *     dbias = the column sums of the fp32 dz,  dgate = those of dout * act(z) over each gate's rows.
+ *   dout [M, N] in residual_dtype; x, kernel, act, gate as in the forward; saved_z from it, not read
+ *       with TE_IDENTITY and without dgate.
+ *   q   TE_E4M3: the quantizer of dz, scale_inv required.  TE_BF16: NULL.
+ *   dx [M, K], dkernel [K, N] bf16; dresidual [M, N] in residual_dtype, dbias [N] and dgate [gates, N]
+ *       fp32, each or NULL (with a residual_scale of 1 dresidual is dout).
+ *   workspace  te_dense_residual_bwd_workspace(M, K, N, gates, dtype) bytes (gates 1 without a gate),
+ *       16-byte aligned; as elsewhere its end may be missing, where products would be split along K.
+ * M = 0 zeroes dkernel, dbias and dgate. */
+size_t te_dense_residual_bwd_workspace(int64_t M, int64_t K, int64_t N, int64_t gates, te_dtype dtype);
+te_status te_dense_residual_bwd(const void* dout, te_dtype residual_dtype, const void* x,
+                                const void* kernel, te_dtype dtype, const void* saved_z,
+                                te_act_type act, const void* gate, int64_t gates,
+                                float residual_scale, const te_quantizer* q,
+                                const float* x_scale_inv, const float* kernel_scale_inv, int64_t M,
+                                int64_t K, int64_t N, void* dx, void* dkernel, void* dresidual,
+                                float* dbias, float* dgate, void* workspace, size_t ws_bytes,
+                                void* stream);
+
+/* One gradient of te_grad_norm and te_clip_grad_norm: numel values of dtype (TE_F32 / TE_BF16), aligned
+ * like one of them; out: where the clipped values go (NULL: in place). */
+typedef struct {
+  const void* data;
+  void* out;
+  int64_t numel;
+  int32_t dtype; /* te_dtype */
+} te_grad;
+
+/* te_grad_norm -- *norm (device fp32) = the square root of the sum of the squares of all values of the
+ * n tensors `grads` (a host array, read before the call returns; empty tensors may have NULL data).
+ *   Sums as exact as fp64's, in a fixed order: right wherever the norm is a finite fp32.
+ *   workspace  te_grad_norm_workspace(n) bytes, 16-byte aligned.
+ * te_clip_grad_norm -- the same, and every value times min(1, max_norm / (norm + epsilon)) (1 where
+ * norm + epsilon is 0), in fp32, rounded to its type.  A NaN among the values makes norm and all of
+ * them NaN; an infinite norm makes the finite values zero.  max_norm, epsilon >= 0 and finite.
+ *   No output overlaps a tensor but its own (so no tensor is clipped twice), nor norm. */
+size_t te_grad_norm_workspace(int64_t n);
+te_status te_grad_norm(const te_grad* grads, int64_t n, float* norm, void* workspace,
+                       size_t ws_bytes, void* stream);
+te_status te_clip_grad_norm(const te_grad* grads, int64_t n, double max_norm, double epsilon,
+                            float* norm, void* workspace, size_t ws_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------------------
  * te_norm_bwd -- gradients of te_norm_fwd (LayerNorm MLP page, Description: the backward pass
  * yields the gradient of every parameter; LayerNorm Dense page, Description: gradients of x,
  * gamma and beta).
