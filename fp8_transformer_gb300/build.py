@@ -21,7 +21,7 @@ LIB_NAME = "libte_gb300.so"
 LIB_PATH = os.path.join(HERE, LIB_NAME)
 SOURCES = ["api.cu", "norm.cu", "elementwise.cu", "gemm.cu", "tmap.cu", "profile.cu", "noalloc.cu",
            "selftest.cu", "host_pipeline.cu", "block_quant.cu", "block_gemm.cu", "block_api.cu",
-           "dact_ckpt.cu", "residual_norm.cu", "dense_residual_grad.cu", "grad_norm.cu",
+           "dact_ckpt.cu", "residual_norm_fwd.cu", "residual_norm_bwd.cu", "dense_residual_grad.cu", "dense_few.cu", "grad_norm.cu",
            "residual_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

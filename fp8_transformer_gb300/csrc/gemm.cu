@@ -402,6 +402,19 @@ __device__ __forceinline__ f32x2 round_bf16_2(f32x2 v) {
 
 // ------------------------------------------------------------------ the kernel ------------
 
+// A bf16 bias of columns col0 .. col0 + 31, by ordinary loads (the kernel in front may have written it).
+__device__ __forceinline__ void load_bias_bf16(const void* bias, int64_t col0, int count, f32x2 (&b)[16]) {
+  const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(bias) + col0);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint4 w = bias && 8 * i < count ? p[i] : make_uint4(0u, 0u, 0u, 0u);
+    b[4 * i] = bf16x2_f2(w.x);
+    b[4 * i + 1] = bf16x2_f2(w.y);
+    b[4 * i + 2] = bf16x2_f2(w.z);
+    b[4 * i + 3] = bf16x2_f2(w.w);
+  }
+}
+
 // 32 values (`count` of them there) of one row of an fp32 or bf16 tensor, as raw words.
 __device__ __forceinline__ void load_seg(const void* base, int64_t off, int count, int dtype, uint4 (&w)[8]) {
   const int n = dtype == TE_BF16 ? count / 8 : count / 4;
@@ -419,7 +432,7 @@ __device__ __forceinline__ void residual_chunk(const GemmDev& g, int64_t row, in
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       if (8 * i < count) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4*>(gt) + i);
+        const uint4 w = reinterpret_cast<const uint4*>(gt)[i];  // (may be the kernel in front's)
         const f32x2 q[4] = {bf16x2_f2(w.x), bf16x2_f2(w.y), bf16x2_f2(w.z), bf16x2_f2(w.w)};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -736,9 +749,12 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
           uint32_t r[32];
           tmem_ld32(taddr + c * 32, r);
           f32x2 bz[16];  // the chunk's bias, loaded while the accumulator columns arrive
-          load_bias_chunk(g.bias, g.bias_dtype, col0, count, bz);
+          if constexpr (!RES) load_bias_chunk(g.bias, g.bias_dtype, col0, count, bz);
           uint4 res[8];  // and its residual
-          if constexpr (RES) load_seg(g.residual, row * g.N + col0, row_ok ? count : 0, g.d_dtype, res);
+          if constexpr (RES) {
+            load_bias_bf16(g.bias, col0, count, bz);
+            load_seg(g.residual, row * g.N + col0, row_ok ? count : 0, g.d_dtype, res);
+          }
           tmem_ld_wait();
           float v[32];
 #pragma unroll
