@@ -1,15 +1,18 @@
 // The global norm of many gradients and their clipping: n = sqrt(sum of g^2), out = g min(1, max / (n + eps)).
 //
 // The tensors go in a kernel's parameters, up to 512 of them a launch, so that a call needs no table
-// in device memory and can be captured.  They are cut into chunks of 1024 vectors of 16 bytes; a CTA
+// in device memory and can be captured.  They are cut into chunks of 2048 vectors of 16 bytes; a CTA
 // takes every grid-th chunk.  The squares pass is bound by reading; the scaling pass reads again (the
-// last chunks first, which the squares pass left in L2) and writes.
+// last chunks first, which the squares pass left in L2) and writes.  353 MB: 68 + 102 us a call, with the
+// results' way out of L2 in the next call's squares.  (Eight vectors to a thread, or the next chunk's
+// asked for ahead, are no faster; two are 95 us for the 68.)
 //
 // Sums: a thread adds the squares of its 32 (bf16) or 16 (fp32) values of a chunk in fp32, and the
-// chunks' sums as an unevaluated pair of fp32, which loses nothing a double would keep; fp64
-// instructions are two orders slower here and would bound the pass.  Where a chunk's fp32 sum leaves
-// [2^-80, 2^100] (a square overflowed, or small ones vanished), the thread takes that chunk's squares
-// again in fp64, so that the norm is right wherever it is a finite fp32.
+// chunks' sums, the warps' and the CTAs' as unevaluated pairs of fp32, which lose nothing that fp64 would
+// keep of them (fp64 instructions are two orders slower here and would bound the small cases).  Where a
+// chunk's fp32 sum leaves [2^-80, 2^80] (a square overflowed, or small ones vanished), the thread takes
+// that chunk's squares again in fp64, and so does every sum that they enter, so that the norm is right
+// wherever it is a finite fp32.
 #include "cast.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -19,9 +22,9 @@ namespace te {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kVecs = 1024;              // vectors of 16 bytes in a chunk
-constexpr int kPer = kVecs / kThreads;   // of a thread
-constexpr int kCtasPerSm = 4;
+constexpr int kVecs = 2048;              // vectors of 16 bytes in a chunk
+constexpr int kPer = kVecs / kThreads;   // of a thread, all in flight at once
+constexpr int kCtasPerSm = 3;
 constexpr int kSmall = 32, kLarge = 512;  // tensors of one launch
 
 template <int CAP>
@@ -70,6 +73,21 @@ __device__ __forceinline__ void store_element(void* p, int64_t i, bool bf16, flo
   else static_cast<float*>(p)[i] = v;
 }
 
+// hi + lo, the sum of some squares; lo the rounding errors of hi.
+struct Pair {
+  float hi, lo;
+};
+__device__ __forceinline__ Pair add_pair(Pair a, Pair b) {
+  const float s = a.hi + b.hi, t = s - a.hi;
+  return Pair{s, (a.hi - (s - t)) + (b.hi - t) + (a.lo + b.lo)};
+}
+__device__ __forceinline__ Pair warp_pair(Pair v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    v = add_pair(v, Pair{__shfl_xor_sync(0xffffffffu, v.hi, o), __shfl_xor_sync(0xffffffffu, v.lo, o)});
+  return v;
+}
+
 __device__ __forceinline__ double square64(const uint4& w, bool bf16) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   double s = 0.0;
@@ -85,10 +103,20 @@ __device__ __forceinline__ double square64(const uint4& w, bool bf16) {
   return s;
 }
 
-__device__ __noinline__ double chunk64(const uint4 (&w)[kPer], bool bf16) {
-  double s = 0.0;
-  for (int k = 0; k < kPer; ++k) s += square64(w[k], bf16);
+// A thread's squares of a chunk (its vectors n, n + kThreads, ... read again) and of one end.
+__device__ __noinline__ double chunk64(const uint4* v, int64_t n, int64_t vecs, float end, bool bf16) {
+  double s = double(end) * double(end);
+  for (int k = 0; k < kPer; ++k)
+    if (n + k * kThreads < vecs) s += square64(v[n + k * kThreads], bf16);
   return s;
+}
+
+// Whether a value is not a zero (of either sign).
+__device__ __forceinline__ bool nonzero(const uint4 (&w)[kPer], float end, bool bf16) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) any |= w[k].x | w[k].y | w[k].z | w[k].w;
+  return (any & (bf16 ? 0x7fff7fffu : 0x7fffffffu)) != 0 || end != 0.0f;
 }
 
 __device__ __forceinline__ double warp_sum64(double v) {
@@ -98,93 +126,105 @@ __device__ __forceinline__ double warp_sum64(double v) {
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, 2048 / kThreads) grad_squares_kernel(const __grid_constant__ Table<CAP> t,
-                                                                                uint32_t chunks, double* slots) {
-  __shared__ double red[kThreads / 32];
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_squares_kernel(const __grid_constant__ Table<CAP> t,
+                                                                                uint32_t chunks, GradSlot* slots) {
+  __shared__ GradSlot red[kThreads / 32];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int tid = threadIdx.x;
-  float hi = 0.0f, lo = 0.0f;  // their exact sum is the squares so far
-  double rest = 0.0;           // squares taken in fp64
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const int i = tensor_of(t, c);
-    const bool bf16 = t.bf16[i];
-    const void* p = t.src[i];
-    const Cut cut = cut_of(p, t.n[i], bf16 ? 2 : 4);
-    const uint32_t at = c - t.first[i];
-    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + int64_t(cut.head) * (bf16 ? 2 : 4));
+  Pair sum{0.0f, 0.0f};
+  double rest = 0.0;  // squares taken in fp64
+  // a thread's part of a chunk: its vectors, and one of the tensor's ends that no vector covers
+  struct Part {
+    const uint4* v;
+    int64_t n, vecs;
+    float end;
+    bool bf16;
     uint4 w[kPer];
+  };
+  auto load = [&](uint32_t c, Part& q) {
+    const int i = tensor_of(t, c);
+    q.bf16 = t.bf16[i];
+    const void* p = t.src[i];
+    const Cut cut = cut_of(p, t.n[i], q.bf16 ? 2 : 4);
+    const uint32_t at = c - t.first[i];
+    q.v = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + int64_t(cut.head) * (q.bf16 ? 2 : 4));
+    q.n = int64_t(at) * kVecs + tid;
+    q.vecs = cut.vecs;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      const int64_t n = int64_t(at) * kVecs + tid + k * kThreads;
-      w[k] = n < cut.vecs ? v[n] : make_uint4(0u, 0u, 0u, 0u);
+    for (int k = 0; k < kPer; ++k)
+      q.w[k] = q.n + k * kThreads < q.vecs ? q.v[q.n + k * kThreads] : make_uint4(0u, 0u, 0u, 0u);
+    q.end = 0.0f;
+    if (at == 0) {
+      if (tid < cut.head) q.end = element(p, tid, q.bf16);
+      else if (tid >= 32 && tid < 32 + cut.tail) q.end = element(p, t.n[i] - cut.tail + (tid - 32), q.bf16);
     }
-    f32x2 s0 = f2s(0.0f), s1 = f2s(0.0f);
-    uint32_t any = 0;
+  };
+  auto add = [&](const Part& q) {
+    f32x2 s0 = f2(q.end * q.end, 0.0f), s1 = f2s(0.0f);
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
-      any |= (w[k].x | w[k].y | w[k].z | w[k].w) & 0x7fff7fffu;
-      if (bf16) {
-        f32x2 q[4];
-        Pairs<__nv_bfloat16>::cvt(w[k], q);
-        s0 = fma2(q[0], q[0], s0);
-        s1 = fma2(q[1], q[1], s1);
-        s0 = fma2(q[2], q[2], s0);
-        s1 = fma2(q[3], q[3], s1);
+      if (q.bf16) {
+        f32x2 u[4];
+        Pairs<__nv_bfloat16>::cvt(q.w[k], u);
+        s0 = fma2(u[0], u[0], s0);
+        s1 = fma2(u[1], u[1], s1);
+        s0 = fma2(u[2], u[2], s0);
+        s1 = fma2(u[3], u[3], s1);
       } else {
-        any |= (w[k].x | w[k].y | w[k].z | w[k].w) & 0x7fffffffu;
-        f32x2 q[2];
-        Pairs<float>::cvt(w[k], q);
-        s0 = fma2(q[0], q[0], s0);
-        s1 = fma2(q[1], q[1], s1);
+        f32x2 u[2];
+        Pairs<float>::cvt(q.w[k], u);
+        s0 = fma2(u[0], u[0], s0);
+        s1 = fma2(u[1], u[1], s1);
       }
     }
     s0 = add2(s0, s1);
     const float s = f2lo(s0) + f2hi(s0);
-    if (s >= 0x1p-80f && s <= 0x1p100f) {
-      const float sum = hi + s, b = sum - hi;  // the sum's rounding error, exactly
-      lo += (hi - (sum - b)) + (s - b);
-      hi = sum;
-    } else if (any) {
-      rest += chunk64(w, bf16);
-    }
-    if (at == 0) {  // the ends that no vector covers
-      const int64_t n = t.n[i];
-      if (tid < cut.head) {
-        const double x = element(p, tid, bf16);
-        rest += x * x;
-      } else if (tid >= 32 && tid < 32 + cut.tail) {
-        const double x = element(p, n - cut.tail + (tid - 32), bf16);
-        rest += x * x;
-      }
-    }
+    if (s >= 0x1p-80f && s <= 0x1p80f) sum = add_pair(sum, Pair{s, 0.0f});
+    else if (nonzero(q.w, q.end, q.bf16)) rest += chunk64(q.v, q.n, q.vecs, q.end, q.bf16);
+  };
+  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
+    Part q;
+    load(c, q);
+    add(q);
   }
-  const double total = warp_sum64(double(hi) + (double(lo) + rest));
-  if ((tid & 31) == 0) red[tid >> 5] = total;
+  sum = warp_pair(sum);
+  if (__any_sync(0xffffffffu, rest != 0.0)) rest = warp_sum64(rest);
+  if ((tid & 31) == 0) red[tid >> 5] = GradSlot{sum.hi, sum.lo, rest};
   __syncthreads();
   if (tid == 0) {
-    double sum = 0.0;
-    for (int w = 0; w < kThreads / 32; ++w) sum += red[w];
-    slots[blockIdx.x] = sum;
+    for (int w = 1; w < kThreads / 32; ++w) {
+      sum = add_pair(sum, Pair{red[w].hi, red[w].lo});
+      if (red[w].rest != 0.0) rest += red[w].rest;
+    }
+    slots[blockIdx.x] = GradSlot{sum.hi, sum.lo, rest};
   }
 }
 
-// The norm from the slots, by one warp, in a fixed order: the same bits in every CTA.
-__device__ __forceinline__ double norm_of(const double* slots, int used, int lane) {
-  double s = 0.0;
+// The norm from the slots, by one warp, in a fixed order: the same bits in every CTA, to every lane.
+__device__ __forceinline__ double norm_of(const GradSlot* slots, int used, int lane) {
+  Pair sum{0.0f, 0.0f};
+  double rest = 0.0;
 #pragma unroll 4
-  for (int i = lane; i < used; i += 32) s += __ldcg(slots + i);
-  return sqrt(warp_sum64(s));
+  for (int i = lane; i < used; i += 32) {
+    const uint4 u = __ldcg(reinterpret_cast<const uint4*>(slots + i));
+    sum = add_pair(sum, Pair{__uint_as_float(u.x), __uint_as_float(u.y)});
+    if (u.z | u.w) rest += __hiloint2double(int(u.w), int(u.z));
+  }
+  sum = warp_pair(sum);
+  double total = double(sum.hi) + double(sum.lo);
+  if (__any_sync(0xffffffffu, rest != 0.0)) total += warp_sum64(rest);
+  return sqrt(total);
 }
 
-__global__ void grad_norm_kernel(const double* slots, int used, float* norm) {
+__global__ void grad_norm_kernel(const GradSlot* slots, int used, float* norm) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const double n = norm_of(slots, used, threadIdx.x);
   if (threadIdx.x == 0) *norm = float(n);
 }
 
 template <int CAP>
-__global__ void __launch_bounds__(kThreads, 2048 / kThreads) grad_clip_kernel(const __grid_constant__ Table<CAP> t,
-                                                                             uint32_t chunks, const double* slots,
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_clip_kernel(const __grid_constant__ Table<CAP> t,
+                                                                             uint32_t chunks, const GradSlot* slots,
                                                                              int used, double max_norm, double eps,
                                                                              float* norm) {
   __shared__ float factor;
@@ -300,7 +340,7 @@ te_status batches(const GradTensor* g, int64_t count, Launch&& launch) {
 }
 
 template <int CAP>
-te_status squares(const GradTensor* g, int64_t count, double* slots, int* used, cudaStream_t s) {
+te_status squares(const GradTensor* g, int64_t count, GradSlot* slots, int* used, cudaStream_t s) {
   return batches<CAP>(g, count, [&](const Table<CAP>& t, uint32_t chunks, int grid) {
     grad_squares_kernel<CAP><<<grid, kThreads, 0, s>>>(t, chunks, slots + *used);
     *used += grid;
@@ -309,7 +349,7 @@ te_status squares(const GradTensor* g, int64_t count, double* slots, int* used, 
 }
 
 template <int CAP>
-te_status clip(const GradTensor* g, int64_t count, const double* slots, int used, double max_norm, double eps,
+te_status clip(const GradTensor* g, int64_t count, const GradSlot* slots, int used, double max_norm, double eps,
                float* norm, cudaStream_t s) {
   return batches<CAP>(g, count, [&](const Table<CAP>& t, uint32_t chunks, int grid) {
     const te_status st = launch_dependent(grad_clip_kernel<CAP>, dim3(unsigned(grid)), dim3(kThreads), s, t, chunks,
@@ -323,20 +363,20 @@ te_status clip(const GradTensor* g, int64_t count, const double* slots, int used
 
 size_t grad_norm_workspace(int64_t count) {
   if (count <= 0) return 0;
-  return size_t(ceil_div(count, int64_t(kLarge)) + 1) * size_t(max_grid()) * sizeof(double);
+  return size_t(ceil_div(count, int64_t(kLarge)) + 1) * size_t(max_grid()) * sizeof(GradSlot);
 }
 
-te_status launch_grad_squares(const GradTensor* t, int64_t count, double* slots, int* used, cudaStream_t s) {
+te_status launch_grad_squares(const GradTensor* t, int64_t count, GradSlot* slots, int* used, cudaStream_t s) {
   ProfileScope prof(TE_KERNEL_QUANTIZE, s);
   *used = 0;
   return count <= kSmall ? squares<kSmall>(t, count, slots, used, s) : squares<kLarge>(t, count, slots, used, s);
 }
 
-te_status launch_grad_norm(const double* slots, int used, float* norm, cudaStream_t s) {
+te_status launch_grad_norm(const GradSlot* slots, int used, float* norm, cudaStream_t s) {
   return launch_dependent(grad_norm_kernel, dim3(1), dim3(32), s, slots, used, norm);
 }
 
-te_status launch_grad_clip(const GradTensor* t, int64_t count, const double* slots, int used, double max_norm,
+te_status launch_grad_clip(const GradTensor* t, int64_t count, const GradSlot* slots, int used, double max_norm,
                            double eps, float* norm, cudaStream_t s) {
   return count <= kSmall ? clip<kSmall>(t, count, slots, used, max_norm, eps, norm, s)
                          : clip<kLarge>(t, count, slots, used, max_norm, eps, norm, s);

@@ -90,7 +90,11 @@ struct ResidualNormArgs {
   float* post_mu = nullptr;
   float* post_rsigma = nullptr;
   CastSpec cast;
+  // the kernel in front on the stream only zeroes cast.amax_out: start beside it, wait before the amax
+  int beside_zero = 0;
 };
+// *p = 0, by a kernel beside which a dependent may start.
+te_status launch_zero_scalar(float* p, cudaStream_t s);
 te_status launch_residual_norm_fwd(const ResidualNormArgs& a, cudaStream_t s);
 
 struct ResidualNormBwdArgs {
@@ -334,11 +338,15 @@ size_t dense_residual_grad_workspace(int64_t M, int64_t N, int64_t gates);
 
 // Sum of the squares of many tensors, and the tensors scaled by min(1, max_norm / (norm + eps)).
 using GradTensor = te_grad;  // `out` set
-// The squares, into `slots` doubles of workspace (the number used is returned in *used).
-te_status launch_grad_squares(const GradTensor* t, int64_t count, double* slots, int* used, cudaStream_t s);
+struct alignas(16) GradSlot {  // a part of the sum: hi + lo + rest
+  float hi, lo;
+  double rest;
+};
+// The squares, into slots in the workspace (*used: how many).
+te_status launch_grad_squares(const GradTensor* t, int64_t count, GradSlot* slots, int* used, cudaStream_t s);
 // norm = the square root of the slots' sum.
-te_status launch_grad_norm(const double* slots, int used, float* norm, cudaStream_t s);
-te_status launch_grad_clip(const GradTensor* t, int64_t count, const double* slots, int used, double max_norm,
+te_status launch_grad_norm(const GradSlot* slots, int used, float* norm, cudaStream_t s);
+te_status launch_grad_clip(const GradTensor* t, int64_t count, const GradSlot* slots, int used, double max_norm,
                            double eps, float* norm, cudaStream_t s);
 size_t grad_norm_workspace(int64_t count);
 

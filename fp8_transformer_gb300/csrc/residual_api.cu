@@ -138,7 +138,7 @@ te_status grads(const te_grad* g, int64_t n, bool clip, double max_norm, double 
     te_status st = check_grads(g, n, clip, norm, ws, ws_bytes, &t);
     if (st != TE_OK) return st;
     if (t.empty()) return zero(norm, sizeof(float), s);
-    double* slots = static_cast<double*>(ws);
+    GradSlot* slots = static_cast<GradSlot*>(ws);
     int used = 0;
     st = launch_grad_squares(t.data(), int64_t(t.size()), slots, &used, s);
     if (st != TE_OK) return st;
@@ -211,11 +211,19 @@ te_status te_residual_norm_fwd(const void* y, te_dtype dtype, const void* residu
   a.post_mu = post_mu;
   a.post_rsigma = post_rsigma;
   const cudaStream_t s = as_stream(stream);
-  if (out_dtype != TE_E4M3) {  // the amax alone, where it is asked for
+  if (out_dtype != TE_E4M3 || q->mode == TE_SCALING_DELAYED) {
     a.cast.out_dtype = out_dtype;
+    if (out_dtype == TE_E4M3) {
+      a.cast.scale = q->scale;
+      a.cast.scale_inv_out = q->scale_inv;
+    }
     a.cast.amax_out = q ? q->amax : nullptr;
-    const te_status st = zero_scalar(a.cast.amax_out, s);
-    return st != TE_OK ? st : launch_residual_norm_fwd(a, s);
+    if (a.cast.amax_out) {
+      const te_status st = launch_zero_scalar(a.cast.amax_out, s);
+      if (st != TE_OK) return st;
+      a.beside_zero = 1;
+    }
+    return launch_residual_norm_fwd(a, s);
   }
   return run_cast(q, out_dtype, 0, s, [&](const CastSpec& c) {
     a.cast = c;

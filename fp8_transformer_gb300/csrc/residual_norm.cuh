@@ -87,7 +87,7 @@ __device__ __forceinline__ f32x2 sum8(const f32x2 (&v)[4]) { return add2(add2(v[
 // each input.  The CTA's row k lies in slot k % slots; one thread refills the slot of row k - 1 after
 // the first barrier of row k, which every thread passes with row k - 1 behind it.
 
-constexpr int kMaxSlots = 6;
+constexpr int kMaxSlots = 3;
 constexpr size_t kSmem = 227 * 1024;  // of one SM, shared by its CTAs
 constexpr size_t kHeader = 128;
 
@@ -143,15 +143,17 @@ __device__ __forceinline__ bool meet(bool bad) {
   return __syncthreads_or(bad) != 0;
 }
 
-// Slots of `bytes` that fit each of the CTAs of an SM, 16 warps (or fewer, where two would not) to an SM.
+// CTAs of an SM (fewer than `ctas` where two slots of `bytes` would not fit each) and the slots of each, at
+// most `most`: beyond what keeps the copies ahead, shared memory is better left to L1, which holds the
+// parameter vectors.  (The carveout is left to the driver: all of it for shared memory cost the backward 8%.)
 struct RingShape {
   int ctas, slots;
 };
-inline RingShape ring_shape(int ctas, size_t bytes) {
+inline RingShape ring_shape(int ctas, size_t bytes, int most) {
   for (; ctas >= 1; ctas = ctas > 1 ? ctas / 2 : 0) {
     const size_t room = kSmem / ctas - 1024 - kHeader - 1024;  // 1 KB to the CTA itself, 1 KB static
     const size_t fit = room / bytes;
-    if (fit >= 2) return RingShape{ctas, int(fit < size_t(kMaxSlots) ? fit : size_t(kMaxSlots))};
+    if (fit >= 2) return RingShape{ctas, int(fit < size_t(most) ? fit : size_t(most))};
   }
   return RingShape{0, 0};
 }
@@ -160,9 +162,7 @@ template <class K>
 bool allow_smem(K kernel, PerDevice<bool>& done) {
   bool ok = false;
   return done.get(&ok, [&](bool* v) {
-    *v = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem - 2048)) == cudaSuccess &&
-         cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared) ==
-             cudaSuccess;
+    *v = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem - 2048)) == cudaSuccess;
     return *v;
   });
 }

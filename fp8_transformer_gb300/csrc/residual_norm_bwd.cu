@@ -35,7 +35,8 @@ __device__ __forceinline__ float2 row_sums(float a, float b, float2* red, bool* 
   return t;
 }
 
-__host__ __device__ constexpr int bwd_warps(int nv) { return nv >= 4 ? 8 : 16; }  // of an SM, by their registers
+// Warps of an SM, by their registers (four: LayerNorm on both sides, with four sums to a column).
+__host__ __device__ constexpr int bwd_warps(int nv, bool four) { return nv >= 4 ? 8 : four && nv == 2 ? 12 : 16; }
 
 // A CTA of G warps takes neighbouring rows.  With S1 = the sum of dx * phat and S2 = that of dx over the
 // rows that share a gate (phat the normalized y, or y itself without a post norm), the gradients of the
@@ -48,10 +49,13 @@ __host__ __device__ constexpr int bwd_warps(int nv) { return nv >= 4 ? 8 : 16; }
 //
 // A ring slot is [dout | x_out | dx_out | y]; where two slots would not fit, y is read from memory.
 template <typename TY, typename TR, bool LN, bool POST, bool SUMS, int NV, int G>
-__global__ void __launch_bounds__(G * 32, bwd_warps(NV) / G)
+__global__ void __launch_bounds__(G * 32, bwd_warps(NV, LN && POST) / G)
     residual_norm_bwd_kernel(ResidualNormBwdArgs a, int* status, int slots, bool y_in_ring) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr int threads = G * 32;
+  // (four sums, measured, us, with / without: 16384 x 8192 754 / 606, x 4096 250 / 282, x 1024 90 / 71)
+  constexpr bool KEEP = !(LN && POST) || (NV == 4 && G < 8);
+  constexpr bool EARLY = KEEP && sizeof(TY) == 2;  // (fp32 vectors in waiting would spill)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[4][G];
   const int tid = threadIdx.x;
@@ -116,35 +120,59 @@ __global__ void __launch_bounds__(G * 32, bwd_warps(NV) / G)
     Param<TY> pa[NV], pb[NV];  // gamma, then the gate; the post norm's gain
 #pragma unroll
     for (int i = 0; i < NV; ++i)
-      if (in[i]) pa[i].ask(a.gamma, (tid + i * threads) * 8);
+      if (EARLY && in[i]) pa[i].ask(a.gamma, (tid + i * threads) * 8);
     bad = !ring.wait(status);
     const uint8_t* here = ring.here();
-    f32x2 xh[NV][4], dx[NV][4];  // xhat; dout * g, then dx
+    // xhat and dout * g, then phat and the gradient on its way, of each unit from one barrier to the next;
+    // KEEP false, where they would spill beside four sums, takes what the slot still holds again instead
+    f32x2 xh[KEEP ? NV : 1][4], dx[NV][4];
     f32x2 t1 = f2s(0.0f), t2 = f2s(0.0f);
-    const f32x2 mu2 = f2s(mu), rs2 = f2s(rs);
+    const f32x2 mu2 = f2s(mu), rs2 = f2s(rs), pmu2 = f2s(pmu), prs2 = f2s(prs);
+    // dout, xhat and dout * g of unit i
+    auto upstream = [&](int i, f32x2 (&d)[4], f32x2 (&h)[4], f32x2 (&dg)[4]) {
+      const int u = (tid + i * threads) * 8;
+      Unit<TY> dout;
+      Unit<TR> x;
+      dout.load(here, u);
+      x.load(here + at_x, u);
+      f32x2 g[4], xp[4];
+      if (!EARLY) pa[i].ask(a.gamma, u);
+      pa[i].get(g, 1.0f);
+      dout.cvt(d);
+      x.cvt(xp);
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        h[p] = LN ? mul2(sub2(xp[p], mu2), rs2) : mul2(xp[p], rs2);
+        dg[p] = mul2(d[p], add2(g[p], shift2));
+      }
+    };
+    auto phat = [&](int i, f32x2 (&h)[4]) {
+      Unit<TY> y;
+      if (y_in_ring) y.load(here + at_y, (tid + i * threads) * 8);
+      else y.load(a.y, base + i * threads * 8);
+      y.cvt(h);
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+        if (POST) h[p] = LN ? mul2(sub2(h[p], pmu2), prs2) : mul2(h[p], prs2);
+    };
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int u = (tid + i * threads) * 8;
       if (in[i]) {
-        Unit<TY> dout;
-        Unit<TR> x;
-        dout.load(here, u);
-        x.load(here + at_x, u);
-        f32x2 g[4], d[4], xp[4];
-        pa[i].get(g, 1.0f);
-        dout.cvt(d);
-        x.cvt(xp);
+        f32x2 d[4], dg[4], h[4];
+        upstream(i, d, h, dg);
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
-          xh[i][p] = LN ? mul2(sub2(xp[p], mu2), rs2) : mul2(xp[p], rs2);
-          dx[i][p] = mul2(d[p], add2(g[p], shift2));
-          if (LN) t1 = add2(t1, dx[i][p]);
-          t2 = fma2(dx[i][p], xh[i][p], t2);
-          ag[i][p] = fma2(d[p], xh[i][p], ag[i][p]);
+          if (LN) t1 = add2(t1, dg[p]);
+          t2 = fma2(dg[p], h[p], t2);
+          ag[i][p] = fma2(d[p], h[p], ag[i][p]);
           if (LN) ab[i][p] = add2(ab[i][p], d[p]);
+          if (KEEP) {
+            xh[KEEP ? i : 0][p] = h[p];
+            dx[i][p] = dg[p];
+          }
         }
-        if (SUMS) pa[i].ask(a.gate, gate_row * a.H + u);
-        if (POST) pb[i].ask(a.post_gamma, u);
+        if (SUMS && KEEP && EARLY) pa[i].ask(a.gate, gate_row * a.H + (tid + i * threads) * 8);
+        if (POST && KEEP && EARLY) pb[i].ask(a.post_gamma, (tid + i * threads) * 8);
       }
     }
     const float2 m = row_sums<G>(f2lo(t1) + f2hi(t1), f2lo(t2) + f2hi(t2), red[par], &bad);
@@ -154,16 +182,23 @@ __global__ void __launch_bounds__(G * 32, bwd_warps(NV) / G)
       issue(issued++, ring.before());
     }
     const f32x2 c1 = f2s(-rs * (m.x * inv_h)), c2 = f2s(-rs * (m.y * inv_h)), scale2 = f2s(a.residual_scale);
-    const f32x2 pmu2 = f2s(pmu), prs2 = f2s(prs);
     t1 = t2 = f2s(0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int u = (tid + i * threads) * 8;
       if (in[i]) {
         const int64_t at = base + i * threads * 8;
+        f32x2 h[4];
+        if (KEEP) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) h[p] = xh[KEEP ? i : 0][p];
+        } else {
+          f32x2 d[4];
+          upstream(i, d, h, dx[i]);
+        }
 #pragma unroll
         for (int p = 0; p < 4; ++p)
-          dx[i][p] = fma2(xh[i][p], c2, LN ? fma2(dx[i][p], rs2, c1) : mul2(dx[i][p], rs2));
+          dx[i][p] = fma2(h[p], c2, LN ? fma2(dx[i][p], rs2, c1) : mul2(dx[i][p], rs2));
         if (a.dx_out) {
           Unit<TR> dxo;
           f32x2 d[4];
@@ -179,18 +214,16 @@ __global__ void __launch_bounds__(G * 32, bwd_warps(NV) / G)
           store8<TR>(a.dresidual, at, o);
         }
         if (SUMS) {
-          Unit<TY> y;
-          if (y_in_ring) y.load(here + at_y, u);
-          else y.load(a.y, at);
-          y.cvt(xh[i]);  // phat from here on
+          phat(i, h);
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
-            if (POST) xh[i][p] = LN ? mul2(sub2(xh[i][p], pmu2), prs2) : mul2(xh[i][p], prs2);
-            s1[i][p] = fma2(dx[i][p], xh[i][p], s1[i][p]);
+            s1[i][p] = fma2(dx[i][p], h[p], s1[i][p]);
             if (POST && LN) s2[i][p] = add2(s2[i][p], dx[i][p]);
+            if (KEEP) xh[KEEP ? i : 0][p] = h[p];
           }
           if (a.gate) {
             f32x2 gt[4];
+            if (!KEEP || !EARLY) pa[i].ask(a.gate, gate_row * a.H + u);
             pa[i].get(gt, 1.0f);
 #pragma unroll
             for (int p = 0; p < 4; ++p) dx[i][p] = mul2(dx[i][p], gt[p]);
@@ -198,12 +231,13 @@ __global__ void __launch_bounds__(G * 32, bwd_warps(NV) / G)
         }
         if (POST) {
           f32x2 g[4];
+          if (!KEEP || !EARLY) pb[i].ask(a.post_gamma, u);
           pb[i].get(g, 1.0f);
 #pragma unroll
           for (int p = 0; p < 4; ++p) {
             dx[i][p] = mul2(dx[i][p], add2(g[p], shift2));
             if (LN) t1 = add2(t1, dx[i][p]);
-            t2 = fma2(dx[i][p], xh[i][p], t2);
+            t2 = fma2(dx[i][p], h[p], t2);
           }
         } else if (a.dy) {
           store8<TY>(a.dy, at, dx[i]);
@@ -217,10 +251,13 @@ __global__ void __launch_bounds__(G * 32, bwd_warps(NV) / G)
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           if (in[i]) {
-            f32x2 o[4];
+            f32x2 o[4], h[4];
+            if (!KEEP) phat(i, h);
 #pragma unroll
-            for (int p = 0; p < 4; ++p)
-              o[p] = fma2(xh[i][p], d2, LN ? fma2(dx[i][p], prs2, d1) : mul2(dx[i][p], prs2));
+            for (int p = 0; p < 4; ++p) {
+              const f32x2 ph = KEEP ? xh[KEEP ? i : 0][p] : h[p];
+              o[p] = fma2(ph, d2, LN ? fma2(dx[i][p], prs2, d1) : mul2(dx[i][p], prs2));
+            }
             store8<TY>(a.dy, base + i * threads * 8, o);
           }
         }
@@ -372,12 +409,12 @@ struct BwdShape {
   int nv, warps;
   int64_t ctas, rows_per_cta;
 };
-BwdShape bwd_shape(int64_t M, int64_t H) {
+BwdShape bwd_shape(int64_t M, int64_t H, bool four) {
   const int64_t units = H / 8;
   BwdShape s;
   s.nv = units <= 32 ? 1 : units <= 128 ? 2 : 4;
   s.warps = units <= 64 ? 1 : units <= 256 ? 2 : units <= 512 ? 4 : 8;
-  const int64_t n = int64_t(num_sms()) * (bwd_warps(s.nv) / s.warps);
+  const int64_t n = int64_t(num_sms()) * (bwd_warps(s.nv, four) / s.warps);
   s.rows_per_cta = M > n ? ceil_div(M, n) : 1;
   s.ctas = ceil_div(M, s.rows_per_cta);
   return s;
@@ -390,9 +427,12 @@ te_status bwd_kernel(const ResidualNormBwdArgs& a, const BwdShape& sh, cudaStrea
   if (!allow_smem(kernel, attr_done)) return TE_ERR_CUDA;
   const size_t y = SUMS ? size_t(a.H) * sizeof(TY) : 0;
   const size_t rest = size_t(a.H) * (sizeof(TY) + (a.dx_out ? 2 : 1) * sizeof(TR));
-  RingShape ring = ring_shape(bwd_warps(NV) / G, rest + y);
+  // (three slots for rows of 4 warps and more: 139 us for 147, LayerNorm with a gate at 16384 x 4096; for
+  // shorter ones two: 80 for 87 at 2048)
+  const int most = G >= 4 ? 3 : 2;
+  RingShape ring = ring_shape(bwd_warps(NV, LN && POST) / G, rest + y, most);
   const bool y_in_ring = ring.ctas != 0;
-  if (!y_in_ring) ring = ring_shape(1, rest);
+  if (!y_in_ring) ring = ring_shape(1, rest, most);
   if (ring.ctas == 0) return TE_ERR_UNSUPPORTED;
   const size_t bytes = kHeader + size_t(ring.slots) * (rest + (y_in_ring ? y : 0));
   kernel<<<unsigned(sh.ctas), G * 32, bytes, s>>>(a, device_status_ptr(), ring.slots, y_in_ring);
@@ -401,7 +441,7 @@ te_status bwd_kernel(const ResidualNormBwdArgs& a, const BwdShape& sh, cudaStrea
 
 template <typename TY, typename TR, bool LN, bool POST, bool SUMS>
 te_status bwd_launch(ResidualNormBwdArgs a, cudaStream_t s) {
-  const BwdShape sh = bwd_shape(a.M, a.H);
+  const BwdShape sh = bwd_shape(a.M, a.H, LN && POST);
   a.rows_per_cta = sh.rows_per_cta;
   a.gate_partials = a.partials + sh.ctas * 2 * a.H;
   te_status st;
@@ -433,8 +473,8 @@ te_status bwd_types(const ResidualNormBwdArgs& a, cudaStream_t s) {
 
 size_t residual_norm_bwd_workspace(int64_t M, int64_t H, int64_t gates) {
   if (M <= 0 || H <= 0) return 0;
-  const int64_t slots = bwd_shape(M, H).ctas + (gates > 0 ? gates : 1);
-  return size_t(bwd_shape(M, H).ctas + slots) * 2 * size_t(H) * sizeof(float);
+  const int64_t ctas = bwd_shape(M, H, false).ctas;  // (no fewer than with four sums)
+  return size_t(2 * ctas + (gates > 0 ? gates : 1)) * 2 * size_t(H) * sizeof(float);
 }
 
 te_status launch_residual_norm_bwd(const ResidualNormBwdArgs& a, cudaStream_t s) {

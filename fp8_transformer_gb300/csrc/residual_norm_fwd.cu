@@ -95,6 +95,7 @@ __global__ void __launch_bounds__(fwd_threads(G), fwd_ctas(G))
   // the kernel after this one may launch its setup now (it waits for this grid's completion)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   constexpr bool RING = G != 0;
+  constexpr bool EARLY = sizeof(TY) == 2;  // (fp32 vectors in waiting would spill)
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 red[4][G == 1 ? 1 : kMaxWarps];
   __shared__ float count[2 * kMaxWarps];  // elements that each warp holds, and one over them
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(fwd_threads(G), fwd_ctas(G))
     const int64_t base = row * a.H + tid * 8;
     const int64_t gate_at = a.gate ? row / a.gate_rows * a.H : 0;
     Unit<TY> y[NV];
-    Unit<TR> r[NV];
+    Unit<TR> r[NV];  // (ring: read from the slot when it is needed)
     Param<TY> gate[NV], g[NV], b[NV];
     if (RING) bad = !ring.wait(status);
     const uint8_t* here = ring.here();
@@ -147,17 +148,15 @@ __global__ void __launch_bounds__(fwd_threads(G), fwd_ctas(G))
     for (int i = 0; i < NV; ++i) {
       const int u = (tid + i * threads) * 8;
       y[i].zero();
-      r[i].zero();
       if (in[i]) {
         if (RING) {
           y[i].load(here, u);
-          r[i].load(here + y_bytes, u);
         } else {
           y[i].load(a.y, base + i * threads * 8);
           r[i].load(a.residual, base + i * threads * 8);
         }
-        gate[i].ask(a.gate, gate_at + u);
-        if (POST) {
+        if (EARLY) gate[i].ask(a.gate, gate_at + u);
+        if (POST && EARLY) {
           g[i].ask(a.post_gamma, u);
           if (LN) b[i].ask(a.post_beta, u);
         }
@@ -173,17 +172,26 @@ __global__ void __launch_bounds__(fwd_threads(G), fwd_ctas(G))
         if (a.post_rsigma) a.post_rsigma[row] = st.y;
       }
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (in[i]) normalize<LN>(x[i], st, g[i], b[i], shift);
+      for (int i = 0; i < NV; ++i) {
+        if (in[i]) {
+          if (!EARLY) {
+            g[i].ask(a.post_gamma, (tid + i * threads) * 8);
+            if (LN) b[i].ask(a.post_beta, (tid + i * threads) * 8);
+          }
+          normalize<LN>(x[i], st, g[i], b[i], shift);
+        }
+      }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (in[i]) {
         const int u = (tid + i * threads) * 8;
         f32x2 rp[4];
+        if (RING) r[i].load(here + y_bytes, u);
         r[i].cvt(rp);
         if (a.gate) {
           f32x2 q[4];
+          if (!EARLY) gate[i].ask(a.gate, gate_at + u);
           gate[i].get(q, 1.0f);
 #pragma unroll
           for (int p = 0; p < 4; ++p) x[i][p] = mul2(x[i][p], q[p]);
@@ -191,13 +199,15 @@ __global__ void __launch_bounds__(fwd_threads(G), fwd_ctas(G))
 #pragma unroll
         for (int p = 0; p < 4; ++p) x[i][p] = fma2(scale2, rp[p], x[i][p]);
         if (kind != OUT_NONE && !bad) store8<TR>(a.x_out, base + i * threads * 8, x[i]);
-        g[i].ask(a.gamma, u);
-        if (LN) b[i].ask(a.beta, u);
+        if (EARLY) {
+          g[i].ask(a.gamma, u);
+          if (LN) b[i].ask(a.beta, u);
+        }
       }
     }
     const float2 st = row_stats<LN, NV, G>(x, in, inv_h, a.eps, red[par], count, &bad);
     if (bad) break;
-    if (RING && tid == 0 && issued < a.M) {  // every thread has this row in registers
+    if (RING && tid == 0 && issued < a.M) {  // every thread has what it reads of this row
       fence_proxy_async_smem();
       issue(issued, ring.slot);
       issued += step;
@@ -211,6 +221,10 @@ __global__ void __launch_bounds__(fwd_threads(G), fwd_ctas(G))
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (in[i]) {
+          if (!EARLY) {
+            g[i].ask(a.gamma, (tid + i * threads) * 8);
+            if (LN) b[i].ask(a.beta, (tid + i * threads) * 8);
+          }
           normalize<LN>(x[i], st, g[i], b[i], shift);
           if (want_amax) {
 #pragma unroll
@@ -231,36 +245,63 @@ __global__ void __launch_bounds__(fwd_threads(G), fwd_ctas(G))
   }
   if (RING && bad && tid == 0) ring.drain((row - blockIdx.x) / step, (issued - blockIdx.x) / step, status);
   if (want_amax) {
-    amax = warp_max(amax);
-    if ((tid & 31) == 0) atomic_max_nonneg(a.cast.amax_out, amax);
+    if (a.beside_zero) asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (G == 1) {
+      amax = warp_max(amax);
+      if (tid == 0) atomic_max_nonneg(a.cast.amax_out, amax);
+    } else {
+      block_amax_commit(amax, a.cast.amax_out);
+    }
   }
 }
 
 inline int round_warp(int64_t n) { return int((n + 31) / 32 * 32); }
 
+__global__ void zero_scalar_kernel(float* p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  *p = 0.0f;
+}
+
+template <class K>
+te_status launch_beside(K kernel, unsigned grid, int threads, size_t smem, const ResidualNormArgs& a, int slots,
+                        cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.beside_zero ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a, device_status_ptr(), slots) == cudaSuccess ? TE_OK : TE_ERR_CUDA;
+}
+
 template <typename TY, typename TR, bool LN, bool POST, int NV, int G>
 te_status fwd_launch(const ResidualNormArgs& a, cudaStream_t s) {
   auto kernel = residual_norm_fwd_kernel<TY, TR, LN, POST, NV, G>;
   if constexpr (G == 0) {
-    kernel<<<unsigned(a.M), round_warp(a.H / 8), 0, s>>>(a, device_status_ptr(), 0);
+    return launch_beside(kernel, unsigned(a.M), round_warp(a.H / 8), 0, a, 0, s);
   } else {
     static PerDevice<bool> attr_done;
     if (!allow_smem(kernel, attr_done)) return TE_ERR_CUDA;
     const size_t slot = size_t(a.H) * (sizeof(TY) + sizeof(TR));
-    const RingShape sh = ring_shape(fwd_ctas(G), slot);
+    // three slots where L1 still holds the parameter vectors beside them (RMSNorm on both sides, 16384 x 4096:
+    // 90 us for 97 with two; LayerNorm with a gate: 95 for 90)
+    const size_t params = size_t(a.H) * sizeof(TY) * ((LN ? 2 : 1) * (POST ? 2 : 1) + (a.gate ? 1 : 0));
+    const RingShape sh = ring_shape(fwd_ctas(G), slot, G > 1 && params <= 20 * 1024 ? 3 : 2);
     if (sh.ctas == 0) return TE_ERR_UNSUPPORTED;
     const int64_t n = int64_t(num_sms()) * sh.ctas;
-    kernel<<<unsigned(a.M < n ? a.M : n), G * 32, kHeader + size_t(sh.slots) * slot, s>>>(a, device_status_ptr(),
-                                                                                         sh.slots);
+    return launch_beside(kernel, unsigned(a.M < n ? a.M : n), G * 32, kHeader + size_t(sh.slots) * slot, a, sh.slots, s);
   }
-  return cudaGetLastError() == cudaSuccess ? TE_OK : TE_ERR_CUDA;
 }
 
 template <typename TY, typename TR, bool LN, bool POST>
 te_status fwd_shape(const ResidualNormArgs& a, cudaStream_t s) {
   const int64_t units = a.H / 8;
-  // up to two rows an SM their latency counts: as many warps to a row as it has units (one token of 4096: 2.5 us)
-  if (units > 32 && a.M <= num_sms() * 2) return fwd_launch<TY, TR, LN, POST, 1, 0>(a, s);
+  // as long as every row has its CTA at once, latency counts: as many warps to a row as it has units
+  if (units > 32 && a.M <= num_sms() * (units <= 512 ? 2 : 1)) return fwd_launch<TY, TR, LN, POST, 1, 0>(a, s);
   if (units <= 32) return fwd_launch<TY, TR, LN, POST, 1, 1>(a, s);
   if (units <= 64) return fwd_launch<TY, TR, LN, POST, 2, 1>(a, s);
   if (units <= 128) return fwd_launch<TY, TR, LN, POST, 4, 1>(a, s);
@@ -278,6 +319,11 @@ te_status fwd_types(const ResidualNormArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+te_status launch_zero_scalar(float* p, cudaStream_t s) {
+  zero_scalar_kernel<<<1, 1, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? TE_OK : TE_ERR_CUDA;
+}
 
 te_status launch_residual_norm_fwd(const ResidualNormArgs& a, cudaStream_t s) {
   if (a.M == 0) return TE_OK;
