@@ -2,9 +2,10 @@
 // pass over dout and z gives dz (the operand of the layer's two products), a * dout, and the column
 // sums behind dbias and dgate.  Bound by memory: it reads and writes each tensor once.
 //
-// A CTA takes a strip of 256 columns (8 to a lane) and up to 128 rows that share a gate; its 8 warps
-// take the rows in turn, keep the columns' sums in registers, and leave one row of partial sums,
-// which a second kernel adds in a fixed order.
+// A CTA takes a strip of 256 columns (8 to a lane) and a chunk of rows that share a gate, as many as put
+// one wave of CTAs on the SMs (in chunks of 128 rows 4100 x 4096 took a second, almost empty one: 35 us
+// with gelu, not 21); its 8 warps take the rows in turn, keep the columns' sums in registers, and leave
+// one row of partial sums, which a second kernel adds in a fixed order.
 #include "cast.cuh"
 #include "common.cuh"
 #include "kernels.h"
@@ -14,8 +15,9 @@ namespace te {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kRows = 128;
-constexpr int kUnroll = 2;  // rows of loads in flight per warp
+constexpr int kCtasPerSm = 2;
+constexpr int kMaxRows = 256;  // of a chunk: no sum of a thread runs over more than 32
+constexpr int kUnroll = 4;  // rows of loads in flight per warp (86 us a call for 89 with 3 CTAs and 2 rows)
 constexpr int kStrip = 256;
 
 template <typename T>
@@ -40,11 +42,32 @@ __device__ __forceinline__ void cvt8(const uint4 (&w)[2], f32x2 (&p)[4]) {
   }
 }
 
-// chunks of one gate's rows
-__host__ __device__ __forceinline__ int64_t chunks_of(int64_t gate_rows) { return (gate_rows + kRows - 1) / kRows; }
+// gelu(h) = h s and gelu'(h) = s + 2 h sqrt(2/pi) (1 + 3 * 0.044715 h^2) s (1 - s) from one logistic
+// s = 1 / (1 + e) of twice the inner function, 1 - s = e s (e's exponent clamped so that it stays finite).
+__device__ __forceinline__ void gelu_both(f32x2 h, f32x2& act, f32x2& dact) {
+  const f32x2 hh = mul2(h, h);
+  const f32x2 e = ex2_2(min2s(mul2(h, fma2(hh, f2s(kGeluA2), f2s(kGeluA1))), 80.0f * kLog2e));
+  const f32x2 s = rcp2(add2(e, f2s(1.0f)));
+  const f32x2 q = mul2(h, fma2(hh, f2s(6.0f * kGeluK0 * kGeluK1), f2s(2.0f * kGeluK0)));
+  act = mul2(h, s);
+  dact = fma2(q, mul2(s, mul2(e, s)), s);
+}
+
+// Rows of a chunk, and the chunks of one gate's rows.
+int64_t rows_of(int64_t M, int64_t N, int64_t gate_rows) {
+  const int64_t chunks = int64_t(num_sms()) * kCtasPerSm / ceil_div(N, int64_t(kStrip));
+  int64_t per_gate = chunks / (M / gate_rows);
+  if (per_gate < 1) per_gate = 1;
+  per_gate *= ceil_div(gate_rows, per_gate * kMaxRows);  // (whole waves of shorter chunks)
+  const int64_t rows = ceil_div(gate_rows, per_gate);
+  return (rows + kWarps - 1) / kWarps * kWarps;  // whole rounds of the warps
+}
+__host__ __device__ __forceinline__ int64_t chunks_of(int64_t gate_rows, int64_t rows) {
+  return (gate_rows + rows - 1) / rows;
+}
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(kWarps * 32, 3) dense_residual_grad_kernel(DenseResidualGradArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_kernel(DenseResidualGradArgs a) {
   __shared__ float red[kWarps][2][kStrip];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const CastState cs = cast_begin(a.cast);
@@ -53,11 +76,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) dense_residual_grad_kernel(Den
   const bool read_z = ACT != TE_IDENTITY || a.dgate != nullptr;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = (int64_t(blockIdx.y) * 32 + lane) * 8;
-  const int64_t per_gate = chunks_of(a.gate_rows);
+  const int64_t per_gate = chunks_of(a.gate_rows, a.chunk_rows);
   const int64_t gate_row = blockIdx.x / per_gate;
-  const int64_t r0 = gate_row * a.gate_rows + (blockIdx.x % per_gate) * kRows;
+  const int64_t r0 = gate_row * a.gate_rows + (blockIdx.x % per_gate) * a.chunk_rows;
   const int64_t end = (gate_row + 1) * a.gate_rows;
-  const int64_t r1 = r0 + kRows < end ? r0 + kRows : end;
+  const int64_t r1 = r0 + a.chunk_rows < end ? r0 + a.chunk_rows : end;
   f32x2 sz[4], sa[4], gt[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) sz[p] = sa[p] = f2s(0.0f), gt[p] = f2s(1.0f);
@@ -95,6 +118,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) dense_residual_grad_kernel(Den
             sigmoid2(zp[p], sg, eg);
             dact = mul2(sg, fma2(zp[p], mul2(eg, sg), f2s(1.0f)));
             act = mul2(zp[p], sg);
+          } else if constexpr (ACT == TE_GELU) {  // as do gelu and gelu'
+            gelu_both(zp[p], act, dact);
           } else if constexpr (ACT != TE_IDENTITY) {
             act = act2c<ACT>(zp[p]);
             dact = dact2c<ACT>(zp[p]);
@@ -147,7 +172,7 @@ __global__ void __launch_bounds__(kSumWarps * 32) dense_residual_sum_kernel(Dens
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t j = int64_t(blockIdx.x) * 128 + lane * 4;  // N is a multiple of 16
-  const int64_t per_gate = chunks_of(a.gate_rows);
+  const int64_t per_gate = chunks_of(a.gate_rows, a.chunk_rows);
   auto column = [&](int64_t c0, int64_t c1, int half, float* out) {
     float4 t = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (j < a.N) {
@@ -190,14 +215,16 @@ void launch_act(const DenseResidualGradArgs& a, dim3 grid, cudaStream_t s) {
 
 size_t dense_residual_grad_workspace(int64_t M, int64_t N, int64_t gates) {
   if (M <= 0 || N <= 0) return 0;
-  if (gates < 1) gates = 1;
-  return size_t(chunks_of(M / gates) * gates) * 2 * size_t(N) * sizeof(float);
+  if (gates < 1 || gates > M) gates = 1;
+  const int64_t gate_rows = M / gates;
+  return size_t(chunks_of(gate_rows, rows_of(M, N, gate_rows)) * gates) * 2 * size_t(N) * sizeof(float);
 }
 
-te_status launch_dense_residual_grad(const DenseResidualGradArgs& a, cudaStream_t s) {
+te_status launch_dense_residual_grad(DenseResidualGradArgs a, cudaStream_t s) {
   if (a.M == 0) return TE_OK;
   ProfileScope prof(TE_KERNEL_DACT_DBIAS, s);
-  const int64_t gates = a.M / a.gate_rows, chunks = gates * chunks_of(a.gate_rows), strips = ceil_div(a.N, kStrip);
+  a.chunk_rows = rows_of(a.M, a.N, a.gate_rows);
+  const int64_t gates = a.M / a.gate_rows, chunks = gates * chunks_of(a.gate_rows, a.chunk_rows), strips = ceil_div(a.N, kStrip);
   if (chunks > 0x7fffffff || strips > 65535) return TE_ERR_UNSUPPORTED;
   const dim3 grid{unsigned(chunks), unsigned(strips)};
   if (a.dtype == TE_F32) launch_act<float>(a, grid, s);

@@ -331,9 +331,10 @@ struct DenseResidualGradArgs {
   float* dbias = nullptr;
   float* dgate = nullptr;      // [M / gate_rows, N]
   float* partials = nullptr;   // workspace
+  int64_t chunk_rows = 0;      // set at launch
   CastSpec cast;
 };
-te_status launch_dense_residual_grad(const DenseResidualGradArgs& a, cudaStream_t s);
+te_status launch_dense_residual_grad(DenseResidualGradArgs a, cudaStream_t s);
 size_t dense_residual_grad_workspace(int64_t M, int64_t N, int64_t gates);
 
 // Sum of the squares of many tensors, and the tensors scaled by min(1, max_norm / (norm + eps)).

@@ -292,7 +292,9 @@ def test_workspaces():
     dout, o = bwd(t, n, "identity", 1.0, z)
     t["dout"] = dout
     need = te.lib().te_dense_residual_bwd_workspace(200, 4096, 256, 1, te.binding.TE_BF16)
-    for size in (need, 200 * 256 * 2 + 2 * 2 * 256 * 4 + 512):
+    gemm = te.binding.TE_OP_GEMM  # the scratch that each of the two products would use: {M, K, N}
+    split = max(te.workspace_size(gemm, 200, 256, 4096), te.workspace_size(gemm, 4096, 200, 256))
+    for size in (need, need - (split + 255) // 256 * 256):
         _, o2 = bwd(t, n, "identity", 1.0, z, workspace=torch.empty(size, dtype=torch.uint8, device=DEV))
         check_bwd(t, "identity", 1.0, z, dout, o2)
     with pytest.raises(te.TEError):
