@@ -561,6 +561,9 @@ _ACT_DTYPES = (torch.float32, torch.bfloat16)
 _F32 = (torch.float32,)
 _U8 = (torch.uint8,)
 _E4M3_BYTES = (torch.uint8, torch.float8_e4m3fn)
+_OUT_DTYPES = _ACT_DTYPES + _E4M3_BYTES
+_BF16 = (torch.bfloat16,)
+_GEMM_DTYPES = _BF16 + _E4M3_BYTES
 
 
 def _format(fmt) -> int:
@@ -907,8 +910,6 @@ def _sized_by(name, *dims):
 
 def _gate(gate, M, H, dtypes, dev):
     """(address, rows) of a gate [H] or [G, H] whose rows divide M."""
-    if gate is None:
-        return None, 1
     g = gate.shape[0] if gate.dim() == 2 else 1
     if gate.dim() == 2:
         p = _arg("gate", gate, (g, H), dtypes, dev)
@@ -917,10 +918,6 @@ def _gate(gate, M, H, dtypes, dev):
     if g < 1 or M % g:
         raise ValueError(f"gate: its {g} rows do not divide {M}")
     return p, g
-
-
-def _opt(name, t, shape, dtypes, dev):
-    return None if t is None else _arg(name, t, shape, dtypes, dev)
 
 
 def te_residual_norm_fwd(y, residual, gamma, beta, x_out, out, norm_type="layernorm", zero_centered_gamma=False,
@@ -933,17 +930,22 @@ def te_residual_norm_fwd(y, residual, gamma, beta, x_out, out, norm_type="layern
     dev = torch.cuda.current_device()
     d, r = (y.dtype,), (residual.dtype,)
     py, pr = _arg("y", y, (M, H), _ACT_DTYPES, dev), _arg("residual", residual, (M, H), _ACT_DTYPES, dev)
-    pg, pb = _arg("gamma", gamma, (H,), d, dev), _opt("beta", beta, (H,), d, dev)
-    ppg, ppb = _opt("post_gamma", post_gamma, (H,), d, dev), _opt("post_beta", post_beta, (H,), d, dev)
-    pgt, ng = _gate(gate, M, H, d, dev)
+    h, m = (H,), (M,)
+    pg = _arg("gamma", gamma, h, d, dev)
+    pb = None if beta is None else _arg("beta", beta, h, d, dev)
+    ppg = None if post_gamma is None else _arg("post_gamma", post_gamma, h, d, dev)
+    ppb = None if post_beta is None else _arg("post_beta", post_beta, h, d, dev)
+    pgt, ng = (None, 1) if gate is None else _gate(gate, M, H, d, dev)
     px = _arg("x_out", x_out, (M, H), r, dev)
-    po = _arg("out", out, (M, H), _ACT_DTYPES + _E4M3_BYTES, dev)
-    stats = [_opt(n, t, (M,), _F32, dev) for n, t in (("mu", mu), ("rsigma", rsigma), ("post_mu", post_mu),
-                                                      ("post_rsigma", post_rsigma))]
+    po = _arg("out", out, (M, H), _OUT_DTYPES, dev)
+    pm = None if mu is None else _arg("mu", mu, m, _F32, dev)
+    prs = None if rsigma is None else _arg("rsigma", rsigma, m, _F32, dev)
+    ppm = None if post_mu is None else _arg("post_mu", post_mu, m, _F32, dev)
+    pprs = None if post_rsigma is None else _arg("post_rsigma", post_rsigma, m, _F32, dev)
     cq = None if q is None else ctypes.byref(_quantizer("q", q, dev))
     st = lib().te_residual_norm_fwd(py, _dt(y), pr, _dt(residual), M, H, pg, pb, ppg, ppb, pgt, ng,
                                     float(residual_scale), _norm_id(norm_type), int(bool(zero_centered_gamma)),
-                                    float(epsilon), cq, px, po, _dt(out), *stats, _stream(stream, dev))
+                                    float(epsilon), cq, px, po, _dt(out), pm, prs, ppm, pprs, _stream(stream, dev))
     _check("te_residual_norm_fwd", st)
     return out
 
@@ -957,24 +959,33 @@ def te_residual_norm_bwd(dout, dx_out, x_out, mu, rsigma, gamma, dresidual, dy, 
     M, H = dout.shape
     dev = torch.cuda.current_device()
     d, r = (dout.dtype,), (x_out.dtype,)
-    pd, pxo = _arg("dout", dout, (M, H), _ACT_DTYPES, dev), _opt("dx_out", dx_out, (M, H), r, dev)
-    px = _arg("x_out", x_out, (M, H), _ACT_DTYPES, dev)
-    py = _opt("y", y, (M, H), d, dev)
-    stats = [_opt(n, t, (M,), _F32, dev) for n, t in (("mu", mu), ("rsigma", rsigma), ("post_mu", post_mu),
-                                                      ("post_rsigma", post_rsigma))]
-    vecs = [_opt(n, t, (H,), d, dev) for n, t in (("gamma", gamma), ("post_gamma", post_gamma),
-                                                  ("post_beta", post_beta))]
-    pgt, ng = _gate(gate, M, H, d, dev)
-    pdr, pdy = _opt("dresidual", dresidual, (M, H), r, dev), _opt("dy", dy, (M, H), d, dev)
-    grads = [_opt(n, t, (H,), _F32, dev) for n, t in (("dgamma", dgamma), ("dbeta", dbeta),
-                                                      ("dpost_gamma", dpost_gamma), ("dpost_beta", dpost_beta))]
+    mh, h, m = (M, H), (H,), (M,)
+    pd = _arg("dout", dout, mh, _ACT_DTYPES, dev)
+    pxo = None if dx_out is None else _arg("dx_out", dx_out, mh, r, dev)
+    px = _arg("x_out", x_out, mh, _ACT_DTYPES, dev)
+    py = None if y is None else _arg("y", y, mh, d, dev)
+    pm = None if mu is None else _arg("mu", mu, m, _F32, dev)
+    prs = None if rsigma is None else _arg("rsigma", rsigma, m, _F32, dev)
+    ppm = None if post_mu is None else _arg("post_mu", post_mu, m, _F32, dev)
+    pprs = None if post_rsigma is None else _arg("post_rsigma", post_rsigma, m, _F32, dev)
+    pg = _arg("gamma", gamma, h, d, dev)
+    ppg = None if post_gamma is None else _arg("post_gamma", post_gamma, h, d, dev)
+    ppb = None if post_beta is None else _arg("post_beta", post_beta, h, d, dev)
+    pgt, ng = (None, 1) if gate is None else _gate(gate, M, H, d, dev)
+    pdr = None if dresidual is None else _arg("dresidual", dresidual, mh, r, dev)
+    pdy = None if dy is None else _arg("dy", dy, mh, d, dev)
+    pdga = None if dgamma is None else _arg("dgamma", dgamma, h, _F32, dev)
+    pdb = None if dbeta is None else _arg("dbeta", dbeta, h, _F32, dev)
+    pdpg = None if dpost_gamma is None else _arg("dpost_gamma", dpost_gamma, h, _F32, dev)
+    pdpb = None if dpost_beta is None else _arg("dpost_beta", dpost_beta, h, _F32, dev)
     pdg = None if dgate is None else _arg("dgate", dgate, (H,) if gate is not None and gate.dim() == 1 else (ng, H),
                                           _F32, dev)
     n = _sized_by("te_residual_norm_bwd_workspace", M, H, ng) if workspace is None else 0
     workspace, pw, nw = _workspace_of(n, dout, workspace, stream)
-    st = lib().te_residual_norm_bwd(pd, pxo, px, py, _dt(dout), _dt(x_out), M, H, *stats, *vecs, pgt, ng,
-                                    float(residual_scale), _norm_id(norm_type), int(bool(zero_centered_gamma)), pdr,
-                                    pdy, *grads, pdg, pw, nw, _stream(stream, dev))
+    st = lib().te_residual_norm_bwd(pd, pxo, px, py, _dt(dout), _dt(x_out), M, H, pm, prs, ppm, pprs, pg, ppg, ppb,
+                                    pgt, ng, float(residual_scale), _norm_id(norm_type),
+                                    int(bool(zero_centered_gamma)), pdr, pdy, pdga, pdb, pdpg, pdpb, pdg, pw, nw,
+                                    _stream(stream, dev))
     _check("te_residual_norm_bwd", st)
 
 
@@ -986,14 +997,15 @@ def te_dense_residual_fwd(x, kernel, residual, out, bias=None, activation="ident
     M, K = x.shape
     N = kernel.shape[1]
     dev = torch.cuda.current_device()
-    bf = (torch.bfloat16,)
+    bf = _BF16
     e4m3 = x.dtype in _E4M3_BYTES
-    px = _arg("x", x, (M, K), bf + _E4M3_BYTES, dev)
+    px = _arg("x", x, (M, K), _GEMM_DTYPES, dev)
     pk = _arg("kernel", kernel, (K, N), _E4M3_BYTES if e4m3 else bf, dev)
     pr = _arg("residual", residual, (M, N), _ACT_DTYPES, dev)
     po = _arg("out", out, (M, N), (residual.dtype,), dev)
-    pb, pz = _opt("bias", bias, (N,), bf, dev), _opt("saved_z", saved_z, (M, N), bf, dev)
-    pgt, ng = _gate(gate, M, N, bf, dev)
+    pb = None if bias is None else _arg("bias", bias, (N,), bf, dev)
+    pz = None if saved_z is None else _arg("saved_z", saved_z, (M, N), bf, dev)
+    pgt, ng = (None, 1) if gate is None else _gate(gate, M, N, bf, dev)
     n = _sized_by("te_dense_residual_fwd_workspace", M, K, N, _dt(x)) if workspace is None else 0
     pw, nw = None, 0
     if n or workspace is not None:
@@ -1013,16 +1025,16 @@ def te_dense_residual_bwd(dout, x, kernel, dx, dkernel, dresidual=None, saved_z=
     M, K = x.shape
     N = kernel.shape[1]
     dev = torch.cuda.current_device()
-    bf = (torch.bfloat16,)
+    bf = _BF16
     e4m3 = x.dtype in _E4M3_BYTES
-    px = _arg("x", x, (M, K), bf + _E4M3_BYTES, dev)
+    px = _arg("x", x, (M, K), _GEMM_DTYPES, dev)
     pk = _arg("kernel", kernel, (K, N), _E4M3_BYTES if e4m3 else bf, dev)
     pd = _arg("dout", dout, (M, N), _ACT_DTYPES, dev)
-    pz = _opt("saved_z", saved_z, (M, N), bf, dev)
-    pgt, ng = _gate(gate, M, N, bf, dev)
+    pz = None if saved_z is None else _arg("saved_z", saved_z, (M, N), bf, dev)
+    pgt, ng = (None, 1) if gate is None else _gate(gate, M, N, bf, dev)
     pdx, pdk = _arg("dx", dx, (M, K), bf, dev), _arg("dkernel", dkernel, (K, N), bf, dev)
-    pdr = _opt("dresidual", dresidual, (M, N), (dout.dtype,), dev)
-    pdb = _opt("dbias", dbias, (N,), _F32, dev)
+    pdr = None if dresidual is None else _arg("dresidual", dresidual, (M, N), (dout.dtype,), dev)
+    pdb = None if dbias is None else _arg("dbias", dbias, (N,), _F32, dev)
     pdg = None if dgate is None else _arg("dgate", dgate, (N,) if gate is not None and gate.dim() == 1 else (ng, N),
                                           _F32, dev)
     cq = None if q is None else ctypes.byref(_quantizer("q", q, dev))

@@ -373,11 +373,13 @@ te_status launch_grad_squares(const GradTensor* t, int64_t count, GradSlot* slot
 }
 
 te_status launch_grad_norm(const GradSlot* slots, int used, float* norm, cudaStream_t s) {
+  ProfileScope prof(TE_KERNEL_QUANTIZE, s);
   return launch_dependent(grad_norm_kernel, dim3(1), dim3(32), s, slots, used, norm);
 }
 
 te_status launch_grad_clip(const GradTensor* t, int64_t count, const GradSlot* slots, int used, double max_norm,
                            double eps, float* norm, cudaStream_t s) {
+  ProfileScope prof(TE_KERNEL_QUANTIZE, s);
   return count <= kSmall ? clip<kSmall>(t, count, slots, used, max_norm, eps, norm, s)
                          : clip<kLarge>(t, count, slots, used, max_norm, eps, norm, s);
 }

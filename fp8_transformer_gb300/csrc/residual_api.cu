@@ -169,7 +169,7 @@ te_status te_residual_norm_fwd(const void* y, te_dtype dtype, const void* residu
   if (!post_gamma && (post_beta || post_mu || post_rsigma)) return TE_ERR_INVALID_ARG;
   const int64_t gate_rows = gate_rows_of(gate, gates, M);
   if (gate_rows == 0) return TE_ERR_INVALID_ARG;
-  if ((out_dtype == TE_E4M3 && !enabled(q)) || !quantizer_ok(q)) return TE_ERR_INVALID_ARG;
+  if ((out_dtype == TE_E4M3 && !enabled(q)) || !quantizer_ok(q) || (q && !aligned4(q->amax))) return TE_ERR_INVALID_ARG;
   if (H % 8 || H > 8192 || M > kMaxDim) return TE_ERR_UNSUPPORTED;
   for (const void* p : {y, residual, gamma, beta, post_gamma, post_beta, gate, static_cast<const void*>(x_out),
                         static_cast<const void*>(out)})

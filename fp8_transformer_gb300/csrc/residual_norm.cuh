@@ -151,7 +151,7 @@ struct RingShape {
 };
 inline RingShape ring_shape(int ctas, size_t bytes, int most) {
   for (; ctas >= 1; ctas = ctas > 1 ? ctas / 2 : 0) {
-    const size_t room = kSmem / ctas - 1024 - kHeader - 1024;  // 1 KB to the CTA itself, 1 KB static
+    const size_t room = kSmem / ctas - 1024 - kHeader - 1536;  // 1 KB to the CTA itself, 1.5 KB static
     const size_t fit = room / bytes;
     if (fit >= 2) return RingShape{ctas, int(fit < size_t(most) ? fit : size_t(most))};
   }

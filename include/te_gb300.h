@@ -665,7 +665,7 @@ te_status te_norm_bwd(const void* dz, const void* x, const float* mu, const floa
  */
 typedef enum {
   TE_KERNEL_NORM_FWD = 0,
-  TE_KERNEL_QUANTIZE = 1,
+  TE_KERNEL_QUANTIZE = 1,    /* casts, and the squares and the clipping of gradients */
   TE_KERNEL_ACT_LU = 2,
   TE_KERNEL_DACT_DBIAS = 3,
   TE_KERNEL_GEMM = 4,        /* GEMM + bias epilogue */

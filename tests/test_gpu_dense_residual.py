@@ -90,7 +90,7 @@ def check_fwd(t, act, scale, out, z, rows=None):
 
 SHAPES = [(1, 16, 16), (1, 4096, 4096), (2, 512, 48), (5, 1040, 272), (8, 2064, 4096), (9, 64, 1008), (16, 4096, 512),
           (17, 1024, 640), (31, 96, 8192), (33, 14336, 256), (64, 256, 64), (65, 528, 272), (129, 512, 528), (130, 1024, 1024),
-          (257, 80, 16), (300, 4096, 784)]
+          (257, 80, 16), (300, 4096, 784), (16, 64, 28672), (9, 4096, 32), (24, 160, 14336), (32, 8192, 80)]
 
 
 @pytest.mark.parametrize("M,K,N", SHAPES)

@@ -3,8 +3,9 @@
 Windows.  A row's sum passes at most 32 values in a thread, 5 steps of a warp and 32 warps: under 70
 roundings of 2^-24, and a value is formed from two such statistics and some ten operations more, so an
 fp32 value lies within W = 2^-17 of its terms' magnitudes.  What is stored is a rounding of a number in
-that window (rounding is monotonic).  Column sums add one rounding for each of a CTA's rows (under 8 in
-these cases), 40 for the joined CTAs and 16 for the warps: W + 64 * 2^-24 < 2^-16 of the magnitudes.
+that window (rounding is monotonic).  Column sums add one rounding for each of a CTA's rows (at most 10 in
+these cases), 40 for the joined CTAs (32 terms and their own number / 32) and a few more:
+W + 64 * 2^-24 < 2^-16 of the magnitudes.
 """
 
 import ctypes
@@ -321,6 +322,70 @@ def test_streams_graphs_and_host_threads():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(x, want_x) and torch.equal(out, want_out)
+
+
+def test_amax_in_a_graph():
+    """The amax is zeroed by every replay, beside the kernel that takes it."""
+    t, n = draw(37, 1024, BF, BF, 0, True)
+    x, out = torch.empty_like(t["y"]), torch.empty(37, 1024, dtype=torch.uint8, device=DEV)
+    q = te.Quantizer(16.0)
+    args = (t["y"], t["residual"], t["gamma"], t["beta"], x, out)
+    kw = dict(post_gamma=t["post_gamma"], post_beta=t["post_beta"], q=q)
+    te.te_residual_norm_fwd(*args, **kw)
+    first = q.amax.item()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        te.te_residual_norm_fwd(*args, **kw)
+        copy = q.amax.clone()
+    q.amax.fill_(1e9)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert copy.item() == first == q.amax.item()
+    t["gamma"].mul_(0.5)
+    t["beta"].mul_(0.5)
+    g.replay()
+    torch.cuda.synchronize()
+    assert copy.item() == pytest.approx(first / 2, rel=2.0 ** -20)
+
+
+def test_two_host_threads():
+    """Calls of two threads on streams of their own, each with its own kept workspace."""
+    import threading
+    t, n = draw(48, 512, BF, BF, 2, True)
+    want, _, _ = run_bwd(t, n, True, False, 1.0)
+    got, errors = {}, []
+
+    def work(k):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    tt, nn = draw(48, 512, BF, BF, 2, True)
+                    torch.cuda.current_stream().synchronize()
+                    got[k], _, _ = run_bwd(tt, nn, True, False, 1.0)
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:  # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(2)]
+    [h.start() for h in threads]
+    [h.join() for h in threads]
+    assert not errors
+    for k in range(2):
+        for name in want:
+            assert torch.equal(want[name], got[k][name]), name
+
+
+@pytest.mark.parametrize("H", [64, 1024, 4096])
+def test_many_rows_to_a_cta(H):
+    """Rows far beyond the ring, their number no multiple of anything, gates that end anywhere."""
+    M = 9009 if H < 4096 else 3003
+    t, n = draw(M, H, BF, BF, 3, True)
+    x, out, s, _ = run_fwd(t, True, False, BF, 1.0)
+    check_fwd(t, True, False, 1.0, x, out, s)
+    g, want, _ = run_bwd(t, n, True, False, 1.0)
+    check_bwd(g, want)
 
 
 def test_workspace_is_checked():
