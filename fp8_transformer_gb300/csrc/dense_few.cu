@@ -1,18 +1,22 @@
 // The dense layer that ends in the residual stream, for a few tokens (up to 32 rows):
 //   out = a residual + gate act(alpha x W + b)
 // Reading W [K, N] once bounds it, so W goes straight from memory into the registers that the tensor
-// cores read: a lane loads 16 bytes of a row of W at a time (8 bf16 or 16 E4M3 columns), four
-// neighbouring rows k .. k + 3 for each step of 16, and pairs two rows' values of a column by byte
-// permutes (E4M3 values become f16, exactly: with mma.sync on E4M3 itself, which needs the bytes of four
-// rows together, 17 tokens through [14336, 4096] took 25 us for 21).  W is the first operand of mma.sync m16n8k16, so that a
-// product takes two columns of each of the 8 lane groups as its 16 rows and 8 tokens as its columns;
-// which row of W is which k of the product does not matter as long as x is read in the same order.
-// mma.sync rather than tcgen05: the arithmetic is far from any bound, and no weight passes through
-// shared memory.
+// cores read: a lane loads 16 bytes of a row of W at a time (8 bf16 or 16 E4M3 columns; of E4M3 beyond 8
+// tokens 8 bytes, for the registers), four neighbouring rows k .. k + 3 for each step of 16, and pairs
+// two rows' values of a column by byte permutes (E4M3 values become f16, exactly: with mma.sync on E4M3
+// itself, which needs the bytes of four rows together, 17 tokens through [14336, 4096] took 25 us for 21).
+// W is the first operand of mma.sync m16n8k16, so that a product takes two columns of each of the 8 lane
+// groups as its 16 rows and 8 tokens as its columns; which row of W is which k of the product does not
+// matter as long as x is read in the same order.  mma.sync rather than tcgen05: the arithmetic is far
+// from any bound, and no weight passes through shared memory.
 //
-// A CTA of 8 warps takes 64 (E4M3: 128) columns, its warps different ranges of K, and a cluster of CTAs
-// the ranges of one block of columns, where the columns alone leave SMs idle.  The partial sums meet
-// in shared memory and over the cluster in a fixed order.
+// A CTA of 8 warps takes the 64 (E4M3 up to 8 tokens: 128) columns of one lane's width, its warps different
+// ranges of K, and a cluster of CTAs the ranges of one block of columns, where the columns alone leave SMs
+// idle.  The partial sums meet in shared memory and over the cluster in a fixed order.  One token through
+// [14336, 4096]: 24 us a call, 4.9 TB/s; about 4 of them are launch, first bytes and the sums' way.
+#include <cstring>
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
 #include "sync.cuh"
@@ -24,7 +28,6 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kAhead = 4;  // steps of 16 rows of W in flight per lane
 constexpr int kMaxCluster = 8;
 
 struct FewArgs {
@@ -42,15 +45,22 @@ struct FewArgs {
   int M, N, K, gate_rows;
 };
 
-template <bool FP8>
+// Two CTAs to an SM throughout, with as many loads in flight as their registers leave room for (one CTA of
+// twice the registers: 36 to 39 us for 27 to 29, 32 tokens in E4M3 through [14336 to 16384, 4096], and 40
+// for 36, 32 in bf16 through [8192, 8192]).  Staged in shared memory by asynchronous copies instead, which
+// leave room for twice the bytes, one token through [14336, 4096] took 35 us for 24.
+template <bool FP8, int XT>
 struct Form {
-  static constexpr int kLane = FP8 ? 16 : 8;   // columns of a lane's 16 bytes
-  static constexpr int kCols = 8 * kLane;      // of a CTA
-  static constexpr int kPitch = kCols + 4;     // floats from row to row of a partial sum
+  static constexpr int kWords = FP8 && XT > 1 ? 2 : 4;  // of 4 bytes, of a row of W to a lane
+  static constexpr int kLane = kWords * (FP8 ? 4 : 2);  // columns of them
+  static constexpr int kCols = 8 * kLane;               // of a CTA
+  static constexpr int kPitch = kCols + 4;              // floats from row to row of a partial sum
+  static constexpr int kAhead = XT == 1 ? 4 : XT == 4 ? 2 : FP8 && XT == 2 ? 4 : !FP8 && XT == 3 ? 2 : 3;  // steps in flight
+  static constexpr int kCtas = 2;                       // of an SM
 };
 
 template <bool FP8, int XT>
-constexpr size_t smem_bytes() { return size_t(kWarps / 2) * 8 * XT * Form<FP8>::kPitch * sizeof(float); }
+constexpr size_t smem_bytes() { return size_t(kWarps / 2) * 8 * XT * Form<FP8, XT>::kPitch * sizeof(float); }
 
 template <bool FP8>
 __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
@@ -78,9 +88,6 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {  // of the low 16
   return r;
 }
 
-// CTAs of an SM, by their registers.
-__host__ __device__ constexpr int few_ctas(bool fp8, int xt) { return (fp8 ? 2 : 1) * xt <= 2 ? 2 : 1; }
-
 // x's values of four neighbouring k: two operand registers.
 template <bool FP8>
 struct XFrag {
@@ -104,8 +111,9 @@ struct XFrag {
 
 // XT: groups of 8 tokens.
 template <bool FP8, int XT>
-__global__ void __launch_bounds__(kThreads, few_ctas(FP8, XT)) dense_few_kernel(const FewArgs a) {
-  using F = Form<FP8>;
+__global__ void __launch_bounds__(kThreads, Form<FP8, XT>::kCtas) dense_few_kernel(const FewArgs a) {
+  using F = Form<FP8, XT>;
+  constexpr int kAhead = F::kAhead, LW = F::kWords;
   constexpr int NP = F::kLane / 2;  // products of a step for each group of tokens: a pair of the lane's columns
   constexpr int ROWS = 8 * XT;
   extern __shared__ __align__(16) float part[];  // [4][ROWS][kPitch]
@@ -123,14 +131,18 @@ __global__ void __launch_bounds__(kThreads, few_ctas(FP8, XT)) dense_few_kernel(
   constexpr int es = FP8 ? 1 : 2;
   const size_t row_bytes = size_t(a.N) * es;
   const uint8_t* wp = static_cast<const uint8_t*>(a.w) + (size_t(s0) * 16 + 4 * t) * row_bytes + size_t(col) * es;
-  uint4 w[kAhead][4];
+  uint32_t w[kAhead][4][LW];
   XFrag<FP8> x[kAhead][XT];
   auto load = [&](int s, int b) {
     const uint8_t* p = wp + size_t(s - s0) * 16 * row_bytes;
     const bool here = s < s1;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      w[b][i] = here && in ? *reinterpret_cast<const uint4*>(p + i * row_bytes) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 4; ++i) {
+      using V = std::conditional_t<LW == 4, uint4, uint2>;
+      V v{};
+      if (here && in) v = *reinterpret_cast<const V*>(p + i * row_bytes);
+      memcpy(w[b][i], &v, sizeof(V));
+    }
 #pragma unroll
     for (int r = 0; r < XT; ++r) {
       const int row = g + 8 * r;
@@ -152,12 +164,9 @@ __global__ void __launch_bounds__(kThreads, few_ctas(FP8, XT)) dense_few_kernel(
       uint32_t xb[XT][2];
 #pragma unroll
       for (int m = 0; m < XT; ++m) x[b][m].get(xb[m][0], xb[m][1]);
-      const uint32_t(&r0)[4] = reinterpret_cast<const uint32_t(&)[4]>(w[b][0]);
-      const uint32_t(&r1)[4] = reinterpret_cast<const uint32_t(&)[4]>(w[b][1]);
-      const uint32_t(&r2)[4] = reinterpret_cast<const uint32_t(&)[4]>(w[b][2]);
-      const uint32_t(&r3)[4] = reinterpret_cast<const uint32_t(&)[4]>(w[b][3]);
+      const auto &r0 = w[b][0], &r1 = w[b][1], &r2 = w[b][2], &r3 = w[b][3];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < LW; ++q) {
         if constexpr (FP8) {
           const uint32_t lo[2] = {__byte_perm(r0[q], r1[q], 0x5140), __byte_perm(r0[q], r1[q], 0x7362)};
           const uint32_t hi[2] = {__byte_perm(r2[q], r3[q], 0x5140), __byte_perm(r2[q], r3[q], 0x7362)};
@@ -267,8 +276,8 @@ te_status launch(const FewArgs& f, cudaStream_t s) {
     return TE_ERR_CUDA;
   // CTAs to a block of columns: as many as keep every SM at the CTAs it holds at once, while each warp has
   // a round of loads to itself
-  const int blocks = int(ceil_div(f.N, int64_t(Form<FP8>::kCols)));
-  const int64_t room = int64_t(num_sms()) * few_ctas(FP8, XT);
+  const int blocks = int(ceil_div(f.N, int64_t(Form<FP8, XT>::kCols)));
+  const int64_t room = int64_t(num_sms()) * Form<FP8, XT>::kCtas;
   int ranks = 1;
   while (ranks < kMaxCluster && int64_t(blocks) * ranks * 2 <= room && f.K / 16 >= ranks * 2 * kWarps) ranks *= 2;
   cudaLaunchConfig_t cfg = {};
@@ -292,13 +301,13 @@ te_status launch(const FewArgs& f, cudaStream_t s) {
 
 // Up to 8 rows always.  Each further group of 8 repeats the products of every weight, while the tiles of
 // launch_gemm (256 columns wide, 128 rows high) cost the same for 1 row and for 128 and gain with their
-// number: from about 4 / 3 tile groups an SM on they are faster.  Measured (us, here / tiles), bf16,
-// K = 4096: N = 28672 (112 tiles) 48 / 62 at 8 rows, 56 / 44 at 16; N = 14336 (56) 29 / 38 at 16, 45 / 38
-// at 32; K = 14336, N = 4096 (16) 25 / 55 at one row, 37 / 55 at 32.  E4M3 likewise: 26 / 34, 41 / 35,
-// 22 / 27, 31 / 25, 17 / 40, 28 / 40.
+// number: from about 6 / 5 tiles and groups an SM on they are faster.  Measured (us, here / tiles), bf16,
+// K = 4096: N = 28672 (112 tiles) 48 / 62 at 8 rows, 55 / 44 at 16; N = 14336 (56) 28 / 38 at 16, 36 / 38
+// at 32; K = 14336, N = 4096 (16) 24 / 55 at one row, 33 / 55 at 32.  E4M3 likewise: 27 / 34, 37 / 35;
+// 20 / 25, 28 / 25; 17 / 40, 27 / 40.
 bool dense_few_serves(int64_t M, int64_t N) {
   const int64_t groups = ceil_div(M, int64_t(8));
-  return groups <= 1 || (groups <= 4 && ceil_div(N, int64_t(256)) * groups * 3 < int64_t(num_sms()) * 4);
+  return groups <= 1 || (groups <= 4 && ceil_div(N, int64_t(256)) * groups * 5 < int64_t(num_sms()) * 6);
 }
 
 te_status launch_dense_few(const GemmArgs& g, cudaStream_t s) {
