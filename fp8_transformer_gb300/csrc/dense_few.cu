@@ -1,21 +1,30 @@
-// The dense layer that ends in the residual stream, for a few tokens (up to 32 rows):
+// The dense layer that ends in the residual stream, for an output of few tiles (decoding, short prompts,
+// narrow layers):
 //   out = a residual + gate act(alpha x W + b)
-// Reading W [K, N] once bounds it, so W goes straight from memory into the registers that the tensor
-// cores read: a lane loads 16 bytes of a row of W at a time (8 bf16 or 16 E4M3 columns; of E4M3 beyond 8
-// tokens 8 bytes, for the registers), four neighbouring rows k .. k + 3 for each step of 16, and pairs
-// two rows' values of a column by byte permutes (E4M3 values become f16, exactly: with mma.sync on E4M3
-// itself, which needs the bytes of four rows together, 17 tokens through [14336, 4096] took 25 us for 21).
-// W is the first operand of mma.sync m16n8k16, so that a product takes two columns of each of the 8 lane
-// groups as its 16 rows and 8 tokens as its columns; which row of W is which k of the product does not
-// matter as long as x is read in the same order.  mma.sync rather than tcgen05: the arithmetic is far
-// from any bound, and no weight passes through shared memory.
+// Reading W [K, N] once bounds it.  The tiles of the batch product (128 tokens x 256 columns, an SM pair to
+// two) leave most SMs idle here.  So W takes the 128-row side of tcgen05.mma and the tokens (rounded up to
+// 32, 64 or 128) its columns, and a cluster splits K: each CTA multiplies its range of K into tensor
+// memory and leaves its partial tile in shared memory, and the CTAs add the partial tiles in rank order
+// through distributed shared memory, each finishing its share of the tile.  No sum depends on timing.
 //
-// A CTA of 8 warps takes the 64 (E4M3 up to 8 tokens: 128) columns of one lane's width, its warps different
-// ranges of K, and a cluster of CTAs the ranges of one block of columns, where the columns alone leave SMs
-// idle.  The partial sums meet in shared memory and over the cluster in a fixed order.  One token through
-// [14336, 4096]: 24 us a call, 4.9 TB/s; about 4 of them are launch, first bytes and the sums' way.
+//   warp 0     TMA producer: a ring of W tiles (as stored, [K, N]: the MMA reads them transposed) and x tiles
+//   warp 1     owns the tensor memory; one thread issues the MMAs
+//   warps 2-9  bring the accumulator to shared memory, a TMEM lane quadrant to two warps
+// and all of them finish the tile.
+// Every wait on an mbarrier is bounded; on expiry a thread records TE_ERR_TIMEOUT, all roles leave their
+// loops, and the CTA goes on to the cluster's barriers without writing results.
+//
+// W [14336, 4096] (us; in brackets the time of its bytes at the measured copy rate): bf16 at 1, 32 and 128
+// tokens 21, 23 and 28 (17.3, 17.5, 18.2); E4M3 13, 15 and 20 (8.7, 8.8, 9.2).  About 4 us of each are the
+// launch, the first bytes and the meeting of the cluster (a [512, 512] layer takes 3.6); from 64 tokens on
+// the x tiles add to the bytes on their way to shared memory and the end sums 8 partial tiles.  A first form,
+// on mma.sync with W in registers, took 23 at one token and 33 at 32 (bf16), 16 and 27 (E4M3).  Starting
+// each block of columns at another place of K, so that they do not all ask for the same x, is slower (13 ->
+// 14 us in E4M3); four places at a time to a thread of the end gains nothing; ten warps for six are 1 to 3
+// us faster from 128 tokens on, whose end is bound by instructions.
+#include <cuda.h>
+
 #include <cstring>
-#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -26,13 +35,27 @@ namespace te {
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
+constexpr int kCols = 128;       // columns of W to a CTA: the MMA's rows
+constexpr int kRowBytes = 128;   // bytes of K (x) or of columns (W) to a row of a tile
+constexpr int kThreads = 320;
+constexpr int kWTile = kCols * kRowBytes;  // 16 KB: 64 (bf16) or 128 (E4M3) rows of W
+constexpr int kPitch = kCols + 4;          // floats from token to token of a partial tile
 constexpr int kMaxCluster = 8;
 
-struct FewArgs {
-  const void* x;
-  const void* w;
+template <bool FP8, int NT>
+struct Form {
+  static constexpr int kK = kRowBytes / (FP8 ? 1 : 2);  // K of a stage
+  static constexpr int kXTile = NT * kRowBytes;
+  static constexpr int kStage = kWTile + kXTile;
+  static constexpr int kStages = 100 * 1024 / kStage;   // two CTAs to an SM
+  static constexpr size_t kRing = size_t(kStages) * kStage;
+  static constexpr size_t kSums = size_t(NT) * kPitch * sizeof(float);
+  static constexpr size_t kSmem = (kRing > kSums ? kRing : kSums) + 1024;  // (the ring starts on 1 KB)
+};
+
+// What ends the layer, for four neighbouring columns of a row to a thread.  (Ordinary loads throughout: the
+// kernel in front may have written any of it.)
+struct End {
   const float* x_scale_inv;
   const float* w_scale_inv;
   const void* bias;
@@ -42,37 +65,66 @@ struct FewArgs {
   void* z;
   float residual_scale;
   int out_dtype, act;
-  int M, N, K, gate_rows;
+  int N, gate_rows, one_gate;
+
+  struct In {
+    uint2 bias, gate;
+    uint4 residual;
+  };
+
+  __device__ __forceinline__ float alpha() const {
+    float a = 1.0f;
+    if (x_scale_inv) a *= *x_scale_inv;
+    if (w_scale_inv) a *= *w_scale_inv;
+    return a;
+  }
+
+  __device__ __forceinline__ In load(int row, int c) const {
+    In in = {};
+    auto bf4 = [](const void* base, int64_t j) {
+      return *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + j);
+    };
+    const int64_t at = int64_t(row) * N + c;
+    if (bias) in.bias = bf4(bias, c);
+    if (gate) in.gate = bf4(gate, int64_t(one_gate ? 0 : row / gate_rows) * N + c);
+    if (out_dtype == TE_BF16) {
+      const uint2 r = bf4(residual, at);
+      in.residual.x = r.x;
+      in.residual.y = r.y;
+    } else {
+      in.residual = *reinterpret_cast<const uint4*>(static_cast<const float*>(residual) + at);
+    }
+    return in;
+  }
+
+  // out = residual_scale * residual + gate * act(alpha v + bias) at columns c .. c + 3 of a row, and z
+  __device__ __forceinline__ void store(int row, int c, float alpha, float (&v)[4], const In& in) const {
+    const int64_t at = int64_t(row) * N + c;
+    const float bb[4] = {bf16_lo(in.bias.x), bf16_hi(in.bias.x), bf16_lo(in.bias.y), bf16_hi(in.bias.y)};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = fmaf(v[k], alpha, bb[k]);
+    if (z)
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(z) + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    const f32x2 v01 = act2(act, f2(v[0], v[1])), v23 = act2(act, f2(v[2], v[3]));
+    float o[4] = {v01.x, v01.y, v23.x, v23.y};
+    if (gate) {
+      o[0] *= bf16_lo(in.gate.x); o[1] *= bf16_hi(in.gate.x);
+      o[2] *= bf16_lo(in.gate.y); o[3] *= bf16_hi(in.gate.y);
+    }
+    if (out_dtype == TE_BF16) {
+      const float rr[4] = {bf16_lo(in.residual.x), bf16_hi(in.residual.x), bf16_lo(in.residual.y), bf16_hi(in.residual.y)};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = fmaf(residual_scale, rr[k], o[k]);
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
+    } else {
+      *reinterpret_cast<float4*>(static_cast<float*>(out) + at) =
+          make_float4(fmaf(residual_scale, __uint_as_float(in.residual.x), o[0]),
+                      fmaf(residual_scale, __uint_as_float(in.residual.y), o[1]),
+                      fmaf(residual_scale, __uint_as_float(in.residual.z), o[2]),
+                      fmaf(residual_scale, __uint_as_float(in.residual.w), o[3]));
+    }
+  }
 };
-
-// Two CTAs to an SM throughout, with as many loads in flight as their registers leave room for (one CTA of
-// twice the registers: 36 to 39 us for 27 to 29, 32 tokens in E4M3 through [14336 to 16384, 4096], and 40
-// for 36, 32 in bf16 through [8192, 8192]).  Staged in shared memory by asynchronous copies instead, which
-// leave room for twice the bytes, one token through [14336, 4096] took 35 us for 24.
-template <bool FP8, int XT>
-struct Form {
-  static constexpr int kWords = FP8 && XT > 1 ? 2 : 4;  // of 4 bytes, of a row of W to a lane
-  static constexpr int kLane = kWords * (FP8 ? 4 : 2);  // columns of them
-  static constexpr int kCols = 8 * kLane;               // of a CTA
-  static constexpr int kPitch = kCols + 4;              // floats from row to row of a partial sum
-  static constexpr int kAhead = XT == 1 ? 4 : XT == 4 ? 2 : FP8 && XT == 2 ? 4 : !FP8 && XT == 3 ? 2 : 3;  // steps in flight
-  static constexpr int kCtas = 2;                       // of an SM
-};
-
-template <bool FP8, int XT>
-constexpr size_t smem_bytes() { return size_t(kWarps / 2) * 8 * XT * Form<FP8, XT>::kPitch * sizeof(float); }
-
-template <bool FP8>
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], const uint32_t (&b)[2]) {
-  if constexpr (FP8)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b[0]), "r"(b[1]));
-}
 
 __device__ __forceinline__ int cluster_ctas() {
   uint32_t n;
@@ -80,210 +132,252 @@ __device__ __forceinline__ int cluster_ctas() {
   return int(n);
 }
 
-// (The kernel starts while the one in front may still write its inputs: ordinary loads throughout, behind
-// the wait.)
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t v) {  // of the low 16 bits
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(uint16_t(v)));
-  return r;
+// Four floats of a CTA of the cluster.  (Volatile, so that it stays behind the
+// cluster's barrier, and no more, so that loads overlap.)
+__device__ __forceinline__ float4 load_cluster4(uint32_t at) {
+  float4 u;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(u.x), "=f"(u.y), "=f"(u.z), "=f"(u.w)
+               : "r"(at));
+  return u;
 }
 
-// x's values of four neighbouring k: two operand registers.
-template <bool FP8>
-struct XFrag {
-  uint2 w;  // bf16: four values; E4M3: four in w.x
-  __device__ __forceinline__ void load(const void* x, int64_t at, bool in) {
-    w = make_uint2(0u, 0u);
-    if (!in) return;
-    if constexpr (FP8) w.x = *reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(x) + at);
-    else w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(x) + at);
-  }
-  __device__ __forceinline__ void get(uint32_t& lo, uint32_t& hi) const {
-    if constexpr (FP8) {
-      lo = e4m3x2_f16x2(w.x);
-      hi = e4m3x2_f16x2(w.x >> 16);
-    } else {
-      lo = w.x;
-      hi = w.y;
-    }
-  }
+struct FewParams {  // aligned like its tensor maps
+  CUtensorMap w;
+  CUtensorMap x;
+  End end;
+  int M, num_kb;
+  int* status;
 };
 
-// XT: groups of 8 tokens.
-template <bool FP8, int XT>
-__global__ void __launch_bounds__(kThreads, Form<FP8, XT>::kCtas) dense_few_kernel(const FewArgs a) {
-  using F = Form<FP8, XT>;
-  constexpr int kAhead = F::kAhead, LW = F::kWords;
-  constexpr int NP = F::kLane / 2;  // products of a step for each group of tokens: a pair of the lane's columns
-  constexpr int ROWS = 8 * XT;
-  extern __shared__ __align__(16) float part[];  // [4][ROWS][kPitch]
-  // launched as a programmatic dependent: nothing is read before the kernel in front has finished
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int g = lane >> 2, t = lane & 3;
+// fp32 accumulator, both operands bf16 or E4M3, A (W) MN-major, B (x) K-major, N >> 3, M >> 4.
+template <bool FP8, int NT>
+__device__ constexpr uint32_t instr_desc() {
+  return (1u << 4) | ((FP8 ? 0u : 1u) << 7) | ((FP8 ? 0u : 1u) << 10) | (1u << 15) | (uint32_t(NT >> 3) << 17) |
+         (uint32_t(kCols >> 4) << 24);
+}
+
+template <bool FP8>
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (FP8)
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+  else
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+                 "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+
+template <bool FP8, int NT>
+__global__ void __launch_bounds__(kThreads, 2) dense_few_kernel(const __grid_constant__ FewParams p) {
+  using F = Form<FP8, NT>;
+  constexpr int STAGES = F::kStages;
+  constexpr uint32_t IDESC = instr_desc<FP8, NT>();
+  constexpr int MMA_K = 32 / (FP8 ? 1 : 2);  // K of one instruction
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+  float* part = reinterpret_cast<float*>(smem);
+  __shared__ uint64_t full[STAGES], empty[STAGES], done;
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int ranks = cluster_ctas(), rank = int(cluster_rank());
-  const int col0 = int(blockIdx.x) / ranks * F::kCols;
-  const int col = col0 + g * F::kLane;  // the lane's columns (N is a multiple of 16: all of them or none)
-  const bool in = col < a.N;
-  const int steps = a.K / 16, share = ranks * kWarps, id = rank * kWarps + warp;
-  const int s0 = int(int64_t(steps) * id / share), s1 = int(int64_t(steps) * (id + 1) / share);
-  constexpr int es = FP8 ? 1 : 2;
-  const size_t row_bytes = size_t(a.N) * es;
-  const uint8_t* wp = static_cast<const uint8_t*>(a.w) + (size_t(s0) * 16 + 4 * t) * row_bytes + size_t(col) * es;
-  uint32_t w[kAhead][4][LW];
-  XFrag<FP8> x[kAhead][XT];
-  auto load = [&](int s, int b) {
-    const uint8_t* p = wp + size_t(s - s0) * 16 * row_bytes;
-    const bool here = s < s1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      using V = std::conditional_t<LW == 4, uint4, uint2>;
-      V v{};
-      if (here && in) v = *reinterpret_cast<const V*>(p + i * row_bytes);
-      memcpy(w[b][i], &v, sizeof(V));
+  const int col0 = int(blockIdx.x) / ranks * kCols;
+  const int row0 = int(blockIdx.y) * NT, rows = p.M - row0 < NT ? p.M - row0 : NT;
+  const int kb0 = int(int64_t(p.num_kb) * rank / ranks), kb1 = int(int64_t(p.num_kb) * (rank + 1) / ranks);
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
     }
+    mbar_init(smem_u32(&done), 1);
+    abort_flag = 0;
+    mbar_init_fence();
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.w)) : "memory");
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&p.x)) : "memory");
+  }
+  // Launched as a programmatic dependent: nothing is read before the kernel in front has finished.  Nor is
+  // tensor memory taken before that, which the kernel in front may still have to allocate, and the next
+  // kernel, which may take some before it waits, is let in after.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  auto issue = [&](int kb, int stage) {
+    const uint32_t bar = smem_u32(&full[stage]);
+    const uint32_t w_dst = smem_u32(smem + stage * F::kStage);
+    mbar_expect_tx(bar, F::kStage);
 #pragma unroll
-    for (int r = 0; r < XT; ++r) {
-      const int row = g + 8 * r;
-      x[b][r].load(a.x, int64_t(row) * a.K + s * 16 + 4 * t, here && row < a.M);
-    }
+    for (int i = 0; i < kCols / F::kK; ++i)
+      tma_load_2d(w_dst + i * F::kK * kRowBytes, &p.w, bar, col0 + i * F::kK, kb * F::kK);
+    tma_load_2d(w_dst + kWTile, &p.x, bar, kb * F::kK, row0);
   };
-  float acc[XT][NP][4];
-#pragma unroll
-  for (int m = 0; m < XT; ++m)
-#pragma unroll
-    for (int j = 0; j < NP; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[m][j][c] = 0.0f;
-#pragma unroll
-  for (int b = 0; b < kAhead; ++b) load(s0 + b, b);
-  for (int s = s0; s < s1; s += kAhead) {
-#pragma unroll
-    for (int b = 0; b < kAhead; ++b) {
-      uint32_t xb[XT][2];
-#pragma unroll
-      for (int m = 0; m < XT; ++m) x[b][m].get(xb[m][0], xb[m][1]);
-      const auto &r0 = w[b][0], &r1 = w[b][1], &r2 = w[b][2], &r3 = w[b][3];
-#pragma unroll
-      for (int q = 0; q < LW; ++q) {
-        if constexpr (FP8) {
-          const uint32_t lo[2] = {__byte_perm(r0[q], r1[q], 0x5140), __byte_perm(r0[q], r1[q], 0x7362)};
-          const uint32_t hi[2] = {__byte_perm(r2[q], r3[q], 0x5140), __byte_perm(r2[q], r3[q], 0x7362)};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t wa[4] = {e4m3x2_f16x2(lo[j]), e4m3x2_f16x2(lo[j] >> 16), e4m3x2_f16x2(hi[j]),
-                                    e4m3x2_f16x2(hi[j] >> 16)};
-#pragma unroll
-            for (int m = 0; m < XT; ++m) mma<FP8>(acc[m][2 * q + j], wa, xb[m]);
-          }
-        } else {
-          const uint32_t wa[4] = {__byte_perm(r0[q], r1[q], 0x5410), __byte_perm(r0[q], r1[q], 0x7632),
-                                  __byte_perm(r2[q], r3[q], 0x5410), __byte_perm(r2[q], r3[q], 0x7632)};
-#pragma unroll
-          for (int m = 0; m < XT; ++m) mma<FP8>(acc[m][q], wa, xb[m]);
+  const int first = kb1 - kb0 < STAGES ? kb1 - kb0 : STAGES;  // tiles that fill the ring
+  if (threadIdx.x == 0)  // (its own barriers: the others have yet to see them)
+    for (int s = 0; s < first; ++s) issue(kb0 + s, s);
+  __syncwarp();
+  if (warp == 1) tmem_alloc<1>(smem_u32(&tmem_slot), NT);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, last_parity = 0;  // of the tile last brought to each stage
+      for (int kb = kb0 + first; kb < kb1; ++kb) {
+        if (!mbar_try_wait(smem_u32(&empty[stage]), phase) &&
+            !wait_bounded(smem_u32(&empty[stage]), phase, &abort_flag, p.status, kWaitLimitNs, true))
+          break;
+        issue(kb, stage);
+        last_parity = (last_parity & ~(1u << stage)) | ((phase ^ 1) << stage);
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
         }
       }
-      load(s + b + kAhead, b);
+      // copies in flight land before the CTA goes on (without a failure they all have)
+      for (int s = 0; s < first; ++s)
+        wait_bounded(smem_u32(&full[s]), (last_parity >> s) & 1, &abort_flag, p.status, kDrainLimitNs, false);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_try_wait(smem_u32(&full[stage]), phase) &&
+            !wait_bounded(smem_u32(&full[stage]), phase, &abort_flag, p.status, kWaitLimitNs, true))
+          break;
+        tc_fence_after();
+        const uint32_t w_base = smem_u32(smem + stage * F::kStage), x_base = w_base + kWTile;
+#pragma unroll
+        for (int j = 0; j < kRowBytes / 32; ++j)
+          mma<FP8>(tmem, smem_desc(w_base + j * MMA_K * kRowBytes, F::kK * kRowBytes, 8 * kRowBytes),
+                   smem_desc(x_base + j * 32, 16, 8 * kRowBytes), IDESC, (kb != kb0 || j != 0) ? 1u : 0u);
+        umma_commit<1>(smem_u32(&empty[stage]));
+        if (++stage == STAGES) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      umma_commit<1>(smem_u32(&done));  // every MMA issued so far
+      wait_bounded(smem_u32(&done), 0, &abort_flag, p.status, kWaitLimitNs, false);
+    }
+  } else {
+    int ok = 1;
+    if (lane == 0) ok = wait_bounded(smem_u32(&done), 0, &abort_flag, p.status, kWaitLimitNs, true) ? 1 : 0;
+    ok = __shfl_sync(0xffffffffu, ok, 0);
+    if (ok) {
+      while (!mbar_try_wait(smem_u32(&done), 0)) {  // it has completed: every lane observes it
+      }
+      __syncwarp();
+      tc_fence_after();
+      const int quad = warp & 3;
+      // (the ring is no longer read: its copies have landed and its MMAs are done)
+#pragma unroll 1
+      for (int c = (warp - 2) / 4 * 32; c < NT && c < rows; c += (kThreads / 32 - 2) / 4 * 32) {
+        uint32_t r[32];
+        tmem_ld32(tmem + (uint32_t(quad * 32) << 16) + uint32_t(c), r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) part[(c + j) * kPitch + quad * 32 + lane] = __uint_as_float(r[j]);
+      }
+      tc_fence_before();
     }
   }
-  // The lane's sums: of tokens 2 t and 2 t + 1 (of each group), product j gives its columns 2 j (c = 0, 1)
-  // and 2 j + 1 (c = 2, 3).  The upper warps' first, then each lower warp's with its upper one's added.
-  auto slab = [&](int s, int row, int c) { return part + (size_t(s) * ROWS + row) * F::kPitch + c; };
-  auto rows_of = [&](auto&& f) {
-#pragma unroll
-    for (int m = 0; m < XT; ++m)
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int j = 0; j < NP; j += 2) {
-          float* p = slab(warp & 3, 8 * m + 2 * t + e, g * F::kLane + 2 * j);
-          f(reinterpret_cast<float4*>(p), acc[m][j][e], acc[m][j][2 + e], acc[m][j + 1][e], acc[m][j + 1][2 + e]);
-        }
-  };
-  if (warp >= 4) rows_of([](float4* p, float u, float v, float y, float z) { *p = make_float4(u, v, y, z); });
   __syncthreads();
-  if (warp < 4)
-    rows_of([](float4* p, float u, float v, float y, float z) {
-      const float4 o = *p;
-      *p = make_float4(u + o.x, v + o.y, y + o.z, z + o.w);
-    });
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, NT);
+  }
+  // Four neighbouring columns of a row to a thread at a time.  What the end reads besides the sums is on its
+  // way while the cluster meets, and then while the place in front is written.
+  constexpr int kQuads = kCols / 4;
+  static_assert(kThreads % kQuads == 0, "a thread's columns stay the same");
+  const float alpha = p.end.alpha();
+  const int c = int(threadIdx.x) % kQuads * 4, step = ranks * (kThreads / kQuads);
+  int row = (rank * kThreads + int(threadIdx.x)) / kQuads;
+  if (col0 + c >= p.end.N) row = rows;
+  End::In in = {};
+  if (row < rows) in = p.end.load(row0 + row, col0 + c);
+  __syncwarp();
   if (ranks > 1) cluster_sync();
-  else __syncthreads();
-  float alpha = 1.0f;
-  if (a.x_scale_inv) alpha *= *a.x_scale_inv;
-  if (a.w_scale_inv) alpha *= *a.w_scale_inv;
-  // four neighbouring columns of a row to a thread of the cluster
-  for (int i = rank * kThreads + int(threadIdx.x); i < a.M * (F::kCols / 4); i += ranks * kThreads) {
-    const int row = i / (F::kCols / 4), c = i % (F::kCols / 4) * 4;
-    if (col0 + c >= a.N) continue;
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int r = 0; r < ranks; ++r) {
+  if (!abort_flag) {
+    uint32_t sums[kMaxCluster];
 #pragma unroll
-      for (int s = 0; s < kWarps / 2; ++s) {
-        float4 p;
-        asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
-                     : "=f"(p.x), "=f"(p.y), "=f"(p.z), "=f"(p.w)
-                     : "r"(map_to_rank(smem_u32(slab(s, row, c)), uint32_t(r)))
-                     : "memory");
-        v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
+    for (int r = 0; r < kMaxCluster; ++r)
+      sums[r] = map_to_rank(smem_u32(part + row * kPitch + c), uint32_t(r < ranks ? r : rank));
+    while (row < rows) {
+      float4 u[kMaxCluster];
+#pragma unroll
+      for (int r = 0; r < kMaxCluster; ++r) {
+        u[r] = r < ranks ? load_cluster4(sums[r]) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        sums[r] += uint32_t(step * kPitch * sizeof(float));
       }
-    }
-    const int64_t at = int64_t(row) * a.N + col0 + c;
-    auto bf4 = [](const void* base, int64_t j) {
-      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + j);
-      return make_float4(bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y));
-    };
-    const float4 b = a.bias ? bf4(a.bias, col0 + c) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float bb[4] = {b.x, b.y, b.z, b.w};
+      float v[4] = {u[0].x, u[0].y, u[0].z, u[0].w};
 #pragma unroll
-    for (int k = 0; k < 4; ++k) v[k] = fmaf(v[k], alpha, bb[k]);
-    if (a.z)
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.z) + at) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
-    const f32x2 v01 = act2(a.act, f2(v[0], v[1])), v23 = act2(a.act, f2(v[2], v[3]));
-    float o[4] = {v01.x, v01.y, v23.x, v23.y};
-    if (a.gate) {
-      const float4 q = bf4(a.gate, int64_t(row / a.gate_rows) * a.N + col0 + c);
-      o[0] *= q.x; o[1] *= q.y; o[2] *= q.z; o[3] *= q.w;
-    }
-    if (a.out_dtype == TE_BF16) {
-      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(a.residual) + at);
-      const float r[4] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = fmaf(a.residual_scale, r[k], o[k]);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) = make_uint2(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]));
-    } else {
-      const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(a.residual) + at);
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) =
-          make_float4(fmaf(a.residual_scale, r.x, o[0]), fmaf(a.residual_scale, r.y, o[1]),
-                      fmaf(a.residual_scale, r.z, o[2]), fmaf(a.residual_scale, r.w, o[3]));
+      for (int r = 1; r < kMaxCluster; ++r) {
+        v[0] += u[r].x; v[1] += u[r].y; v[2] += u[r].z; v[3] += u[r].w;
+      }
+      const End::In now = in;
+      const int at = row0 + row;
+      row += step;
+      if (row < rows) in = p.end.load(row0 + row, col0 + c);
+      p.end.store(at, col0 + c, alpha, v, now);
     }
   }
   __syncwarp();
   if (ranks > 1) cluster_sync();  // no CTA leaves while another reads its sums
 }
 
-template <bool FP8, int XT>
-te_status launch(const FewArgs& f, cudaStream_t s) {
-  constexpr size_t smem = smem_bytes<FP8, XT>();
+// Tokens of a tile.
+int tile_tokens(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+
+// CTAs to a tile: up to one CTA an SM in all as long as each has a stage of K, and up to two, which an SM
+// holds at once, while each has 8 (in all 7 / 8 of them: clusters do not fill every SM of a GPC).  (us, two /
+// one CTA an SM: [14336, 4096] in bf16 at one token 20.4 / 21.7, at 128 27.5 / 33.8; with 2 stages instead
+// of 8 [2048, 4096] in E4M3 goes from 5.1 to 5.8.  [4096, 9728] in E4M3 at 128 tokens, all of two CTAs an SM /
+// half of them: 26 / 21.)
+int cluster_of(int64_t tiles, int64_t num_kb) {
+  const int64_t sms = num_sms();
+  int ranks = 1;
+  while (ranks < kMaxCluster && num_kb >= ranks * 2) {
+    const int64_t ctas = tiles * ranks * 2;
+    if (ctas > sms && (ctas * 4 > sms * 7 || num_kb < ranks * 2 * 8)) break;
+    ranks *= 2;
+  }
+  return ranks;
+}
+
+template <bool FP8, int NT>
+te_status launch(const GemmArgs& g, cudaStream_t s) {
+  using F = Form<FP8, NT>;
   static PerDevice<bool> attr_done;
   bool ok = false;
   if (!attr_done.get(&ok, [](bool* v) {
-        *v = cudaFuncSetAttribute(dense_few_kernel<FP8, XT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)) ==
-             cudaSuccess;
+        *v = cudaFuncSetAttribute(dense_few_kernel<FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  int(F::kSmem)) == cudaSuccess;
         return *v;
       }))
     return TE_ERR_CUDA;
-  // CTAs to a block of columns: as many as keep every SM at the CTAs it holds at once, while each warp has
-  // a round of loads to itself
-  const int blocks = int(ceil_div(f.N, int64_t(Form<FP8, XT>::kCols)));
-  const int64_t room = int64_t(num_sms()) * Form<FP8, XT>::kCtas;
-  int ranks = 1;
-  while (ranks < kMaxCluster && int64_t(blocks) * ranks * 2 <= room && f.K / 16 >= ranks * 2 * kWarps) ranks *= 2;
+  FewParams p;
+  memset(&p, 0, sizeof(p));
+  const int dt = FP8 ? TE_E4M3 : TE_BF16;
+  if (!make_tmap_2d(&p.w, g.B, dt, g.N, g.K, F::kK, F::kK, 128) || !make_tmap_2d(&p.x, g.A, dt, g.K, g.M, F::kK, NT, 128))
+    return TE_ERR_CUDA;
+  p.end = End{g.a_scale_inv, g.b_scale_inv, g.bias, g.gate, g.residual, g.D, g.saved_h, g.residual_scale,
+              g.cast.out_dtype, g.act, int(g.N), int(g.gate_rows), g.gate_rows == g.M};
+  p.M = int(g.M);
+  p.num_kb = int(ceil_div(g.K, int64_t(F::kK)));
+  p.status = device_status_ptr();
+  const int blocks = int(ceil_div(g.N, int64_t(kCols)));
+  const int rows = int(ceil_div(g.M, int64_t(NT)));
+  const int ranks = cluster_of(int64_t(blocks) * rows, p.num_kb);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(blocks * ranks));
+  cfg.gridDim = dim3(unsigned(blocks * ranks), unsigned(rows));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.dynamicSmemBytes = F::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -294,49 +388,34 @@ te_status launch(const FewArgs& f, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, dense_few_kernel<FP8, XT>, f) == cudaSuccess ? TE_OK : TE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, dense_few_kernel<FP8, NT>, p) == cudaSuccess ? TE_OK : TE_ERR_CUDA;
 }
 
 }  // namespace
 
-// Up to 8 rows always.  Each further group of 8 repeats the products of every weight, while the tiles of
-// launch_gemm (256 columns wide, 128 rows high) cost the same for 1 row and for 128 and gain with their
-// number: from about 6 / 5 tiles and groups an SM on they are faster.  Measured (us, here / tiles), bf16,
-// K = 4096: N = 28672 (112 tiles) 48 / 62 at 8 rows, 55 / 44 at 16; N = 14336 (56) 28 / 38 at 16, 36 / 38
-// at 32; K = 14336, N = 4096 (16) 24 / 55 at one row, 33 / 55 at 32.  E4M3 likewise: 27 / 34, 37 / 35;
-// 20 / 25, 28 / 25; 17 / 40, 27 / 40.
-bool dense_few_serves(int64_t M, int64_t N) {
-  const int64_t groups = ceil_div(M, int64_t(8));
-  return groups <= 1 || (groups <= 4 && ceil_div(N, int64_t(256)) * groups * 5 < int64_t(num_sms()) * 6);
+// Up to 32 tokens always; up to 64 with at most 3 / 2 tiles an SM; and with more where a tile's K is split
+// (half a tile an SM, or 7 / 8 with K of 16 stages).  Behind that the batch product's tiles, whose loads serve
+// twice the columns, are faster.  Measured (us, here / there):
+//   [14336, 4096]  128 tokens bf16 28 / 58, E4M3 20 / 43; 256: 36 / 49, 24 / 39; 512: 59 / 58, 36 / 41
+//   [4096, 14336]  1: 23 / 38, 14 / 27; 64: 25 / 39, 17 / 23; 128: 31 / 42, 22 / 26
+//   [4096, 28672]  1: 41 / 64, 23 / 35; 64: 43 / 45, 27 / 28; 128 (there): 57 / 49, 40 / 31
+//   [4096, 57344]  1: 74 / 104, 41 / 54; 32: 81 / 86, 49 / 48
+//   [1024, 1024]   1024: 13 / 15, 11 / 12;  [4096, 512]  2048: 18 / 29, 14 / 19
+bool dense_few_serves(int64_t M, int64_t N, int64_t K, int ab_dtype) {
+  const int nt = tile_tokens(M);
+  const int64_t tiles = ceil_div(N, int64_t(kCols)) * ceil_div(M, int64_t(nt)), sms = num_sms();
+  if (nt == 32 || tiles * 2 <= sms * (nt == 64 ? 3 : 1)) return true;
+  return cluster_of(tiles, ceil_div(K, int64_t(kRowBytes / (ab_dtype == TE_E4M3 ? 1 : 2)))) > 1;
 }
 
 te_status launch_dense_few(const GemmArgs& g, cudaStream_t s) {
   if (g.M == 0) return TE_OK;
-  if (g.M > 32 || g.epilogue != EPI_RESIDUAL || g.N > (1 << 30) || g.K > (1 << 30)) return TE_ERR_UNSUPPORTED;
+  if (g.epilogue != EPI_RESIDUAL || !dense_few_serves(g.M, g.N, g.K, g.ab_dtype)) return TE_ERR_UNSUPPORTED;
   ProfileScope prof(TE_KERNEL_GEMM_ACT, s);
-  FewArgs f;
-  f.x = g.A;
-  f.w = g.B;
-  f.x_scale_inv = g.a_scale_inv;
-  f.w_scale_inv = g.b_scale_inv;
-  f.bias = g.bias;
-  f.gate = g.gate;
-  f.residual = g.residual;
-  f.out = g.D;
-  f.z = g.saved_h;
-  f.residual_scale = g.residual_scale;
-  f.out_dtype = g.cast.out_dtype;
-  f.act = g.act;
-  f.M = int(g.M);
-  f.N = int(g.N);
-  f.K = int(g.K);
-  f.gate_rows = int(g.gate_rows);
-  const int groups = int(ceil_div(g.M, int64_t(8)));
+  const int nt = tile_tokens(g.M);
   if (g.ab_dtype == TE_E4M3)
-    return groups == 1 ? launch<true, 1>(f, s) : groups == 2 ? launch<true, 2>(f, s)
-           : groups == 3 ? launch<true, 3>(f, s) : launch<true, 4>(f, s);
-  return groups == 1 ? launch<false, 1>(f, s) : groups == 2 ? launch<false, 2>(f, s)
-         : groups == 3 ? launch<false, 3>(f, s) : launch<false, 4>(f, s);
+    return nt == 32 ? launch<true, 32>(g, s) : nt == 64 ? launch<true, 64>(g, s) : launch<true, 128>(g, s);
+  return nt == 32 ? launch<false, 32>(g, s) : nt == 64 ? launch<false, 64>(g, s) : launch<false, 128>(g, s);
 }
 
 }  // namespace te

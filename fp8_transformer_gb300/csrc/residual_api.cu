@@ -70,7 +70,7 @@ te_status zero(void* p, size_t bytes, cudaStream_t s) {
 }
 
 size_t dense_fwd_workspace(int64_t M, int64_t K, int64_t N, int dtype) {
-  return dense_few_serves(M, N) ? 0 : gemm_split_workspace(M, N, K, dtype, EPI_RESIDUAL);
+  return dense_few_serves(M, N, K, dtype) ? 0 : gemm_split_workspace(M, N, K, dtype, EPI_RESIDUAL);
 }
 
 struct DenseBwdLayout {
@@ -382,7 +382,7 @@ te_status te_dense_residual_fwd(const void* x, const void* kernel, te_dtype dtyp
   g.cast.out_dtype = residual_dtype;
   g.split_ws = workspace;
   g.split_ws_bytes = used;
-  return dense_few_serves(M, N) ? launch_dense_few(g, as_stream(stream)) : launch_gemm(g, as_stream(stream));
+  return dense_few_serves(M, N, K, dtype) ? launch_dense_few(g, as_stream(stream)) : launch_gemm(g, as_stream(stream));
 }
 
 size_t te_dense_residual_bwd_workspace(int64_t M, int64_t K, int64_t N, int64_t gates, te_dtype dtype) {

@@ -139,6 +139,88 @@ def test_rows_do_not_touch_one_another(M):
         assert torch.equal(out[:M - 1], got[:M - 1])
 
 
+# outputs of many tiles, which the batch product's kernel makes whatever K is
+MANY = [(257, 80, 16384), (2500, 96, 1040), (70, 64, 28672), (5000, 16, 528), (1300, 1040, 2064), (4099, 128, 592)]
+
+
+@pytest.mark.parametrize("M,K,N", MANY)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rt", [BF, F32])
+def test_forward_many_tiles(M, K, N, fp8, rt):
+    i = MANY.index((M, K, N))
+    act = ["gelu", "identity", "relu", "silu"][i % 4]
+    t, _ = draw(M, K, N, fp8, [1, 4, 0, 8, 13, 0][i], bias=i % 2 == 0, rt=rt)
+    out, z = run_fwd(t, act, 0.5, save=i % 3 != 2)
+    check_fwd(t, act, 0.5, out, z)
+    r = t["residual"].clone()
+    again, _ = run_fwd(t, act, 0.5, out=r, residual=r)
+    assert torch.equal(out, again)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        t["x"][M - 1] = float("nan")
+        other, _ = run_fwd(t, act, 0.5)
+    s.synchronize()
+    assert torch.equal(out[:M - 1], other[:M - 1]) and (act == "relu" or bool(torch.isnan(other[M - 1]).all()))
+
+
+# outputs of few tiles: every width of a tile, ends of K inside a stage, clusters of one to eight
+FEW = [(32, 16, 16), (32, 16400, 144), (33, 80, 1040), (48, 1168, 272), (64, 4112, 128), (63, 128, 19456), (65, 16, 4096),
+       (96, 2064, 2064), (128, 14336, 144), (127, 256, 9600), (129, 640, 400), (255, 4112, 272), (700, 208, 160),
+       (1025, 1024, 1024), (2000, 48, 16)]
+
+
+@pytest.mark.parametrize("M,K,N", FEW)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("rt", [BF, F32])
+def test_forward_few_tiles(M, K, N, fp8, rt):
+    i = FEW.index((M, K, N))
+    act = ["silu", "gelu", "identity", "relu"][i % 4]
+    t, _ = draw(M, K, N, fp8, [0, 1, M][i % 3], bias=i % 2 == 0, rt=rt)
+    out, z = run_fwd(t, act, 0.5, save=i % 3 != 2)
+    check_fwd(t, act, 0.5, out, z)
+    for _ in range(3):  # the same sums in the same order every time
+        r = t["residual"].clone()
+        again, _ = run_fwd(t, act, 0.5, out=r, residual=r)
+        assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("M", [20, 50, 120, 300])
+def test_layers_one_after_another(M):
+    """Each layer may start while the one in front ends: a chain of few tiles, of many tiles, and a norm between
+    them gives what the layers give one by one."""
+    t, n = draw(M, 1024, 1024, False, 1)
+    wide, back = n(1024, 28672, std=0.03), n(28672, 1024, std=0.01)
+    r_wide = n(M, 28672)
+    gamma, beta = n(1024, std=0.1, mean=1.0), n(1024, std=0.1)
+
+    def chain(wait):
+        x = t["x"]
+        for _ in range(4):
+            for w, r in ((t["w"], t["residual"]), (wide, r_wide), (back, t["residual"])):
+                out = torch.empty_like(r)
+                te.te_dense_residual_fwd(x, w, r, out, activation="silu", residual_scale=0.5)
+                wait()
+                x = out
+            out, ln = torch.empty_like(x), torch.empty_like(x)
+            te.te_residual_norm_fwd(x, t["residual"], gamma, beta, out, ln)
+            wait()
+            x = ln
+        return x
+
+    want = chain(torch.cuda.synchronize)
+    for _ in range(5):
+        assert torch.equal(chain(lambda: None), want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = chain(lambda: None)
+    for _ in range(3):
+        got.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 # ------------------------------------------------------------------------------- backward ---
 
 
