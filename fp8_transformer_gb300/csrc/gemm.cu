@@ -108,6 +108,7 @@ struct GemmDev {
   float* out_scale_inv;
   float* amax_out;
   int* status;
+  int order;
   // The tiles after the first `full_tiles` (the last, partial wave) are split along K into
   // `split` chunks of `kb_chunk` k-blocks; chunks 0 .. split-2 leave their raw accumulators in
   // `partials` and count themselves in `flags` (zeroed before the launch); the last chunk's
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   constexpr uint32_t IDESC = instr_desc<KIND, CG>(A_KMAJOR ? 0 : 1, B_KMAJOR ? 0 : 1);
   const GemmDev& g = p.g;
   // the kernel after this one may launch its setup now (it waits for this grid's completion)
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (g.order != PRODUCT_BEFORE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -530,7 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
   const uint32_t tmem_base = *tmem_slot;
   // Launched as a programmatic dependent of the kernel before it: the setup above overlapped
   // that kernel's tail; nothing it writes (the A operand, the scales) is read before this wait.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // The second of two products reads nothing of the first's, which lets it in only when all that stands
+  // before the first has ended: its CTAs start on the SMs that the first's last wave leaves idle.
+  if (g.order != PRODUCT_BESIDE) asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (g.order == PRODUCT_BEFORE) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     // ----------------------------------------------------------- TMA producer -----------
@@ -839,6 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_kernel(const __grid_constant
     tc_fence_after();
     tmem_dealloc<CG>(tmem_base, kTmemCols);
   }
+  // what comes after this grid comes after the one beside it as well
+  if (g.order == PRODUCT_BESIDE) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 // ------------------------------------------------------------------ host side -------------
@@ -1081,6 +1087,8 @@ te_status launch_gemm(const GemmArgs& a, cudaStream_t s) {
     g.flags = reinterpret_cast<int*>(static_cast<char*>(a.split_ws) + sp.partial_bytes);
     if (cudaMemsetAsync(g.flags, 0, sp.flag_bytes, s) != cudaSuccess) return TE_ERR_CUDA;
   }
+  // (behind the clearing of its flags a second product waits like any other)
+  g.order = sp.split > 1 && a.order == PRODUCT_BESIDE ? int(PRODUCT_ALONE) : a.order;
   const int64_t items = sp.full_tiles + (tiles - sp.full_tiles) * sp.split;
   const int grid = int(items < slots ? items : slots) * cg;
   ProfileScope prof(a.epilogue == EPI_BIAS ? TE_KERNEL_GEMM : TE_KERNEL_GEMM_ACT, s);

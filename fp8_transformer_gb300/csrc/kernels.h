@@ -253,6 +253,14 @@ te_status launch_update_scales(const ScaleUpdateArgs& a, cudaStream_t s);
 // stored [K, N], bf16 or E4M3.
 enum Epilogue { EPI_BIAS = 0, EPI_BIAS_ACT = 1, EPI_BIAS_GATED = 2, EPI_RESIDUAL = 3 };
 
+// Two products in a row of which the second reads nothing that the first writes.  (Neither may write what the
+// other reads or writes; a second product that splits along K clears its flags behind the first and waits.)
+enum GemmOrder {
+  PRODUCT_ALONE = 0,
+  PRODUCT_BEFORE = 1,  // the first: lets the second in
+  PRODUCT_BESIDE = 2,  // the second: starts while the first ends
+};
+
 struct GemmArgs {
   const void* A = nullptr;
   const void* B = nullptr;
@@ -280,6 +288,7 @@ struct GemmArgs {
   // no tile is split.
   void* split_ws = nullptr;
   size_t split_ws_bytes = 0;
+  int order = PRODUCT_ALONE;
 };
 te_status launch_gemm(const GemmArgs& g, cudaStream_t s);
 // Bytes of split_ws that launch_gemm would use for this GEMM on the current device (0: none).

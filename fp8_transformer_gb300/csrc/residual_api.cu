@@ -481,6 +481,7 @@ te_status te_dense_residual_bwd(const void* dout, te_dtype residual_dtype, const
   g.D = dx;
   g.cast.out_dtype = TE_BF16;
   give_split(g, L.split, workspace, ws_bytes);
+  g.order = PRODUCT_BEFORE;
   st = launch_gemm(g, s);
   if (st != TE_OK) return st;
   GemmArgs h;  // dkernel = x^T dz, the contraction over the rows
@@ -497,6 +498,7 @@ te_status te_dense_residual_bwd(const void* dout, te_dtype residual_dtype, const
   h.D = dkernel;
   h.cast.out_dtype = TE_BF16;
   give_split(h, L.split, workspace, ws_bytes);
+  h.order = PRODUCT_BESIDE;
   return launch_gemm(h, s);
 }
 

@@ -336,6 +336,51 @@ def test_no_rows():
     assert all(bool((v == 0).all()) for v in (dk, db, dg))
 
 
+# (the last three split the first product, the second and neither along K)
+BESIDE = [(1, 64, 64), (130, 1024, 1024), (2100, 2048, 1040), (300, 64, 16384), (17000, 64, 256), (700, 8192, 272)]
+
+
+@pytest.mark.parametrize("M,K,N", BESIDE)
+@pytest.mark.parametrize("fp8", [False, True])
+def test_backward_products_beside_one_another(M, K, N, fp8):
+    """The second product of a call starts while the first ends, and the next call reuses the workspace: calls on
+    two sets of inputs in turn, without a wait, give what each gives by itself, eager and from a graph."""
+    sets = []
+    for k in range(2):
+        t, n = draw(M, K, N, fp8, 1, seed=k)
+        t["dout"] = n(M, N)
+        _, z = run_fwd(t, "gelu", 1.0)
+        sets.append((t, n, z, te.Quantizer(40.0, mode="current") if fp8 else None))
+
+    def call(k):
+        t, n, z, q = sets[k]
+        return bwd(t, n, "gelu", 1.0, z, q=q)[1]
+
+    want = []
+    for k in range(2):
+        want.append(call(k))
+        torch.cuda.synchronize()
+    t, _, z, q = sets[1]
+    check_bwd(t, "gelu", 1.0, z, t["dout"], want[1], q)
+    got = [call(i % 2) for i in range(8)]
+    # what follows on the stream sees both products' results
+    sums = [o["dx"].double().sum() + o["dkernel"].double().sum() for o in got]
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert all(torch.equal(o[name], want[i % 2][name]) for name in o if o[name] is not None)
+        assert sums[i] == want[i % 2]["dx"].double().sum() + want[i % 2]["dkernel"].double().sum()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = [call(i % 2) for i in range(4)]
+    for _ in range(3):
+        for o in out:
+            o["dx"].zero_(), o["dkernel"].zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    for i, o in enumerate(out):
+        assert all(torch.equal(o[name], want[i % 2][name]) for name in o if o[name] is not None)
+
+
 @pytest.mark.parametrize("M", [1, 12, 200])
 def test_streams_and_graphs(M):
     t, n = draw(M, 2048, 512, False, 1)
