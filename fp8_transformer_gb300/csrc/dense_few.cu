@@ -1,6 +1,7 @@
 // The dense layer that ends in the residual stream, for an output of few tiles (decoding, short prompts,
 // narrow layers):
 //   out = a residual + gate act(alpha x W + b)
+// and its gradient dx = alpha dz W^T (the same kernel with W's rows for columns and nothing to join).
 // Reading W [K, N] once bounds it.  The tiles of the batch product (128 tokens x 256 columns, an SM pair to
 // two) leave most SMs idle here.  So W takes the 128-row side of tcgen05.mma and the tokens (rounded up to
 // 32, 64 or 128) its columns, and a cluster splits K: each CTA multiplies its range of K into tensor
@@ -87,6 +88,7 @@ struct End {
     const int64_t at = int64_t(row) * N + c;
     if (bias) in.bias = bf4(bias, c);
     if (gate) in.gate = bf4(gate, int64_t(one_gate ? 0 : row / gate_rows) * N + c);
+    if (!residual) return in;
     if (out_dtype == TE_BF16) {
       const uint2 r = bf4(residual, at);
       in.residual.x = r.x;
@@ -150,10 +152,10 @@ struct FewParams {  // aligned like its tensor maps
   int* status;
 };
 
-// fp32 accumulator, both operands bf16 or E4M3, A (W) MN-major, B (x) K-major, N >> 3, M >> 4.
-template <bool FP8, int NT>
+// fp32 accumulator, both operands bf16 or E4M3, A (W) MN-major or, for W^T, K-major, B (x) K-major, N >> 3, M >> 4.
+template <bool FP8, int NT, bool WT>
 __device__ constexpr uint32_t instr_desc() {
-  return (1u << 4) | ((FP8 ? 0u : 1u) << 7) | ((FP8 ? 0u : 1u) << 10) | (1u << 15) | (uint32_t(NT >> 3) << 17) |
+  return (1u << 4) | ((FP8 ? 0u : 1u) << 7) | ((FP8 ? 0u : 1u) << 10) | ((WT ? 0u : 1u) << 15) | (uint32_t(NT >> 3) << 17) |
          (uint32_t(kCols >> 4) << 24);
 }
 
@@ -169,11 +171,11 @@ __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t
                  "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
 }
 
-template <bool FP8, int NT>
+template <bool FP8, int NT, bool WT>
 __global__ void __launch_bounds__(kThreads, 2) dense_few_kernel(const __grid_constant__ FewParams p) {
   using F = Form<FP8, NT>;
   constexpr int STAGES = F::kStages;
-  constexpr uint32_t IDESC = instr_desc<FP8, NT>();
+  constexpr uint32_t IDESC = instr_desc<FP8, NT, WT>();
   constexpr int MMA_K = 32 / (FP8 ? 1 : 2);  // K of one instruction
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -205,9 +207,13 @@ __global__ void __launch_bounds__(kThreads, 2) dense_few_kernel(const __grid_con
     const uint32_t bar = smem_u32(&full[stage]);
     const uint32_t w_dst = smem_u32(smem + stage * F::kStage);
     mbar_expect_tx(bar, F::kStage);
+    if constexpr (WT) {
+      tma_load_2d(w_dst, &p.w, bar, kb * F::kK, col0);
+    } else {
 #pragma unroll
-    for (int i = 0; i < kCols / F::kK; ++i)
-      tma_load_2d(w_dst + i * F::kK * kRowBytes, &p.w, bar, col0 + i * F::kK, kb * F::kK);
+      for (int i = 0; i < kCols / F::kK; ++i)
+        tma_load_2d(w_dst + i * F::kK * kRowBytes, &p.w, bar, col0 + i * F::kK, kb * F::kK);
+    }
     tma_load_2d(w_dst + kWTile, &p.x, bar, kb * F::kK, row0);
   };
   const int first = kb1 - kb0 < STAGES ? kb1 - kb0 : STAGES;  // tiles that fill the ring
@@ -252,7 +258,9 @@ __global__ void __launch_bounds__(kThreads, 2) dense_few_kernel(const __grid_con
         const uint32_t w_base = smem_u32(smem + stage * F::kStage), x_base = w_base + kWTile;
 #pragma unroll
         for (int j = 0; j < kRowBytes / 32; ++j)
-          mma<FP8>(tmem, smem_desc(w_base + j * MMA_K * kRowBytes, F::kK * kRowBytes, 8 * kRowBytes),
+          mma<FP8>(tmem,
+                   WT ? smem_desc(w_base + j * 32, 16, 8 * kRowBytes)
+                      : smem_desc(w_base + j * MMA_K * kRowBytes, F::kK * kRowBytes, 8 * kRowBytes),
                    smem_desc(x_base + j * 32, 16, 8 * kRowBytes), IDESC, (kb != kb0 || j != 0) ? 1u : 0u);
         umma_commit<1>(smem_u32(&empty[stage]));
         if (++stage == STAGES) {
@@ -338,25 +346,27 @@ int tile_tokens(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 // holds at once, while each has 8 (in all 7 / 8 of them: clusters do not fill every SM of a GPC).  (us, two /
 // one CTA an SM: [14336, 4096] in bf16 at one token 20.4 / 21.7, at 128 27.5 / 33.8; with 2 stages instead
 // of 8 [2048, 4096] in E4M3 goes from 5.1 to 5.8.  [4096, 9728] in E4M3 at 128 tokens, all of two CTAs an SM /
-// half of them: 26 / 21.)
+// half of them: 26 / 21.)  Clusters of 8 on more than 3 / 4 of the SMs wait for room and want 8 stages too ([1024,
+// 1024] at 256 tokens in bf16: 9.6 us, of 4 7.5; [1024, 1024] at one, on half the SMs, 4.0 and 4.6).
 int cluster_of(int64_t tiles, int64_t num_kb) {
   const int64_t sms = num_sms();
   int ranks = 1;
   while (ranks < kMaxCluster && num_kb >= ranks * 2) {
     const int64_t ctas = tiles * ranks * 2;
-    if (ctas > sms && (ctas * 4 > sms * 7 || num_kb < ranks * 2 * 8)) break;
+    const bool full = ctas > sms || (ranks * 2 == kMaxCluster && ctas * 4 > sms * 3);
+    if (full && (ctas * 4 > sms * 7 || num_kb < ranks * 2 * 8)) break;
     ranks *= 2;
   }
   return ranks;
 }
 
-template <bool FP8, int NT>
+template <bool FP8, int NT, bool WT>
 te_status launch(const GemmArgs& g, cudaStream_t s) {
   using F = Form<FP8, NT>;
   static PerDevice<bool> attr_done;
   bool ok = false;
   if (!attr_done.get(&ok, [](bool* v) {
-        *v = cudaFuncSetAttribute(dense_few_kernel<FP8, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        *v = cudaFuncSetAttribute(dense_few_kernel<FP8, NT, WT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                   int(F::kSmem)) == cudaSuccess;
         return *v;
       }))
@@ -364,7 +374,9 @@ te_status launch(const GemmArgs& g, cudaStream_t s) {
   FewParams p;
   memset(&p, 0, sizeof(p));
   const int dt = FP8 ? TE_E4M3 : TE_BF16;
-  if (!make_tmap_2d(&p.w, g.B, dt, g.N, g.K, F::kK, F::kK, 128) || !make_tmap_2d(&p.x, g.A, dt, g.K, g.M, F::kK, NT, 128))
+  const bool w = WT ? make_tmap_2d(&p.w, g.B, dt, g.K, g.N, F::kK, kCols, 128)
+                    : make_tmap_2d(&p.w, g.B, dt, g.N, g.K, F::kK, F::kK, 128);
+  if (!w || !make_tmap_2d(&p.x, g.A, dt, g.K, g.M, F::kK, NT, 128))
     return TE_ERR_CUDA;
   p.end = End{g.a_scale_inv, g.b_scale_inv, g.bias, g.gate, g.residual, g.D, g.saved_h, g.residual_scale,
               g.cast.out_dtype, g.act, int(g.N), int(g.gate_rows), g.gate_rows == g.M};
@@ -388,7 +400,13 @@ te_status launch(const GemmArgs& g, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, dense_few_kernel<FP8, NT>, p) == cudaSuccess ? TE_OK : TE_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, dense_few_kernel<FP8, NT, WT>, p) == cudaSuccess ? TE_OK : TE_ERR_CUDA;
+}
+
+template <bool FP8, bool WT>
+te_status launch_of(const GemmArgs& g, cudaStream_t s) {
+  const int nt = tile_tokens(g.M);
+  return nt == 32 ? launch<FP8, 32, WT>(g, s) : nt == 64 ? launch<FP8, 64, WT>(g, s) : launch<FP8, 128, WT>(g, s);
 }
 
 }  // namespace
@@ -410,12 +428,13 @@ bool dense_few_serves(int64_t M, int64_t N, int64_t K, int ab_dtype) {
 
 te_status launch_dense_few(const GemmArgs& g, cudaStream_t s) {
   if (g.M == 0) return TE_OK;
-  if (g.epilogue != EPI_RESIDUAL || !dense_few_serves(g.M, g.N, g.K, g.ab_dtype)) return TE_ERR_UNSUPPORTED;
-  ProfileScope prof(TE_KERNEL_GEMM_ACT, s);
-  const int nt = tile_tokens(g.M);
-  if (g.ab_dtype == TE_E4M3)
-    return nt == 32 ? launch<true, 32>(g, s) : nt == 64 ? launch<true, 64>(g, s) : launch<true, 128>(g, s);
-  return nt == 32 ? launch<false, 32>(g, s) : nt == 64 ? launch<false, 64>(g, s) : launch<false, 128>(g, s);
+  const bool wt = g.epilogue == EPI_BIAS;
+  if ((!wt && g.epilogue != EPI_RESIDUAL) || !g.a_kmajor || g.b_kmajor != int(wt) ||
+      !dense_few_serves(g.M, g.N, g.K, g.ab_dtype))
+    return TE_ERR_UNSUPPORTED;
+  ProfileScope prof(wt ? TE_KERNEL_GEMM : TE_KERNEL_GEMM_ACT, s);
+  if (g.ab_dtype == TE_E4M3) return wt ? launch_of<true, true>(g, s) : launch_of<true, false>(g, s);
+  return wt ? launch_of<false, true>(g, s) : launch_of<false, false>(g, s);
 }
 
 }  // namespace te

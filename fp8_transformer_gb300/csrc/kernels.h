@@ -294,7 +294,8 @@ te_status launch_gemm(const GemmArgs& g, cudaStream_t s);
 // Bytes of split_ws that launch_gemm would use for this GEMM on the current device (0: none).
 size_t gemm_split_workspace(int64_t M, int64_t N, int64_t K, int ab_dtype, int epilogue);
 
-// EPI_RESIDUAL for outputs of few tiles, split along K over a cluster, and whether it is the faster way.
+// EPI_RESIDUAL with B stored [K, N], or EPI_BIAS without a bias with B stored [N, K], for outputs of few tiles, split
+// along K over a cluster; and whether it is the faster way.
 bool dense_few_serves(int64_t M, int64_t N, int64_t K, int ab_dtype);
 te_status launch_dense_few(const GemmArgs& g, cudaStream_t s);
 

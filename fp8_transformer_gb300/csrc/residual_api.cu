@@ -482,7 +482,10 @@ te_status te_dense_residual_bwd(const void* dout, te_dtype residual_dtype, const
   g.cast.out_dtype = TE_BF16;
   give_split(g, L.split, workspace, ws_bytes);
   g.order = PRODUCT_BEFORE;
-  st = launch_gemm(g, s);
+  // (Few tiles of one row: above 128 rows the tiles of launch_gemm leave SMs on which the second product starts.
+  // Both products and the gradient in front, us, few tiles / those: 4096 x 4096 in bf16 at one row 38 / 57, at 128
+  // 44 / 59, at 512 58 / 58; 1024 x 1024 at 128 15 / 18, at 512 24 / 20.)
+  st = M <= 128 && dense_few_serves(M, K, N, dtype) ? launch_dense_few(g, s) : launch_gemm(g, s);
   if (st != TE_OK) return st;
   GemmArgs h;  // dkernel = x^T dz, the contraction over the rows
   h.A = x;

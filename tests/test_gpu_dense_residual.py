@@ -336,8 +336,10 @@ def test_no_rows():
     assert all(bool((v == 0).all()) for v in (dk, db, dg))
 
 
-# (the last three split the first product, the second and neither along K)
-BESIDE = [(1, 64, 64), (130, 1024, 1024), (2100, 2048, 1040), (300, 64, 16384), (17000, 64, 256), (700, 8192, 272)]
+# (the last five: the first product on many tiles, the same split along K, on single rows of tiles; the second product
+# split; and neither)
+BESIDE = [(1, 64, 64), (48, 2064, 4112), (128, 528, 2064), (20, 9616, 80), (130, 1024, 1024), (2100, 2048, 1040),
+          (2100, 2048, 80), (2304, 1024, 8192), (100, 20480, 64), (17000, 64, 256), (700, 8192, 272)]
 
 
 @pytest.mark.parametrize("M,K,N", BESIDE)
