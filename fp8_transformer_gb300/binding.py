@@ -81,6 +81,7 @@ class _Grad(ctypes.Structure):
 
 
 _lib = None
+_read_grads = None  # of the library that reads tensors
 _lock = threading.Lock()
 
 _vp, _i64, _f, _i32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int32, ctypes.c_size_t
@@ -177,16 +178,20 @@ def lib_path() -> str:
 
 def lib(build_if_stale: bool = True) -> ctypes.CDLL:
     """The loaded library; compiles it first when it is missing or older than its sources."""
-    global _lib
+    global _lib, _read_grads
     if _lib is not None:
         return _lib
     with _lock:
         if _lib is None:
             if build_if_stale and not _build.up_to_date():
                 _build.build()
-            if not os.path.exists(_build.LIB_PATH):
-                raise ImportError(f"{_build.LIB_PATH} is missing: build it with "
-                                  "fp8_transformer_gb300.build.build()")
+            for path in (_build.LIB_PATH, _build.TENSOR_LIB_PATH):
+                if not os.path.exists(path):
+                    raise ImportError(f"{path} is missing: build it with "
+                                      "fp8_transformer_gb300.build.build()")
+            _read_grads = ctypes.PyDLL(_build.TENSOR_LIB_PATH).te_read_grads
+            _read_grads.restype = _i64
+            _read_grads.argtypes = [ctypes.py_object, ctypes.py_object, _GP, ctypes.POINTER(_i64)]
             h = ctypes.CDLL(_build.LIB_PATH)
             for name, (res, args) in _SIGS.items():
                 fn = getattr(h, name)
@@ -1049,34 +1054,34 @@ def te_dense_residual_bwd(dout, x, kernel, dx, dkernel, dresidual=None, saved_z=
 
 
 class GradList:
-    """Gradients for te_grad_norm and te_clip_grad_norm, checked and laid out once: dense float32 / bfloat16
-    tensors on one device, and outs, where their clipped values go (None: in place).  It keeps the tensors;
-    one that has moved since (a new .data) is checked and laid out again at the next call."""
+    """Gradients for te_grad_norm and te_clip_grad_norm: dense float32 / bfloat16 tensors on one device, and
+    outs, where their clipped values go (None: in place).  It keeps the tensors; where they lie, their sizes
+    and types are read at each call, so that a tensor may change them in between (resize_, a new .data)."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
         self.outs = None if outs is None else list(outs)
-        if self.outs is not None and len(self.outs) != len(self.grads):
-            raise ValueError("outs: one for each gradient")
-        self._at = None
-        self._table()
-
-    def _where(self):
-        at = list(map(torch.Tensor.data_ptr, self.grads))
-        return at if self.outs is None else at + list(map(torch.Tensor.data_ptr, self.outs))
+        self.device = self._table()[1]
 
     def _table(self):
-        """The C table, its device and the first gradient (None of an empty list)."""
-        at = self._where()
-        if at == self._at:
-            return
-        self._c = (_Grad * max(len(self.grads), 1))()
-        self.device = self.grads[0].get_device() if self.grads else None
-        for i, g in enumerate(self.grads):
-            p = _arg("grads", g, g.shape, _ACT_DTYPES, self.device)
-            o = None if self.outs is None else _arg("outs", self.outs[i], g.shape, (g.dtype,), self.device)
-            self._c[i] = _Grad(p, o, g.numel(), _dt(g))
-        self._at = at
+        """The C table, and the index of its device (-1 the CPU, None of an empty list)."""
+        n = len(self.grads)
+        if self.outs is not None and len(self.outs) != n:
+            raise ValueError("outs: one for each gradient")
+        if _read_grads is None:
+            lib()
+        table, dev = (_Grad * max(n, 1))(), _i64(-1)
+        i = _read_grads(self.grads, self.outs, table, dev)
+        if i >= 0:
+            self._refuse(i)
+        return table, dev.value if n else None
+
+    def _refuse(self, i):
+        g, dev = self.grads[i], self.grads[0].get_device()
+        _arg("grads", g, g.shape, _ACT_DTYPES, dev)
+        if self.outs is not None:
+            _arg("outs", self.outs[i], g.shape, (g.dtype,), dev)
+        raise ValueError(f"grads: entry {i} is not a dense float32 or bfloat16 tensor")
 
 
 def _grad_args(grads, norm, outs, workspace, stream):
@@ -1084,27 +1089,27 @@ def _grad_args(grads, norm, outs, workspace, stream):
         grads = GradList(grads, outs)
     elif outs is not None:
         raise ValueError("outs: given with the GradList")
-    grads._table()
+    table, where = grads._table()
     dev = torch.cuda.current_device()
-    if grads.device is not None and grads.device != dev:
+    if where is not None and where != dev:
         raise ValueError(f"grads: tensors must live on the current device (cuda:{dev})")
     pn = _arg("norm", norm.reshape(-1), (1,), _F32, dev)
     n = len(grads.grads)
     size = _sized_by("te_grad_norm_workspace", n) if workspace is None else 0
     workspace, pw, nw = _workspace_of(size, norm, workspace, stream)
-    return grads, n, pn, workspace, pw, nw, _stream(stream, dev)
+    return table, n, pn, workspace, pw, nw, _stream(stream, dev)
 
 
 def te_grad_norm(grads, norm, workspace=None, stream=None):
     """norm (one float32) = the root of the sum of the squares of all values of the tensors `grads` (a list, or
     a GradList)."""
-    grads, n, pn, workspace, pw, nw, s = _grad_args(grads, norm, None, workspace, stream)
-    _check("te_grad_norm", lib().te_grad_norm(grads._c, n, pn, pw, nw, s))
+    table, n, pn, workspace, pw, nw, s = _grad_args(grads, norm, None, workspace, stream)
+    _check("te_grad_norm", lib().te_grad_norm(table, n, pn, pw, nw, s))
     return norm
 
 
 def te_clip_grad_norm(grads, max_norm, norm, outs=None, epsilon=1e-6, workspace=None, stream=None):
     """te_grad_norm, and every value times min(1, max_norm / (norm + epsilon)): in place, or into outs."""
-    grads, n, pn, workspace, pw, nw, s = _grad_args(grads, norm, outs, workspace, stream)
-    _check("te_clip_grad_norm", lib().te_clip_grad_norm(grads._c, n, float(max_norm), float(epsilon), pn, pw, nw, s))
+    table, n, pn, workspace, pw, nw, s = _grad_args(grads, norm, outs, workspace, stream)
+    _check("te_clip_grad_norm", lib().te_clip_grad_norm(table, n, float(max_norm), float(epsilon), pn, pw, nw, s))
     return norm
