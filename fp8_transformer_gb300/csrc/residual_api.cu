@@ -113,6 +113,10 @@ te_status check_grads(const te_grad* grads, int64_t n, bool clip, const float* n
     out->push_back(g);
   }
   if (!aligned4(norm)) return TE_ERR_UNSUPPORTED;
+  if (!out->empty() && ws) {
+    const size_t used = std::min(ws_bytes, grad_norm_workspace(n));
+    if (used) written.push_back({reinterpret_cast<uintptr_t>(ws), reinterpret_cast<uintptr_t>(ws) + used});
+  }
   // what is written overlaps nothing
   auto before = [](const Span& a, const Span& b) { return a.lo < b.lo; };
   for (auto* v : {&in, &written})

@@ -151,6 +151,35 @@ def test_clip_refusals():
     assert clip([ok], ws=None) == b.TE_ERR_WORKSPACE and clip([ok], n=4) == b.TE_ERR_WORKSPACE
 
 
+@pytest.mark.parametrize("call", ["te_grad_norm", "te_clip_grad_norm"])
+def test_gradients_workspace_overlaps_nothing(call):
+    """The workspace on a gradient, on the place of a clipped one, on the norm, and beside them."""
+    lib, W, X = te.lib(), P["ws"], P["x"]
+    n = lib.te_grad_norm_workspace(1)
+    assert n >= 16
+
+    def run(spec, ws=W, norm=P["amax"], nbytes=64 * MB):
+        mid = (1.0, 1e-6) if call == "te_clip_grad_norm" else ()
+        return getattr(lib, call)(grads(spec), 1, *mid, norm, ws, nbytes, None)
+
+    inside = [W, W + n - 4, W - 396]
+    for at in inside:
+        assert run((at, None, 100, b.TE_F32)) == b.TE_ERR_INVALID_ARG, at
+    for at in (W, W + 4, W + n - 4):
+        assert run((X, None, 100, b.TE_F32), norm=at) == b.TE_ERR_INVALID_ARG, at
+    if call == "te_clip_grad_norm":
+        for at in inside:
+            assert run((X, at, 100, b.TE_F32)) == b.TE_ERR_INVALID_ARG, at
+    # a workspace that is too short is refused for that, unless what there is of it overlaps already
+    assert run((X, None, 100, b.TE_F32), nbytes=n - 1) == b.TE_ERR_WORKSPACE
+    assert run((W, None, 100, b.TE_F32), nbytes=n - 1) == b.TE_ERR_INVALID_ARG
+    # (neighbours are allowed: these go on to the launch, which finds no device here or is not made)
+    if not torch.cuda.is_available():
+        for spec in ((W + n, None, 100, b.TE_F32), (W - 400, None, 100, b.TE_F32)):
+            assert run(spec) == b.TE_ERR_CUDA, spec
+        assert run((X, None, 100, b.TE_F32), norm=W + n) == b.TE_ERR_CUDA
+
+
 def test_binding_refuses_cpu_tensors_and_shapes():
     lst = te.GradList([torch.ones(3)])
     assert lst.device == -1
