@@ -8,11 +8,12 @@
 // asked for ahead, are no faster; two are 95 us for the 68.)
 //
 // Sums: a thread adds the squares of its 32 (bf16) or 16 (fp32) values of a chunk in fp32, and the
-// chunks' sums, the warps' and the CTAs' as unevaluated pairs of fp32, which lose nothing that fp64 would
-// keep of them (fp64 instructions are two orders slower here and would bound the small cases).  Where a
-// chunk's fp32 sum leaves [2^-80, 2^80] (a square overflowed, or small ones vanished), the thread takes
-// that chunk's squares again in fp64, and so does every sum that they enter, so that the norm is right
-// wherever it is a finite fp32.
+// chunks' sums, the warps' and the CTAs' as unevaluated pairs of fp32 (fp64 instructions are two orders slower
+// here and would bound the small cases).  A square passes at most 11 roundings on its way into a pair (its
+// chain's 8, one of an end of the tensor, two where the chains meet) and all terms are positive: the sum is
+// within 11 * 2^-24, the norm within half of that and its own rounding, 2^-21.  Where a chunk's fp32 sum
+// leaves [2^-80, 2^80] (a square overflowed, or small ones vanished), the thread takes that chunk's squares
+// again in fp64, and so does every sum that they enter, so that this holds wherever the norm is a finite fp32.
 #include "cast.cuh"
 #include "common.cuh"
 #include "kernels.h"

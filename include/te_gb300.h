@@ -623,11 +623,13 @@ typedef struct {
 
 /* te_grad_norm -- *norm (device fp32) = the square root of the sum of the squares of all values of the
  * n tensors `grads` (a host array, read before the call returns; empty tensors may have NULL data).
- *   Sums as exact as fp64's, in a fixed order: right wherever the norm is a finite fp32.
+ *   A thread's 16 (TE_F32) or 32 (TE_BF16) squares of a chunk are added in fp32, all else as pairs of
+ *   fp32, in a fixed order: norm within 2^-21 of its value wherever that is a finite fp32.
  *   workspace  te_grad_norm_workspace(n) bytes, 16-byte aligned.
  * te_clip_grad_norm -- the same, and every value times min(1, max_norm / (norm + epsilon)) (1 where
- * norm + epsilon is 0), in fp32, rounded to its type.  A NaN among the values makes norm and all of
- * them NaN; an infinite norm makes the finite values zero.  max_norm, epsilon >= 0 and finite.
+ * norm + epsilon is 0), in fp32, rounded to its type.  The factor takes the norm before it is rounded, so
+ * that it is right where *norm has passed the largest fp32.  A NaN among the values makes norm and all of
+ * them NaN; an infinity among them makes the finite ones zero.  max_norm, epsilon >= 0 and finite.
  *   No output overlaps a tensor but its own (so no tensor is clipped twice), nor norm. */
 size_t te_grad_norm_workspace(int64_t n);
 te_status te_grad_norm(const te_grad* grads, int64_t n, float* norm, void* workspace,

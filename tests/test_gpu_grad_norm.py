@@ -1,8 +1,9 @@
 """te_grad_norm / te_clip_grad_norm on the GPU against float64.
 
-The norm's sums lose less than fp64's would at these lengths (chunk sums in fp32 of at most 32 values,
-2^-19 of a sum; the root halves it): norm within 2^-20 relative, plus its rounding.  A clipped value is
-one fp32 product with the rounded factor (2^-20 from the norm, 2^-24 each) rounded to its type.
+A thread's squares of a chunk are added in fp32 (at most 11 roundings of 2^-24 on the way of any), the rest in
+pairs that lose nothing of it, and the root halves that: the norm is within 2^-21 relative, its rounding
+included, and the windows here are wider (2^-19).  A clipped value is one fp32 product with the rounded factor
+(2^-20 from the norm, 2^-24 each) rounded to its type.
 """
 
 import numpy as np
