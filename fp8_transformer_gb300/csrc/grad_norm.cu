@@ -228,20 +228,26 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_clip_kernel(const _
                                                                              uint32_t chunks, const GradSlot* slots,
                                                                              int used, double max_norm, double eps,
                                                                              float* norm) {
-  __shared__ float factor;
+  __shared__ float2 factor;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int tid = threadIdx.x;
   if (tid < 32) {
     const double n = norm_of(slots, used, tid);
     if (tid == 0) {
       const double c = n + eps == 0.0 ? 1.0 : max_norm / (n + eps);
-      factor = c > 1.0 ? 1.0f : float(c);  // a NaN stays one
+      // (a NaN stays one; a factor that fp32 holds in few bits or none is split into its power of two and the rest)
+      if (c > 0.0 && c < 0x1p-100) {
+        const int k = max(ilogb(c), -126);
+        factor = make_float2(ldexpf(1.0f, k), float(ldexp(c, -k)));
+      } else {
+        factor = make_float2(1.0f, c > 1.0 ? 1.0f : float(c));
+      }
       if (blockIdx.x == 0 && norm) *norm = float(n);
     }
   }
   __syncthreads();
-  const float f = factor;
-  const f32x2 f2v = f2s(f);
+  const float pre = factor.x, f = factor.y;
+  const f32x2 pre2 = f2s(pre), f2v = f2s(f);
   // the last chunks first: they are what the squares pass has left in L2
   for (int64_t back = int64_t(chunks) - 1 - blockIdx.x; back >= 0; back -= gridDim.x) {
     const uint32_t c = uint32_t(back);
@@ -273,14 +279,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_clip_kernel(const _
           f32x2 q[4];
           Pairs<__nv_bfloat16>::cvt(w[k], q);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) q[e] = mul2(q[e], f2v);
+          for (int e = 0; e < 4; ++e) q[e] = mul2(mul2(q[e], pre2), f2v);
           r = make_uint4(pack_bf16x2(q[0].x, q[0].y), pack_bf16x2(q[1].x, q[1].y), pack_bf16x2(q[2].x, q[2].y),
                          pack_bf16x2(q[3].x, q[3].y));
         } else {
           f32x2 q[2];
           Pairs<float>::cvt(w[k], q);
-          q[0] = mul2(q[0], f2v);
-          q[1] = mul2(q[1], f2v);
+          q[0] = mul2(mul2(q[0], pre2), f2v);
+          q[1] = mul2(mul2(q[1], pre2), f2v);
           r = make_uint4(__float_as_uint(q[0].x), __float_as_uint(q[0].y), __float_as_uint(q[1].x),
                          __float_as_uint(q[1].y));
         }
@@ -290,13 +296,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) grad_clip_kernel(const _
       const int64_t e0 = cut.head + v0 * (16 / es);
       const int64_t last = v0 + kVecs < cut.vecs ? v0 + kVecs : cut.vecs;
       const int64_t e1 = cut.head + last * (16 / es);
-      for (int64_t e = e0 + tid; e < e1; e += kThreads) store_element(d, e, bf16, element(p, e, bf16) * f);
+      for (int64_t e = e0 + tid; e < e1; e += kThreads) store_element(d, e, bf16, element(p, e, bf16) * pre * f);
     }
     if (at == 0) {
-      if (tid < cut.head) store_element(d, tid, bf16, element(p, tid, bf16) * f);
+      if (tid < cut.head) store_element(d, tid, bf16, element(p, tid, bf16) * pre * f);
       else if (tid >= 32 && tid < 32 + cut.tail) {
         const int64_t e = n - cut.tail + (tid - 32);
-        store_element(d, e, bf16, element(p, e, bf16) * f);
+        store_element(d, e, bf16, element(p, e, bf16) * pre * f);
       }
     }
   }

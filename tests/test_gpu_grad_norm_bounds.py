@@ -54,3 +54,22 @@ def test_a_norm_past_the_largest_fp32():
         assert (np.abs(out.cpu().double().numpy() - want) <= rel * np.abs(want)).all()
         te.te_clip_grad_norm([g], 1e39, norm, outs=[out])  # a limit above it: nothing changes
         assert torch.equal(out, g)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("std,max_norm", [(1e30, 1e-12), (1e36, 1e-8), (1e35, 3e-3), (1e37, 1e-20)])
+def test_a_factor_below_the_normal_numbers(dtype, std, max_norm):
+    """A factor of 2^-127 and less, which fp32 holds in few bits, on values that stay normal numbers."""
+    g = torch.Generator().manual_seed(5)
+    for offset in (0, 1):
+        t = (torch.randn(5000, generator=g).clamp(-8, 8) * std).to(dtype).to(DEV)[offset:]
+        norm, outs = torch.empty(1, device=DEV), [torch.empty(t.numel() + 8, dtype=dtype, device=DEV)]
+        old = t.cpu().double().numpy()
+        for at in (0, 3):  # places of the source's alignment and of another
+            out = outs[0][at:at + t.numel()]
+            te.te_clip_grad_norm([t], max_norm, norm, outs=[out], epsilon=0.0)
+            want = old * (max_norm / np.sqrt((old * old).sum()))
+            # as above; a value below the normal numbers may be off by two of its last places (2^-133 in bf16)
+            last = 2.0 ** -149 if dtype == F32 else 2.0 ** -133
+            w = (7.5 * U + torch.finfo(dtype).eps / 2) * np.abs(want) + 2 * last
+            assert (np.abs(out.cpu().double().numpy() - want) <= w).all()
