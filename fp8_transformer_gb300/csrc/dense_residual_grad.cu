@@ -67,7 +67,7 @@ __host__ __device__ __forceinline__ int64_t chunks_of(int64_t gate_rows, int64_t
 }
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_kernel(DenseResidualGradArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_kernel(DenseResidualGradArgs a, unsigned chunks) {
   __shared__ float red[kWarps][2][kStrip];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const CastState cs = cast_begin(a.cast);
@@ -75,10 +75,11 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_k
   const bool want_amax = a.cast.amax_out != nullptr;
   const bool read_z = ACT != TE_IDENTITY || a.dgate != nullptr;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t col = (int64_t(blockIdx.y) * 32 + lane) * 8;
+  const unsigned strip = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
+  const int64_t col = (int64_t(strip) * 32 + lane) * 8;
   const int64_t per_gate = chunks_of(a.gate_rows, a.chunk_rows);
-  const int64_t gate_row = blockIdx.x / per_gate;
-  const int64_t r0 = gate_row * a.gate_rows + (blockIdx.x % per_gate) * a.chunk_rows;
+  const int64_t gate_row = chunk / per_gate;
+  const int64_t r0 = gate_row * a.gate_rows + (chunk % per_gate) * a.chunk_rows;
   const int64_t end = (gate_row + 1) * a.gate_rows;
   const int64_t r1 = r0 + a.chunk_rows < end ? r0 + a.chunk_rows : end;
   f32x2 sz[4], sa[4], gt[4];
@@ -152,9 +153,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_k
       float sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) sum += red[w][h][j];
-      const int64_t c = int64_t(blockIdx.y) * kStrip + j;
+      const int64_t c = int64_t(strip) * kStrip + j;
       if (c < a.N && (h == 0 ? a.dbias != nullptr : a.dgate != nullptr))
-        a.partials[(int64_t(blockIdx.x) * 2 + h) * a.N + c] = sum;
+        a.partials[(int64_t(chunk) * 2 + h) * a.N + c] = sum;
     }
   }
   if (a.cast.amax_out) {
@@ -202,16 +203,29 @@ __global__ void __launch_bounds__(kSumWarps * 32) dense_residual_sum_kernel(Dens
 }
 
 template <typename T>
-void launch_act(const DenseResidualGradArgs& a, dim3 grid, cudaStream_t s) {
+void launch_act(const DenseResidualGradArgs& a, unsigned grid, unsigned chunks, cudaStream_t s) {
   switch (a.act) {
-    case TE_RELU: dense_residual_grad_kernel<T, TE_RELU><<<grid, kWarps * 32, 0, s>>>(a); break;
-    case TE_GELU: dense_residual_grad_kernel<T, TE_GELU><<<grid, kWarps * 32, 0, s>>>(a); break;
-    case TE_SILU: dense_residual_grad_kernel<T, TE_SILU><<<grid, kWarps * 32, 0, s>>>(a); break;
-    default: dense_residual_grad_kernel<T, TE_IDENTITY><<<grid, kWarps * 32, 0, s>>>(a); break;
+    case TE_RELU: dense_residual_grad_kernel<T, TE_RELU><<<grid, kWarps * 32, 0, s>>>(a, chunks); break;
+    case TE_GELU: dense_residual_grad_kernel<T, TE_GELU><<<grid, kWarps * 32, 0, s>>>(a, chunks); break;
+    case TE_SILU: dense_residual_grad_kernel<T, TE_SILU><<<grid, kWarps * 32, 0, s>>>(a, chunks); break;
+    default: dense_residual_grad_kernel<T, TE_IDENTITY><<<grid, kWarps * 32, 0, s>>>(a, chunks); break;
   }
 }
 
+// Chunks of all gates' rows, and the CTAs that take them in strips.
+struct Cover {
+  int64_t chunks, ctas;
+};
+Cover cover(int64_t M, int64_t N, int64_t gate_rows) {
+  const int64_t chunks = M / gate_rows * chunks_of(gate_rows, rows_of(M, N, gate_rows));
+  return {chunks, chunks * ceil_div(N, int64_t(kStrip))};
+}
+
 }  // namespace
+
+bool dense_residual_grad_fits(int64_t M, int64_t N, int64_t gate_rows) {
+  return M <= 0 || cover(M, N, gate_rows).ctas <= 0x7fffffff;
+}
 
 size_t dense_residual_grad_workspace(int64_t M, int64_t N, int64_t gates) {
   if (M <= 0 || N <= 0) return 0;
@@ -222,13 +236,13 @@ size_t dense_residual_grad_workspace(int64_t M, int64_t N, int64_t gates) {
 
 te_status launch_dense_residual_grad(DenseResidualGradArgs a, cudaStream_t s) {
   if (a.M == 0) return TE_OK;
+  if (!dense_residual_grad_fits(a.M, a.N, a.gate_rows)) return TE_ERR_UNSUPPORTED;
   ProfileScope prof(TE_KERNEL_DACT_DBIAS, s);
   a.chunk_rows = rows_of(a.M, a.N, a.gate_rows);
-  const int64_t gates = a.M / a.gate_rows, chunks = gates * chunks_of(a.gate_rows, a.chunk_rows), strips = ceil_div(a.N, kStrip);
-  if (chunks > 0x7fffffff || strips > 65535) return TE_ERR_UNSUPPORTED;
-  const dim3 grid{unsigned(chunks), unsigned(strips)};
-  if (a.dtype == TE_F32) launch_act<float>(a, grid, s);
-  else launch_act<__nv_bfloat16>(a, grid, s);
+  const int64_t gates = a.M / a.gate_rows;
+  const Cover c = cover(a.M, a.N, a.gate_rows);
+  if (a.dtype == TE_F32) launch_act<float>(a, unsigned(c.ctas), unsigned(c.chunks), s);
+  else launch_act<__nv_bfloat16>(a, unsigned(c.ctas), unsigned(c.chunks), s);
   if (cudaGetLastError() != cudaSuccess) return TE_ERR_CUDA;
   if (!a.dbias && !a.dgate) return TE_OK;
   const int64_t rows = a.dgate ? 1 + (gates < 1024 ? gates : 1024) : 1;

@@ -6,7 +6,7 @@ bias within WZ = 2^-18 |x| |w| + 2^-22 (|z| + |b|), act(z) within 1.2 WZ + 1e-5 
 is steeper than 1.13), and what joins the stream adds 2^-22 of its terms.  What is stored is a rounding
 of a number in the window.  dz is rounded before the products: where its window holds a border, the
 product may see the value on either side, and the jump counts through the operand's magnitudes.  Column
-sums pass at most 16 rows in a warp, 8 warps, chunks and 16 warps again: 2^-17 of their terms.
+sums pass at most 32 rows in a warp, 8 warps, chunks and 16 warps again: 2^-17 of their terms.
 """
 
 import numpy as np
@@ -412,6 +412,29 @@ def test_streams_and_graphs(M):
             g.replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
+def test_backward_of_very_many_columns():
+    """More than 65535 strips of 256 columns; whole numbers, whose sums are exact in any order."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    M, K, N = 2, 16, 65537 * 256 + 16
+    g = torch.Generator(device=DEV).manual_seed(3)
+
+    def few(*s, d=BF):
+        return torch.randint(-1, 2, s, generator=g, device=DEV, dtype=torch.int8).to(d)
+
+    x, w, dout, z, gate = few(M, K), few(K, N), few(M, N), few(M, N), few(N)
+    dx, dw, dres = torch.empty_like(x), torch.empty_like(w), torch.empty_like(dout)
+    db, dg = torch.empty(N, device=DEV), torch.empty(N, device=DEV)
+    te.te_dense_residual_bwd(dout, x, w, dx, dw, dresidual=dres, saved_z=z, activation="relu", gate=gate, residual_scale=0.5,
+                             dbias=db, dgate=dg)
+    dz = (dout * gate * (z > 0)).float()
+    assert torch.equal(db, dz.sum(0)) and torch.equal(dg, (dout * z.clamp(min=0)).float().sum(0))
+    assert torch.equal(dres, dout * 0.5)
+    assert torch.equal(dw, (x[0, :, None] * dz[0] + x[1, :, None] * dz[1]).to(BF))
+    want = torch.stack([(w[k].float() * dz).double().sum(1) for k in range(K)], 1)
+    assert torch.equal(dx, want.float().to(BF))
 
 
 def test_workspaces():

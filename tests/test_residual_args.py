@@ -124,6 +124,18 @@ def test_dense_bwd_workspace():
     assert dense_bwd(ws=None) == b.TE_ERR_WORKSPACE and dense_bwd(n=128) == b.TE_ERR_WORKSPACE
 
 
+def test_dense_bwd_many_columns():
+    """More than 65535 strips of 256 columns pass the checks (and find no device here); what no grid holds is
+    refused before anything is launched."""
+    far = {k: (i + 1) << 40 for i, k in enumerate(P)}
+    if not torch.cuda.is_available():
+        kw = dict(far, dtype=b.TE_E4M3, q=quantizer(scale=far["scale"], inv=far["scale_inv"], amax=None), M=2, K=16,
+                  n=1 << 34)
+        for N in (65535 * 256, 65535 * 256 + 16, 1 << 28):
+            assert dense_bwd(N=N, **kw) == b.TE_ERR_CUDA, N
+    assert dense_bwd(M=1 << 30, N=1 << 30, gates=1 << 30, K=16) == b.TE_ERR_UNSUPPORTED
+
+
 def grads(*spec):
     return (b._Grad * max(len(spec), 1))(*(b._Grad(*s) for s in spec))
 
