@@ -47,6 +47,7 @@ EXPORTED = ["te_status_string", "te_version", "te_get_device_status", "te_worksp
             "te_layernorm_dense_bwd",
             "te_dact_dbias_quantize_noalloc",
             "te_dact_dbias_noalloc_capacity", "te_selftest_wait_timeout",
+            "te_selftest_cluster_abort",
             "te_layernorm_mlp_fwd_host", "te_update_scales", "te_stream_probe",
             "te_block_scale_bytes", "te_block_quantize", "te_block_dequantize", "te_block_gemm",
             "te_dense_fp4_fwd", "te_dense_fp4_bwd", "te_dact_dbias_ckpt",
@@ -120,6 +121,7 @@ _SIGS = {
                                             _i64, _i64, _i64, ctypes.c_int, _vp, _vp, _vp, _vp,
                                             _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "te_selftest_wait_timeout": (ctypes.c_int, [_i64, _vp]),
+    "te_selftest_cluster_abort": (ctypes.c_int, [_i64, ctypes.c_int, _vp, _vp]),
     "te_layernorm_mlp_fwd_host": (ctypes.c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_int,
                                                  ctypes.c_int, ctypes.c_float, ctypes.c_int, _i64,
                                                  _i64, _i64, ctypes.c_int, _vp, ctypes.c_int, _vp,
@@ -300,6 +302,13 @@ def selftest_wait_timeout(limit_us: int = 20000, stream=None):
     """Launch the library's bounded-wait self-test: a wait that nothing completes gives up after
     limit_us and records TE_ERR_TIMEOUT, which get_device_status() then returns."""
     _check("te_selftest_wait_timeout", lib().te_selftest_wait_timeout(int(limit_us), _stream(stream)))
+
+
+def selftest_cluster_abort(out, rank, limit_us: int = 20000, stream=None):
+    """The same wait in CTA `rank` (-1: in none) of a cluster; out (8 int32) receives 1 for each of its CTAs that
+    would still write results."""
+    _check("te_selftest_cluster_abort", lib().te_selftest_cluster_abort(
+        int(limit_us), int(rank), _arg("out", out, (8,), (torch.int32,), torch.cuda.current_device()), _stream(stream)))
 
 
 def workspace_size(op, M, H, F_or_N, dtype=TE_BF16, quantized=False, kernel_dtype=None,

@@ -13,7 +13,8 @@
 //   warps 2-9  bring the accumulator to shared memory, a TMEM lane quadrant to two warps
 // and all of them finish the tile.
 // Every wait on an mbarrier is bounded; on expiry a thread records TE_ERR_TIMEOUT, all roles leave their
-// loops, and the CTA goes on to the cluster's barriers without writing results.
+// loops, and the CTA goes on to the cluster's barriers, behind the first of which no CTA of the cluster writes
+// results.
 //
 // W [14336, 4096] (us; in brackets the time of its bytes at the measured copy rate): bf16 at 1, 32 and 128
 // tokens 21, 23 and 28 (17.3, 17.5, 18.2); E4M3 13, 15 and 20 (8.7, 8.8, 9.2).  About 4 us of each are the
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 2) dense_few_kernel(const __grid_con
   if (row < rows) in = p.end.load(row0 + row, col0 + c);
   __syncwarp();
   if (ranks > 1) cluster_sync();
-  if (!abort_flag) {
+  if (!(ranks > 1 ? cluster_aborted(&abort_flag, ranks) : abort_flag != 0)) {
     uint32_t sums[kMaxCluster];
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)

@@ -132,6 +132,11 @@ te_status te_get_device_status(int32_t* device_status);
  * TE_ERR_INVALID_ARG for a limit outside the range. */
 te_status te_selftest_wait_timeout(int64_t limit_us, void* stream);
 
+/* te_selftest_cluster_abort -- the same in one CTA (`rank`, or -1: in none) of a cluster of 8 whose CTAs read one
+ * another's partial results: out (8 device int32) receives 1 for each CTA that would write its share, which is
+ * none once one has given up. */
+te_status te_selftest_cluster_abort(int64_t limit_us, int rank, int32_t* out, void* stream);
+
 /* Bytes of workspace a call needs.  dims = {M, H, F or N}; `dtype` is the activation dtype,
  * `quantized` is nonzero when a quantizer set is passed, `kernel_dtype` the weights' storage
  * dtype.  Unused dims may be 0.  Returns 0 for operations that need none.
