@@ -171,6 +171,7 @@ te_status te_residual_norm_fwd(const void* y, te_dtype dtype, const void* residu
     return TE_ERR_INVALID_ARG;
   if (M > 0 && (!y || !residual || !gamma || !x_out || !out)) return TE_ERR_INVALID_ARG;
   if (!post_gamma && (post_beta || post_mu || post_rsigma)) return TE_ERR_INVALID_ARG;
+  if (norm_type == TE_RMSNORM) beta = post_beta = nullptr;  // not read
   const int64_t gate_rows = gate_rows_of(gate, gates, M);
   if (gate_rows == 0) return TE_ERR_INVALID_ARG;
   if ((out_dtype == TE_E4M3 && !enabled(q)) || !quantizer_ok(q) || (q && !aligned4(q->amax))) return TE_ERR_INVALID_ARG;
@@ -189,7 +190,8 @@ te_status te_residual_norm_fwd(const void* y, te_dtype dtype, const void* residu
   spans.writes(x_out, rows * esize(residual_dtype));
   spans.writes(out, rows * esize(out_dtype));
   for (const void* p : {mu, rsigma, post_mu, post_rsigma}) spans.writes(p, stat);
-  spans.quantizer(q);
+  if (out_dtype == TE_E4M3) spans.quantizer(q);
+  else if (q) spans.writes(q->amax, 4);
   if (spans.clash()) return TE_ERR_INVALID_ARG;
   ResidualNormArgs a;
   a.y = y;
@@ -199,9 +201,9 @@ te_status te_residual_norm_fwd(const void* y, te_dtype dtype, const void* residu
   a.M = M;
   a.H = H;
   a.gamma = gamma;
-  a.beta = norm_type == TE_LAYERNORM ? beta : nullptr;
+  a.beta = beta;
   a.post_gamma = post_gamma;
-  a.post_beta = norm_type == TE_LAYERNORM ? post_beta : nullptr;
+  a.post_beta = post_beta;
   a.gate = gate;
   a.gate_rows = gate_rows;
   a.residual_scale = residual_scale;
@@ -255,6 +257,10 @@ te_status te_residual_norm_bwd(const void* dout, const void* dx_out, const void*
   if (M > 0 && (!dout || !x_out || !rsigma || (ln && !mu) || ((post || gate) && !y) || (post && !post_rsigma) ||
                 (post && ln && !post_mu)))
     return TE_ERR_INVALID_ARG;
+  // what is not read may be anything, and lie anywhere
+  if (!post && !gate) y = nullptr;
+  if (!ln) mu = post_mu = nullptr;
+  if (!ln || !dgate) post_beta = nullptr;
   if (H % 8 || H > 8192 || M > kMaxDim) return TE_ERR_UNSUPPORTED;
   for (const void* p : {dout, dx_out, x_out, y, gamma, post_gamma, post_beta, gate, static_cast<const void*>(dresidual),
                         static_cast<const void*>(dy), static_cast<const void*>(workspace)})
@@ -310,7 +316,7 @@ te_status te_residual_norm_bwd(const void* dout, const void* dx_out, const void*
   a.post_rsigma = post_rsigma;
   a.gamma = gamma;
   a.post_gamma = post_gamma;
-  a.post_beta = ln ? post_beta : nullptr;
+  a.post_beta = post_beta;
   a.gate = gate;
   a.gate_rows = gate_rows;
   a.residual_scale = residual_scale;
@@ -410,6 +416,7 @@ te_status te_dense_residual_bwd(const void* dout, te_dtype residual_dtype, const
   if (gate_rows == 0 || (!gate && dgate) || !dkernel) return TE_ERR_INVALID_ARG;
   if (M > 0 && (!dout || !x || !kernel || !dx || ((act != TE_IDENTITY || dgate) && !saved_z)))
     return TE_ERR_INVALID_ARG;
+  if (act == TE_IDENTITY && !dgate) saved_z = nullptr;  // not read
   if (K % 16 || N % 16 || M > kMaxDim || K > kMaxDim || N > kMaxDim || !dense_residual_grad_fits(M, N, gate_rows))
     return TE_ERR_UNSUPPORTED;
   for (const void* p : {dout, x, kernel, saved_z, gate, static_cast<const void*>(dx), static_cast<const void*>(dkernel),

@@ -124,6 +124,28 @@ def test_dense_bwd_workspace():
     assert dense_bwd(ws=None) == b.TE_ERR_WORKSPACE and dense_bwd(n=128) == b.TE_ERR_WORKSPACE
 
 
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the calls would go on to the launch")
+def test_what_is_not_read_is_not_held_against_what_is_written():
+    """Tensors that a call takes and does not read may lie anywhere (these pass the checks and find no device)."""
+    rms, plain = b.TE_RMSNORM, dict(post_gamma=None, post_beta=None, post_mu=None, post_rsigma=None)
+    for kw in (dict(norm=rms, beta=P["out"]), dict(norm=rms, post_beta=P["x_out"] + 8),
+               dict(q=quantizer(scale=P["out"], inv=P["x_out"]))):
+        assert fwd(**kw) == b.TE_ERR_CUDA, kw
+    assert fwd(q=quantizer(amax=P["out"])) == b.TE_ERR_INVALID_ARG
+    assert fwd(od=b.TE_E4M3, q=quantizer(scale=P["out"])) == b.TE_ERR_INVALID_ARG
+    none = dict(plain, gate=None, dgate=None, dpost_gamma=None, dpost_beta=None)
+    for kw in (dict(none, dy=P["y"]), dict(none, y=P["dresidual"] + 8), dict(norm=rms, mu=P["dy"]),
+               dict(norm=rms, post_mu=P["dgamma"] + 1), dict(norm=rms, post_beta=P["dy"]),
+               dict(post_beta=P["dy"], dgate=None)):
+        assert bwd(**kw) == b.TE_ERR_CUDA, kw
+    for kw in (dict(dy=P["y"]), dict(none, dy=P["x_out"]), dict(norm=rms, rsigma=P["dy"]), dict(post_beta=P["dy"])):
+        assert bwd(**kw) == b.TE_ERR_INVALID_ARG, kw
+    for kw in (dict(act=b.TE_IDENTITY, dgate=None, z=P["dx"]), dict(act=b.TE_IDENTITY, dgate=None, z=P["dbias"] + 2)):
+        assert dense_bwd(**kw) == b.TE_ERR_CUDA, kw
+    for kw in (dict(act=b.TE_IDENTITY, z=P["dx"]), dict(act=b.TE_RELU, dgate=None, z=P["dx"])):
+        assert dense_bwd(**kw) == b.TE_ERR_INVALID_ARG, kw
+
+
 def test_dense_bwd_many_columns():
     """More than 65535 strips of 256 columns pass the checks (and find no device here); what no grid holds is
     refused before anything is launched."""
