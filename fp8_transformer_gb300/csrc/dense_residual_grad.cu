@@ -42,15 +42,39 @@ __device__ __forceinline__ void cvt8(const uint4 (&w)[2], f32x2 (&p)[4]) {
   }
 }
 
+// v, but no less than lo and no more than hi; a NaN stays one.
+__device__ __forceinline__ f32x2 above(f32x2 v, float lo) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v.x) : "f"(lo));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v.y) : "f"(lo));
+  return v;
+}
+__device__ __forceinline__ f32x2 below(f32x2 v, float hi) {
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(v.x) : "f"(hi));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(v.y) : "f"(hi));
+  return v;
+}
+
 // gelu(h) = h s and gelu'(h) = s + 2 h sqrt(2/pi) (1 + 3 * 0.044715 h^2) s (1 - s) from one logistic
 // s = 1 / (1 + e) of twice the inner function, 1 - s = e s (e's exponent clamped so that it stays finite).
+// Beyond +-16 s is 0 or 1 to fp32 and the powers of h would only overflow against it.
 __device__ __forceinline__ void gelu_both(f32x2 h, f32x2& act, f32x2& dact) {
-  const f32x2 hh = mul2(h, h);
-  const f32x2 e = ex2_2(min2s(mul2(h, fma2(hh, f2s(kGeluA2), f2s(kGeluA1))), 80.0f * kLog2e));
+  h = above(h, -16.0f);
+  const f32x2 c = below(h, 16.0f), cc = mul2(c, c);
+  const f32x2 e = ex2_2(min2s(mul2(c, fma2(cc, f2s(kGeluA2), f2s(kGeluA1))), 80.0f * kLog2e));
   const f32x2 s = rcp2(add2(e, f2s(1.0f)));
-  const f32x2 q = mul2(h, fma2(hh, f2s(6.0f * kGeluK0 * kGeluK1), f2s(2.0f * kGeluK0)));
+  const f32x2 q = mul2(c, fma2(cc, f2s(6.0f * kGeluK0 * kGeluK1), f2s(2.0f * kGeluK0)));
   act = mul2(h, s);
   dact = fma2(q, mul2(s, mul2(e, s)), s);
+}
+
+// silu(z) = z s and silu'(z) = s (1 + z (1 - s)), the same way, beyond +-128.
+__device__ __forceinline__ void silu_both(f32x2 z, f32x2& act, f32x2& dact) {
+  f32x2 s, e;
+  z = above(z, -128.0f);
+  const f32x2 c = below(z, 128.0f);
+  sigmoid2(c, s, e);
+  act = mul2(z, s);
+  dact = mul2(s, fma2(c, mul2(e, s), f2s(1.0f)));
 }
 
 // Rows of a chunk, and the chunks of one gate's rows.
@@ -114,12 +138,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_k
           s[2 * p] = a.residual_scale * f2lo(dp[p]);
           s[2 * p + 1] = a.residual_scale * f2hi(dp[p]);
           f32x2 act = zp[p], dact = f2s(1.0f);
-          if constexpr (ACT == TE_SILU) {  // silu and silu' share one logistic
-            f32x2 sg, eg;
-            sigmoid2(zp[p], sg, eg);
-            dact = mul2(sg, fma2(zp[p], mul2(eg, sg), f2s(1.0f)));
-            act = mul2(zp[p], sg);
-          } else if constexpr (ACT == TE_GELU) {  // as do gelu and gelu'
+          if constexpr (ACT == TE_SILU) {
+            silu_both(zp[p], act, dact);
+          } else if constexpr (ACT == TE_GELU) {
             gelu_both(zp[p], act, dact);
           } else if constexpr (ACT != TE_IDENTITY) {
             act = act2c<ACT>(zp[p]);
