@@ -19,6 +19,7 @@ constexpr int kCtasPerSm = 2;
 constexpr int kMaxRows = 256;  // of a chunk: no sum of a thread runs over more than 32
 constexpr int kUnroll = 4;  // rows of loads in flight per warp (86 us a call for 89 with 3 CTAs and 2 rows)
 constexpr int kStrip = 256;
+constexpr int64_t kMaxCols = int64_t(65535) * kStrip;  // of one launch
 
 template <typename T>
 __device__ __forceinline__ void load8(const void* base, int64_t at, uint4 (&w)[2]) {
@@ -42,39 +43,43 @@ __device__ __forceinline__ void cvt8(const uint4 (&w)[2], f32x2 (&p)[4]) {
   }
 }
 
-// v, but no less than lo and no more than hi; a NaN stays one.
-__device__ __forceinline__ f32x2 above(f32x2 v, float lo) {
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v.x) : "f"(lo));
-  asm("max.NaN.f32 %0, %0, %1;" : "+f"(v.y) : "f"(lo));
-  return v;
+// Two bf16 values, but no less than lo and no more than hi; a NaN stays one.
+__device__ __forceinline__ uint32_t above(uint32_t w, uint32_t lo) {
+  asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(lo));
+  return w;
 }
-__device__ __forceinline__ f32x2 below(f32x2 v, float hi) {
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(v.x) : "f"(hi));
-  asm("min.NaN.f32 %0, %0, %1;" : "+f"(v.y) : "f"(hi));
-  return v;
+__device__ __forceinline__ uint32_t below(uint32_t w, uint32_t hi) {
+  asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(w) : "r"(hi));
+  return w;
 }
 
+// An activation and its derivative at two bf16 values.
 // gelu(h) = h s and gelu'(h) = s + 2 h sqrt(2/pi) (1 + 3 * 0.044715 h^2) s (1 - s) from one logistic
-// s = 1 / (1 + e) of twice the inner function, 1 - s = e s (e's exponent clamped so that it stays finite).
-// Beyond +-16 s is 0 or 1 to fp32 and the powers of h would only overflow against it.
-__device__ __forceinline__ void gelu_both(f32x2 h, f32x2& act, f32x2& dact) {
-  h = above(h, -16.0f);
-  const f32x2 c = below(h, 16.0f), cc = mul2(c, c);
-  const f32x2 e = ex2_2(min2s(mul2(c, fma2(cc, f2s(kGeluA2), f2s(kGeluA1))), 80.0f * kLog2e));
-  const f32x2 s = rcp2(add2(e, f2s(1.0f)));
-  const f32x2 q = mul2(c, fma2(cc, f2s(6.0f * kGeluK0 * kGeluK1), f2s(2.0f * kGeluK0)));
-  act = mul2(h, s);
-  dact = fma2(q, mul2(s, mul2(e, s)), s);
-}
-
-// silu(z) = z s and silu'(z) = s (1 + z (1 - s)), the same way, beyond +-128.
-__device__ __forceinline__ void silu_both(f32x2 z, f32x2& act, f32x2& dact) {
-  f32x2 s, e;
-  z = above(z, -128.0f);
-  const f32x2 c = below(z, 128.0f);
-  sigmoid2(c, s, e);
-  act = mul2(z, s);
-  dact = mul2(s, fma2(c, mul2(e, s), f2s(1.0f)));
+// s = 1 / (1 + e) of twice the inner function, 1 - s = e s; silu(h) = h s and silu'(h) = s (1 + h (1 - s)) likewise.
+// h is held where s still moves: from below, so that e stays finite (at -9.875 and -80 s is under 2^-115), and for
+// all but the product h s from above, where the powers of h would overflow against 1 - s = 0.
+template <int ACT>
+__device__ __forceinline__ void act_both(uint32_t w, f32x2& act, f32x2& dact) {
+  if constexpr (ACT == TE_GELU) {
+    w = above(w, 0xC11EC11Eu);
+    const f32x2 h = bf16x2_f2(w), c = bf16x2_f2(below(w, 0x41804180u)), cc = mul2(c, c);  // 16
+    const f32x2 e = ex2_2(mul2(c, fma2(cc, f2s(kGeluA2), f2s(kGeluA1))));
+    const f32x2 s = rcp2(add2(e, f2s(1.0f)));
+    const f32x2 q = mul2(c, fma2(cc, f2s(6.0f * kGeluK0 * kGeluK1), f2s(2.0f * kGeluK0)));
+    act = mul2(h, s);
+    dact = fma2(q, mul2(s, mul2(e, s)), s);
+  } else if constexpr (ACT == TE_SILU) {
+    w = above(w, 0xC2A0C2A0u);
+    const f32x2 h = bf16x2_f2(w), c = bf16x2_f2(below(w, 0x43004300u));  // 128
+    const f32x2 e = ex2_2(mul2(c, f2s(-kLog2e)));
+    const f32x2 s = rcp2(add2(e, f2s(1.0f)));
+    act = mul2(h, s);
+    dact = mul2(s, fma2(c, mul2(e, s), f2s(1.0f)));
+  } else {
+    const f32x2 h = bf16x2_f2(w);
+    act = act2c<ACT>(h);
+    dact = dact2c<ACT>(h);
+  }
 }
 
 // Rows of a chunk, and the chunks of one gate's rows.
@@ -91,7 +96,7 @@ __host__ __device__ __forceinline__ int64_t chunks_of(int64_t gate_rows, int64_t
 }
 
 template <typename T, int ACT>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_kernel(DenseResidualGradArgs a, unsigned chunks) {
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_kernel(DenseResidualGradArgs a) {
   __shared__ float red[kWarps][2][kStrip];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const CastState cs = cast_begin(a.cast);
@@ -99,18 +104,17 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_k
   const bool want_amax = a.cast.amax_out != nullptr;
   const bool read_z = ACT != TE_IDENTITY || a.dgate != nullptr;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const unsigned strip = blockIdx.x / chunks, chunk = blockIdx.x % chunks;
-  const int64_t col = (int64_t(strip) * 32 + lane) * 8;
+  const int64_t col = (int64_t(blockIdx.y) * 32 + lane) * 8;
   const int64_t per_gate = chunks_of(a.gate_rows, a.chunk_rows);
-  const int64_t gate_row = chunk / per_gate;
-  const int64_t r0 = gate_row * a.gate_rows + (chunk % per_gate) * a.chunk_rows;
+  const int64_t gate_row = blockIdx.x / per_gate;
+  const int64_t r0 = gate_row * a.gate_rows + (blockIdx.x % per_gate) * a.chunk_rows;
   const int64_t end = (gate_row + 1) * a.gate_rows;
   const int64_t r1 = r0 + a.chunk_rows < end ? r0 + a.chunk_rows : end;
   f32x2 sz[4], sa[4], gt[4];
 #pragma unroll
   for (int p = 0; p < 4; ++p) sz[p] = sa[p] = f2s(0.0f), gt[p] = f2s(1.0f);
   float amax = 0.0f;
-  if (col < a.N) {
+  if (col < a.cols) {
     if (a.gate) Pairs<__nv_bfloat16>::cvt(__ldg(reinterpret_cast<const uint4*>(
                     static_cast<const uint16_t*>(a.gate) + gate_row * a.N + col)), gt);
     for (int64_t rb = r0 + warp; rb < r1; rb += kUnroll * kWarps) {
@@ -129,23 +133,16 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_k
         const int64_t r = rb + j * kWarps;
         if (r >= r1) break;
         const int64_t at = r * a.N + col;
-        f32x2 dp[4], zp[4];
+        f32x2 dp[4];
         cvt8<T>(d[j], dp);
-        cvt8<__nv_bfloat16>(z[j], zp);
+        const uint32_t zw[4] = {z[j][0].x, z[j][0].y, z[j][0].z, z[j][0].w};
         float o[8], s[8];
 #pragma unroll
         for (int p = 0; p < 4; ++p) {
           s[2 * p] = a.residual_scale * f2lo(dp[p]);
           s[2 * p + 1] = a.residual_scale * f2hi(dp[p]);
-          f32x2 act = zp[p], dact = f2s(1.0f);
-          if constexpr (ACT == TE_SILU) {
-            silu_both(zp[p], act, dact);
-          } else if constexpr (ACT == TE_GELU) {
-            gelu_both(zp[p], act, dact);
-          } else if constexpr (ACT != TE_IDENTITY) {
-            act = act2c<ACT>(zp[p]);
-            dact = dact2c<ACT>(zp[p]);
-          }
+          f32x2 act, dact;
+          act_both<ACT>(zw[p], act, dact);
           sa[p] = fma2(dp[p], act, sa[p]);
           f32x2 v = ACT == TE_IDENTITY ? dp[p] : mul2(dp[p], dact);
           v = mul2(v, gt[p]);
@@ -174,9 +171,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) dense_residual_grad_k
       float sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) sum += red[w][h][j];
-      const int64_t c = int64_t(strip) * kStrip + j;
-      if (c < a.N && (h == 0 ? a.dbias != nullptr : a.dgate != nullptr))
-        a.partials[(int64_t(chunk) * 2 + h) * a.N + c] = sum;
+      const int64_t c = int64_t(blockIdx.y) * kStrip + j;
+      if (c < a.cols && (h == 0 ? a.dbias != nullptr : a.dgate != nullptr))
+        a.partials[(int64_t(blockIdx.x) * 2 + h) * a.N + c] = sum;
     }
   }
   if (a.cast.amax_out) {
@@ -224,29 +221,16 @@ __global__ void __launch_bounds__(kSumWarps * 32) dense_residual_sum_kernel(Dens
 }
 
 template <typename T>
-void launch_act(const DenseResidualGradArgs& a, unsigned grid, unsigned chunks, cudaStream_t s) {
+void launch_act(const DenseResidualGradArgs& a, dim3 grid, cudaStream_t s) {
   switch (a.act) {
-    case TE_RELU: dense_residual_grad_kernel<T, TE_RELU><<<grid, kWarps * 32, 0, s>>>(a, chunks); break;
-    case TE_GELU: dense_residual_grad_kernel<T, TE_GELU><<<grid, kWarps * 32, 0, s>>>(a, chunks); break;
-    case TE_SILU: dense_residual_grad_kernel<T, TE_SILU><<<grid, kWarps * 32, 0, s>>>(a, chunks); break;
-    default: dense_residual_grad_kernel<T, TE_IDENTITY><<<grid, kWarps * 32, 0, s>>>(a, chunks); break;
+    case TE_RELU: dense_residual_grad_kernel<T, TE_RELU><<<grid, kWarps * 32, 0, s>>>(a); break;
+    case TE_GELU: dense_residual_grad_kernel<T, TE_GELU><<<grid, kWarps * 32, 0, s>>>(a); break;
+    case TE_SILU: dense_residual_grad_kernel<T, TE_SILU><<<grid, kWarps * 32, 0, s>>>(a); break;
+    default: dense_residual_grad_kernel<T, TE_IDENTITY><<<grid, kWarps * 32, 0, s>>>(a); break;
   }
 }
 
-// Chunks of all gates' rows, and the CTAs that take them in strips.
-struct Cover {
-  int64_t chunks, ctas;
-};
-Cover cover(int64_t M, int64_t N, int64_t gate_rows) {
-  const int64_t chunks = M / gate_rows * chunks_of(gate_rows, rows_of(M, N, gate_rows));
-  return {chunks, chunks * ceil_div(N, int64_t(kStrip))};
-}
-
 }  // namespace
-
-bool dense_residual_grad_fits(int64_t M, int64_t N, int64_t gate_rows) {
-  return M <= 0 || cover(M, N, gate_rows).ctas <= 0x7fffffff;
-}
 
 size_t dense_residual_grad_workspace(int64_t M, int64_t N, int64_t gates) {
   if (M <= 0 || N <= 0) return 0;
@@ -257,13 +241,26 @@ size_t dense_residual_grad_workspace(int64_t M, int64_t N, int64_t gates) {
 
 te_status launch_dense_residual_grad(DenseResidualGradArgs a, cudaStream_t s) {
   if (a.M == 0) return TE_OK;
-  if (!dense_residual_grad_fits(a.M, a.N, a.gate_rows)) return TE_ERR_UNSUPPORTED;
   ProfileScope prof(TE_KERNEL_DACT_DBIAS, s);
   a.chunk_rows = rows_of(a.M, a.N, a.gate_rows);
-  const int64_t gates = a.M / a.gate_rows;
-  const Cover c = cover(a.M, a.N, a.gate_rows);
-  if (a.dtype == TE_F32) launch_act<float>(a, unsigned(c.ctas), unsigned(c.chunks), s);
-  else launch_act<__nv_bfloat16>(a, unsigned(c.ctas), unsigned(c.chunks), s);
+  const int64_t gates = a.M / a.gate_rows, chunks = gates * chunks_of(a.gate_rows, a.chunk_rows);
+  // Strips go along y, whose size is limited: what lies behind it in another launch.  (One dimension, taken apart
+  // in the kernel, or a first strip among the arguments cost 8% at 16384 x 8192: the kernel needs every register.)
+  for (int64_t at = 0; at < a.N; at += kMaxCols) {
+    DenseResidualGradArgs b = a;
+    auto from = [&](auto* p, size_t es) { return p ? reinterpret_cast<decltype(p)>(uintptr_t(p) + size_t(at) * es) : p; };
+    const size_t es = a.dtype == TE_F32 ? 4 : 2;
+    b.dout = from(a.dout, es);
+    b.dresidual = from(a.dresidual, es);
+    b.z = from(a.z, 2);
+    b.gate = from(a.gate, 2);
+    b.dz = from(a.dz, a.cast.out_dtype == TE_E4M3 ? 1 : 2);
+    b.partials = from(a.partials, 4);
+    b.cols = a.N - at < kMaxCols ? a.N - at : kMaxCols;
+    const dim3 grid{unsigned(chunks), unsigned(ceil_div(b.cols, kStrip))};
+    if (a.dtype == TE_F32) launch_act<float>(b, grid, s);
+    else launch_act<__nv_bfloat16>(b, grid, s);
+  }
   if (cudaGetLastError() != cudaSuccess) return TE_ERR_CUDA;
   if (!a.dbias && !a.dgate) return TE_OK;
   const int64_t rows = a.dgate ? 1 + (gates < 1024 ? gates : 1024) : 1;

@@ -341,12 +341,11 @@ struct DenseResidualGradArgs {
   float* dbias = nullptr;
   float* dgate = nullptr;      // [M / gate_rows, N]
   float* partials = nullptr;   // workspace
-  int64_t chunk_rows = 0;      // set at launch
+  int64_t chunk_rows = 0;      // set at launch, like cols
+  int64_t cols = 0;            // of N, those of one launch
   CastSpec cast;
 };
 te_status launch_dense_residual_grad(DenseResidualGradArgs a, cudaStream_t s);
-// Whether its CTAs fit a grid (tensors past 2^39 values may not).
-bool dense_residual_grad_fits(int64_t M, int64_t N, int64_t gate_rows);
 size_t dense_residual_grad_workspace(int64_t M, int64_t N, int64_t gates);
 
 // Sum of the squares of many tensors, and the tensors scaled by min(1, max_norm / (norm + eps)).

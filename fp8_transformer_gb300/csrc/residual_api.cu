@@ -417,8 +417,7 @@ te_status te_dense_residual_bwd(const void* dout, te_dtype residual_dtype, const
   if (M > 0 && (!dout || !x || !kernel || !dx || ((act != TE_IDENTITY || dgate) && !saved_z)))
     return TE_ERR_INVALID_ARG;
   if (act == TE_IDENTITY && !dgate) saved_z = nullptr;  // not read
-  if (K % 16 || N % 16 || M > kMaxDim || K > kMaxDim || N > kMaxDim || !dense_residual_grad_fits(M, N, gate_rows))
-    return TE_ERR_UNSUPPORTED;
+  if (K % 16 || N % 16 || M > kMaxDim || K > kMaxDim || N > kMaxDim) return TE_ERR_UNSUPPORTED;
   for (const void* p : {dout, x, kernel, saved_z, gate, static_cast<const void*>(dx), static_cast<const void*>(dkernel),
                         static_cast<const void*>(dresidual), static_cast<const void*>(workspace)})
     if (!aligned16(p)) return TE_ERR_UNSUPPORTED;

@@ -606,7 +606,7 @@ te_status te_dense_residual_fwd(const void* x, const void* kernel, te_dtype dtyp
  *       fp32, each or NULL (with a residual_scale of 1 dresidual is dout).
  *   workspace  te_dense_residual_bwd_workspace(M, K, N, gates, dtype) bytes (gates 1 without a gate),
  *       16-byte aligned; as elsewhere its end may be missing, where products would be split along K.
- * M = 0 zeroes dkernel, dbias and dgate.  (Tensors of M * N past 2^38 may be refused.) */
+ * M = 0 zeroes dkernel, dbias and dgate. */
 size_t te_dense_residual_bwd_workspace(int64_t M, int64_t K, int64_t N, int64_t gates, te_dtype dtype);
 te_status te_dense_residual_bwd(const void* dout, te_dtype residual_dtype, const void* x,
                                 const void* kernel, te_dtype dtype, const void* saved_z,

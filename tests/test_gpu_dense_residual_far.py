@@ -2,8 +2,8 @@
 dbias is dz itself in fp32 and dgate dout * act(z).
 
 gelu'(z) and silu'(z) are 1 above 16 and 128, and 0 below -16 and -128, to 2^-24; act(z) is z or 0.  The
-logistic of a far negative value is held above 2^-116 (its exponent is clamped at 80 log2 e), so that what stands
-for a zero is at most 6000 (|q|, at -16) * 2^-115 of dout."""
+logistic of a far negative value is held at 2^-115 or less, not at 0, and what multiplies it in the derivative
+is under 6000 (2 h sqrt(2 / pi) (1 + 3 * 0.044715 h^2) at 16): what stands for a zero is at most 6000 * 2^-115 of dout."""
 
 import math
 
