@@ -85,9 +85,10 @@ class GradBuckets:
         dist.all_reduce(self.vectors, op=dist.ReduceOp.SUM, group=group)
 
     def clip(self, max_norm, norm, epsilon=1e-6, stream=None):
-        """Scale every gradient by min(1, max_norm / (norm + epsilon)) in place, on the device; norm (one
-        float32) receives their global norm.  After allreduce each rank computes the same factor from
-        the same sums."""
+        """Scale every gradient of this block by min(1, max_norm / (norm + epsilon)) in place, on the device;
+        norm (one float32) receives their norm.  After allreduce each rank computes the same factor from
+        the same sums.  A model of several blocks takes one norm over all of them: te_clip_grad_norm over
+        the weights and vectors of all their buckets."""
         return te_clip_grad_norm(GradList([self.weights, self.vectors]), max_norm, norm, epsilon=epsilon,
                                  stream=stream)
 
