@@ -54,7 +54,9 @@ extern "C" te_status te_selftest_wait_timeout(int64_t limit_us, void* stream) {
 }
 
 extern "C" te_status te_selftest_cluster_abort(int64_t limit_us, int rank, int32_t* out, void* stream) {
-  if (limit_us <= 0 || limit_us > 1000000 || rank < -1 || rank >= te::kClusterTest || !out) return TE_ERR_INVALID_ARG;
+  if (limit_us <= 0 || limit_us > 1000000 || rank < -1 || rank >= te::kClusterTest || !out ||
+      reinterpret_cast<uintptr_t>(out) % 4)
+    return TE_ERR_INVALID_ARG;
   te::cluster_abort_kernel<<<te::kClusterTest, 64, 0, static_cast<cudaStream_t>(stream)>>>(
       te::device_status_ptr(), uint64_t(limit_us) * 1000u, rank, out);
   return cudaGetLastError() == cudaSuccess ? TE_OK : TE_ERR_CUDA;

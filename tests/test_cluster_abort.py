@@ -12,7 +12,7 @@ b = te.binding
 
 def test_arguments():
     f = te.lib().te_selftest_cluster_abort
-    for limit, rank, out in ((0, 0, 64), (-1, 0, 64), (1000001, 0, 64), (10, -2, 64), (10, 8, 64), (10, 0, None)):
+    for limit, rank, out in ((0, 0, 64), (-1, 0, 64), (1000001, 0, 64), (10, -2, 64), (10, 8, 64), (10, 0, None), (10, 0, 66)):
         assert f(limit, rank, out, None) == b.TE_ERR_INVALID_ARG
 
 
