@@ -193,7 +193,7 @@ def lib(build_if_stale: bool = True) -> ctypes.CDLL:
                                       "fp8_transformer_gb300.build.build()")
             _read_grads = ctypes.PyDLL(_build.TENSOR_LIB_PATH).te_read_grads
             _read_grads.restype = _i64
-            _read_grads.argtypes = [ctypes.py_object, ctypes.py_object, _GP, ctypes.POINTER(_i64)]
+            _read_grads.argtypes = [ctypes.py_object, ctypes.py_object, _i64, _GP, ctypes.POINTER(_i64)]
             h = ctypes.CDLL(_build.LIB_PATH)
             for name, (res, args) in _SIGS.items():
                 fn = getattr(h, name)
@@ -1079,13 +1079,15 @@ class GradList:
             raise ValueError("outs: one for each gradient")
         if _read_grads is None:
             lib()
-        table, dev = (_Grad * max(n, 1))(), _i64(-1)
-        i = _read_grads(self.grads, self.outs, table, dev)
+        table, dev = (_Grad * max(n, 1))(), _i64(-1)  # a call's own: another thread may use the list
+        i = _read_grads(self.grads, self.outs, n, table, dev)
         if i >= 0:
-            self._refuse(i)
+            self._refuse(i, n)
         return table, dev.value if n else None
 
-    def _refuse(self, i):
+    def _refuse(self, i, n):
+        if i == n:
+            raise ValueError("grads and outs: lists, which keep their length during a call")
         g, dev = self.grads[i], self.grads[0].get_device()
         _arg("grads", g, g.shape, _ACT_DTYPES, dev)
         if self.outs is not None:

@@ -28,14 +28,16 @@ bool read(PyObject* o, const at::TensorBase** t, int32_t* dtype) {
 
 }  // namespace
 
-// grads: a list of tensors; outs: a list as long, or None.  Fills table and *device (the first tensor's
+// grads: a list of n tensors; outs: another, or None.  Fills table (n entries) and *device (the first tensor's
 // index, -1 on the CPU, left alone by an empty list) and returns -1, or the place of the first entry that is not a
-// dense float32 / bfloat16 tensor on that device with an out of its shape and type.
-extern "C" int64_t te_read_grads(PyObject* grads, PyObject* outs, te_grad* table, int64_t* device) {
-  const Py_ssize_t n = PyList_GET_SIZE(grads);
-  Py_ssize_t i = 0;
+// dense float32 / bfloat16 tensor on that device with an out of its shape and type, or n where these are no such lists.
+extern "C" int64_t te_read_grads(PyObject* grads, PyObject* outs, int64_t n, te_grad* table, int64_t* device) {
+  auto holds = [n](PyObject* o) { return PyList_Check(o) && PyList_GET_SIZE(o) == n; };
+  int64_t i = 0;
   try {
+    if (n == 0 && !(holds(grads) && (outs == Py_None || holds(outs)))) return n;
     for (; i < n; ++i) {
+      if (!holds(grads) || !(outs == Py_None || holds(outs))) return n;  // (a type's own check may run Python)
       const at::TensorBase *g = nullptr, *o = nullptr;
       int32_t dtype = 0, out_dtype = 0;
       if (!read(PyList_GET_ITEM(grads, i), &g, &dtype)) return i;

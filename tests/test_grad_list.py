@@ -97,6 +97,11 @@ def test_lists():
     plan.outs.pop()
     with pytest.raises(ValueError):
         plan._table()
+    for grads, outs in (((a, c), None), ([a, c], (a, c)), ((), None)):
+        plan = te.GradList([a, c])
+        plan.grads, plan.outs = grads, outs
+        with pytest.raises(ValueError):
+            plan._table()
     for bad in ([a, None], [a, 3.0], [a, torch.ones(3, dtype=torch.float64)], [torch.ones(4).to_sparse()],
                 [a, torch.ones(3, device="meta")]):
         with pytest.raises((ValueError, AttributeError)):
