@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kThreads, 2) dense_few_kernel(const __grid_con
   if (row < rows) in = p.end.load(row0 + row, col0 + c);
   __syncwarp();
   if (ranks > 1) cluster_sync();
-  if (!(ranks > 1 ? cluster_aborted(&abort_flag, ranks) : abort_flag != 0)) {
+  {
+    ClusterFlags<kMaxCluster> flags(&abort_flag, ranks, rank);
     uint32_t sums[kMaxCluster];
 #pragma unroll
     for (int r = 0; r < kMaxCluster; ++r)
@@ -329,6 +330,7 @@ __global__ void __launch_bounds__(kThreads, 2) dense_few_kernel(const __grid_con
       for (int r = 1; r < kMaxCluster; ++r) {
         v[0] += u[r].x; v[1] += u[r].y; v[2] += u[r].z; v[3] += u[r].w;
       }
+      if (flags.raised()) break;
       const End::In now = in;
       const int at = row0 + row;
       row += step;

@@ -37,7 +37,7 @@ __global__ void __cluster_dims__(kClusterTest, 1, 1) cluster_abort_kernel(int* s
   if (threadIdx.x == 0 && rank == waits) wait_bounded(smem_u32(&bar), 0, &abort_flag, status, limit_ns, true);
   __syncthreads();
   cluster_sync();
-  const bool stop = cluster_aborted(&abort_flag, kClusterTest);
+  const bool stop = ClusterFlags<kClusterTest>(&abort_flag, kClusterTest, rank).raised();
   const bool all = __syncthreads_and(!stop) != 0, any = __syncthreads_or(!stop) != 0;
   if (threadIdx.x == 0) out[rank] = all ? 1 : any ? 2 : 0;
   cluster_sync();

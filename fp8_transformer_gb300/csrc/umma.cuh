@@ -131,18 +131,25 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Whether a CTA of the cluster has raised its abort flag, which lies at the same place in each; by whole warps,
-// between two barriers of the cluster (the first so that the flags have settled, the second so that they last).
-__device__ __forceinline__ bool cluster_aborted(const volatile int* flag, int ranks) {
-  const uint32_t lane = threadIdx.x & 31;
-  int f = 0;
-  if (lane < uint32_t(ranks))
-    asm volatile("ld.shared::cluster.u32 %0, [%1];"
-                 : "=r"(f)
-                 : "r"(map_to_rank(smem_u32(const_cast<const int*>(flag)), lane))
-                 : "memory");
-  return __any_sync(0xffffffffu, f != 0);
-}
+// The abort flags of a cluster's CTAs, which lie at the same place in each; between two barriers of the cluster (the
+// first so that the flags have settled, the second so that they last).  Each thread asks for all of them at once, and
+// waits for them where it looks.
+template <int MAX>
+struct ClusterFlags {
+  int f[MAX];
+  __device__ __forceinline__ ClusterFlags(const volatile int* flag, int ranks, int rank) {
+    const uint32_t at = smem_u32(const_cast<const int*>(flag));
+#pragma unroll
+    for (int r = 0; r < MAX; ++r)
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(f[r]) : "r"(map_to_rank(at, uint32_t(r < ranks ? r : rank))));
+  }
+  __device__ __forceinline__ bool raised() const {
+    int any = 0;
+#pragma unroll
+    for (int r = 0; r < MAX; ++r) any |= f[r];
+    return any != 0;
+  }
+};
 
 // 32 lanes x 32 consecutive fp32 columns: thread t of the warp receives its TMEM lane's row.
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
